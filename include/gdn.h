@@ -47,6 +47,12 @@
  *                            checkpoint plus buffered rows, periodic flush.
  *   gdn_accept_prefix        greedy accepted lengths from token ids, on the
  *                            device.
+ *   gdn_rope_append          attention layers: rotary positions of a step's
+ *                            queries and keys, keys and values written to the
+ *                            pages of a key/value cache.
+ *   gdn_paged_attn           attention of the step's rows over that cache, all
+ *                            of it or a sliding window with first tokens that
+ *                            stay visible.
  *   gdn_selftest_wait_timeout  runs the bounded wait to its expiry (diagnostic).
  *
  * Device-side argument errors (a slot id outside [0, pool_slots), a_r outside
@@ -121,6 +127,8 @@ typedef enum gdn_algo {
                                    ends.  Treat every later result on the stream as suspect until
                                    the CUDA context has been rebuilt. */
 #define GDN_DEVERR_REPLAY  16   /* replay buffer: len_in[slot] < 0, or buffered plus new rows > capacity */
+#define GDN_DEVERR_KV_LEN  32   /* cache: kv_len[r] < 0, or kv_len[r] + T_r > max_pages * page_size */
+#define GDN_DEVERR_PAGE    64   /* cache: a page id that the call needs is outside [0, n_pages) */
 
 /* Variant bits of gdn_problem.flags (the same in every problem of a layer batch). */
 #define GDN_FLAG_O_BF16    1    /* o is bfloat16 [N_tok][heads][dv], round to nearest even of the
@@ -302,6 +310,99 @@ typedef struct gdn_prev_step {
 
 GDN_API gdn_status gdn_commit_verify(const gdn_problem *p, const gdn_prev_step *prev, void *o,
                                      float *w, cudaStream_t stream);
+
+/* Attention layers.  The other layers of a hybrid model keep keys and values
+ * in a paged cache.  A step has the same requests and rows as the GDN calls
+ * (uniform max_T, or cu_seqlens); kv_len[r] tokens of request r are in the
+ * cache before it, and its row t (0 <= t < T_r) is the token at place
+ * c = kv_len[r] + t.  Place c of request r lies in page
+ * page_table[r][c / page_size], row c % page_size.  A rejected draft is rolled
+ * back by leaving kv_len where it was: kv_len[r] += accepted[r] after a step,
+ * and the next step overwrites the rejected rows.
+ *
+ * Layout: k_pages and v_pages are [n_pages][kv_heads][page_size][head_dim],
+ * consecutive pages page_stride elements apart (>= kv_heads * page_size *
+ * head_dim, so that both may lie in one allocation).  Query head h reads key
+ * head h / (q_heads / kv_heads). */
+#define GDN_ATTN_MAX_T 65536    /* rows per request of the two attention calls */
+
+typedef struct gdn_attn {
+    int32_t batch;               /* B >= 0 requests (B = 0: calls return GDN_OK, no launch) */
+    int32_t q_heads;             /* a multiple of kv_heads */
+    int32_t kv_heads;            /* >= 1 */
+    int32_t head_dim;            /* 32, 64, 128 or 256 */
+    int32_t max_T;               /* uniform rows per request (cu_seqlens NULL) or the ragged maximum, 0..GDN_ATTN_MAX_T */
+    int32_t dtype;               /* gdn_dtype of q, k, v, the pages and o */
+    int32_t page_size;           /* 16, 32, 64, 128 or 256 */
+    int32_t max_pages;           /* columns of page_table; max_pages * page_size <= 2^31 - 1 */
+    int32_t window;              /* 0: every place up to the row's own; W > 0: the last W of them, itself among them */
+    int32_t sinks;               /* first places that stay visible under a window (0 without one) */
+    float scale;                 /* factor on q.k, finite (1 / sqrt(head_dim) in most models) */
+    int32_t reserved;            /* must be 0 */
+    const int32_t *cu_seqlens;   /* device [batch+1] token-row offsets, or NULL (uniform) */
+    int64_t n_tok;               /* rows of q/k/v/o: REQUIRED for ragged input, ignored for uniform */
+    void *k_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
+    void *v_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
+    int64_t n_pages;             /* 1 .. 2^31 - 1 */
+    int64_t page_stride;         /* elements from a page to the next; a multiple of 16 bytes */
+    const int32_t *page_table;   /* device [batch][max_pages]; entries no row needs are not read */
+    const int32_t *kv_len;       /* device [batch]: tokens in the cache before this step */
+    int32_t *dev_err;            /* device int32 error word (GDN_DEVERR_* bits), or NULL */
+} gdn_attn;
+
+/* Rotary positions.  The first rot_dim elements of a head are rotated, the
+ * rest pass unchanged.  Pair i of rot_dim / 2 is (x, y) = elements (i, i +
+ * rot_dim / 2), or (2i, 2i + 1) when interleaved; with angle a = p *
+ * inv_freq[i], p = positions[row] (or the row's place c when NULL),
+ *     x' = mscale (x cos a - y sin a),   y' = mscale (x sin a + y cos a).
+ * Scalings for long contexts are choices of inv_freq and mscale. */
+typedef struct gdn_rope {
+    int32_t rot_dim;             /* a multiple of 16, 16 .. head_dim */
+    int32_t interleaved;         /* 0: halves, 1: neighbours */
+    float mscale;                /* factor on cosine and sine, finite (1 without scaling) */
+    int32_t reserved;            /* must be 0 */
+    const float *inv_freq;       /* device float32 [rot_dim / 2]: radians per position */
+    const int32_t *positions;    /* device int32 [N_tok], or NULL: the row's place in the cache */
+} gdn_rope;
+
+/* One step's rows: q_out <- rotated q, and the rotated k and the v of each row
+ * to its place in the pages.
+ *   q      device [N_tok][q_heads][head_dim], q_stride elements from a row to the next
+ *   k, v   device [N_tok][kv_heads][head_dim], k_stride and v_stride elements apart
+ *          (strides >= the row, multiples of 16 bytes: slices of one projection's output)
+ *   q_out  device [N_tok][q_heads][head_dim], contiguous; overlaps nothing else of the call
+ * All 16-byte aligned.  A request with a bad kv_len or bad row offsets is skipped; a row
+ * whose page id is outside [0, n_pages) gets its q_out and sets GDN_DEVERR_PAGE.  No two rows
+ * of a call may share a place (a shared page that one of them writes is a precondition
+ * violation). */
+GDN_API gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, const void *q,
+                                   int64_t q_stride, const void *k, int64_t k_stride,
+                                   const void *v, int64_t v_stride, void *q_out,
+                                   cudaStream_t stream);
+
+/* Attention of the step's rows over the cache, which holds the step's own
+ * keys and values already.  Row t of request r at place c = kv_len[r] + t sees
+ * the places j <= c with (window = 0, or j > c - window, or j < sinks):
+ *     o = sum_j e_j v_j / sum_j e_j,   e_j = exp(scale q.k_j - m),   m = max_j scale q.k_j
+ *   q    device [N_tok][q_heads][head_dim], q_stride elements apart, 16-byte aligned
+ *   o    device [N_tok][q_heads][head_dim], contiguous, dtype, 16-byte aligned
+ *   lse  device float32 [N_tok][q_heads]: m + log(sum_j e_j), or NULL
+ *   workspace  device, 16-byte aligned, at least gdn_paged_attn_workspace(p)
+ *        bytes, zero when it is first used; one per stream.  Calls leave
+ *        nothing in it that a later call reads.
+ * o, lse and the workspace overlap nothing else of the call.  Sums and the
+ * softmax's statistics are 32-bit.  Keys and values at places that no row of a
+ * request sees are never used, whatever they hold.  A request with a
+ * bad kv_len or bad row offsets is skipped (nothing is written for it); a page
+ * whose id is outside [0, n_pages) sets GDN_DEVERR_PAGE and reads as zeros. */
+GDN_API gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, void *o,
+                                  float *lse, void *workspace, int64_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/* Bytes of workspace that gdn_paged_attn needs for p (host only, no CUDA
+ * call; depends on sizes and dtype, not on lengths), or -1 when p's sizes fail
+ * validation. */
+GDN_API int64_t gdn_paged_attn_workspace(const gdn_attn *p);
 
 /* Waits for `stream`, copies *p->dev_err to *host_code (0 when dev_err is NULL).
  * Returns GDN_ERR_DEVICE_ARG when the word is non-zero, GDN_OK when it is zero. */

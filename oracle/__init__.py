@@ -17,11 +17,12 @@ The greedy accept-length rule lives in `accept.py` (pure Python loops); the
 ReplaySSM buffer (checkpoint plus buffered rows, periodic flush) in `replay.py`,
 which runs this recurrence over the replayed rows; the step that commits the
 previous step's accepted prefix and then verifies the next drafts in
-`lagged.py`.
+`lagged.py`; the attention layers' rotary positions and paged-cache attention
+in `attention.py`.
 
 Parity unpinned: none.  Every function here is pinned by `tests/test_oracle_pins.py`,
-`tests/test_accept_oracle.py`, `tests/test_replay_oracle.py` and
-`tests/test_lagged_oracle.py`.
+`tests/test_accept_oracle.py`, `tests/test_replay_oracle.py`,
+`tests/test_lagged_oracle.py` and `tests/test_attn_oracle.py`.
 """
 from __future__ import annotations
 
@@ -36,6 +37,7 @@ import numpy as np
 
 from .accept import accept_prefix  # noqa: F401  (greedy accept length)
 from .replay import replay_commit, replay_verify  # noqa: F401  (ReplaySSM buffer)
+from .attention import cached_rows, paged_attention, rope, write_rows  # noqa: F401  (attention layers)
 from .lagged import commit_verify  # noqa: F401  (commit the previous step, verify the next)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -24,7 +24,9 @@ GDN_FLAG_O_BF16, GDN_FLAG_LOG_GATE = 1, 2
 GDN_ALGO_AUTO, GDN_ALGO_RECURRENT, GDN_ALGO_CHUNK, GDN_ALGO_CHUNK_TC = 0, 1, 2, 3
 GDN_DEVERR_SLOT, GDN_DEVERR_ACCEPTED, GDN_DEVERR_SEQLEN = 1, 2, 4
 GDN_DEVERR_TIMEOUT, GDN_DEVERR_REPLAY = 8, 16
+GDN_DEVERR_KV_LEN, GDN_DEVERR_PAGE = 32, 64
 GDN_MAX_T = 1024
+GDN_ATTN_MAX_T = 65536
 
 # Every symbol include/gdn.h declares.
 EXPORTED = (
@@ -33,6 +35,7 @@ EXPORTED = (
     "gdn_accept_prefix", "gdn_replay_verify", "gdn_replay_commit", "gdn_commit_verify",
     "gdn_read_device_error", "gdn_selftest_wait_timeout",
     "gdn_select_algo", "gdn_status_string", "gdn_last_error_string", "gdn_version",
+    "gdn_rope_append", "gdn_paged_attn", "gdn_paged_attn_workspace",
 )
 
 
@@ -79,6 +82,31 @@ class gdn_prev_step(ctypes.Structure):
     ]
 
 
+class gdn_attn(ctypes.Structure):
+    """Mirror of the C struct gdn_attn (include/gdn.h), field for field."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("max_T", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("n_tok", ctypes.c_int64),
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p), ("dev_err", ctypes.c_void_p),
+    ]
+
+
+class gdn_rope(ctypes.Structure):
+    """Mirror of the C struct gdn_rope (include/gdn.h), field for field."""
+
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
 _lib_handle: Optional[ctypes.CDLL] = None
 
 
@@ -104,6 +132,11 @@ def lib() -> ctypes.CDLL:
         h.gdn_replay_verify.argtypes = [P, R, S, S]
         h.gdn_replay_commit.argtypes = [P, R, S, S]
         h.gdn_commit_verify.argtypes = [P, ctypes.POINTER(gdn_prev_step), S, S, S]
+        I64, A = ctypes.c_int64, ctypes.POINTER(gdn_attn)
+        h.gdn_rope_append.argtypes = [A, ctypes.POINTER(gdn_rope), S, I64, S, I64, S, I64, S, S]
+        h.gdn_paged_attn.argtypes = [A, S, I64, S, S, S, I64, S]
+        h.gdn_paged_attn_workspace.argtypes = [A]
+        h.gdn_paged_attn_workspace.restype = I64
         h.gdn_read_device_error.argtypes = [P, S, ctypes.POINTER(ctypes.c_int32)]
         h.gdn_selftest_wait_timeout.argtypes = [S, S]
         h.gdn_select_algo.argtypes = [P]
@@ -112,7 +145,7 @@ def lib() -> ctypes.CDLL:
                      "gdn_verify_layers", "gdn_commit_layers", "gdn_verify_commit_fused_layers",
                      "gdn_accept_prefix", "gdn_replay_verify", "gdn_replay_commit",
                      "gdn_commit_verify", "gdn_read_device_error", "gdn_selftest_wait_timeout",
-                     "gdn_select_algo"):
+                     "gdn_select_algo", "gdn_rope_append", "gdn_paged_attn"):
             getattr(h, name).restype = ctypes.c_int
         for name in ("gdn_status_string", "gdn_last_error_string", "gdn_version"):
             getattr(h, name).restype = ctypes.c_char_p
@@ -405,3 +438,154 @@ def gdn_commit_verify(prob: Problem, prev: Optional[PrevStep], o: torch.Tensor, 
     _check(w, "w", (torch.float32,), None)
     _raise(lib().gdn_commit_verify(prob.ref, None if prev is None else prev.ref, _ptr(o), _ptr(w),
                                    _stream(stream)), "gdn_commit_verify")
+
+
+class Attn:
+    """A gdn_attn (the requests, their paged cache and the mask of one attention layer)
+    plus references to the tensors it points into."""
+
+    def __init__(self, c: gdn_attn, refs: tuple, dtype, device):
+        self.c = c
+        self.refs = refs
+        self.dtype, self.device = dtype, device
+        self.ref = ctypes.byref(c)
+
+
+def make_attn(*, q_heads: int, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, kv_len: torch.Tensor, max_T: int,
+              cu_seqlens: Optional[torch.Tensor] = None, n_tok: Optional[int] = None,
+              window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+              dev_err: Optional[torch.Tensor] = None) -> Attn:
+    """Builds the C description of one attention layer's step (include/gdn.h).
+
+    k_pages, v_pages: [n_pages, kv_heads, page_size, head_dim] bf16 or fp32, each page
+    contiguous, pages any equal distance apart; page_table: [B, max_pages] int32;
+    kv_len: [B] int32, the tokens cached before the step; cu_seqlens: [B+1] int32 with
+    n_tok rows, or None (uniform length max_T).  window: 0, or the last places a row
+    sees; sinks: first places that stay visible under it.  scale: 1 / sqrt(head_dim)
+    when None."""
+    dev = k_pages.device
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [n_pages, kv_heads, page_size, head_dim]")
+    if k_pages.dtype not in (torch.bfloat16, torch.float32) or v_pages.dtype != k_pages.dtype:
+        raise TypeError("k_pages and v_pages must both be bf16 or both fp32")
+    n_pages, kv_heads, page, hd = k_pages.shape
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, expected {dev}")
+        if t.stride()[1:] != (page * hd, hd, 1):
+            raise ValueError(f"a page of {n} must be contiguous")
+    if n_pages > 1 and v_pages.stride(0) != k_pages.stride(0):
+        raise ValueError("k_pages and v_pages must have the same page stride")
+    for t, n in ((page_table, "page_table"), (kv_len, "kv_len"), (cu_seqlens, "cu_seqlens"),
+                 (dev_err, "dev_err")):
+        _check(t, n, (torch.int32,), dev)
+    batch = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError("page_table must be [batch, max_pages]")
+    if cu_seqlens is not None and (cu_seqlens.numel() != batch + 1 or n_tok is None):
+        raise ValueError("a ragged step needs cu_seqlens [batch + 1] and n_tok")
+    c = gdn_attn()
+    c.batch, c.q_heads, c.kv_heads, c.head_dim = batch, int(q_heads), kv_heads, hd
+    c.max_T = int(max_T)
+    c.dtype = GDN_BF16 if k_pages.dtype == torch.bfloat16 else GDN_FP32
+    c.page_size, c.max_pages = page, page_table.shape[1]
+    c.window, c.sinks = int(window), int(sinks)
+    c.scale = hd ** -0.5 if scale is None else float(scale)
+    c.cu_seqlens = _ptr(cu_seqlens)
+    c.n_tok = int(n_tok) if cu_seqlens is not None else batch * int(max_T)
+    c.k_pages, c.v_pages = _ptr(k_pages), _ptr(v_pages)
+    c.n_pages = n_pages
+    c.page_stride = k_pages.stride(0) if n_pages > 1 else kv_heads * page * hd
+    c.page_table, c.kv_len, c.dev_err = _ptr(page_table), _ptr(kv_len), _ptr(dev_err)
+    return Attn(c, (k_pages, v_pages, page_table, kv_len, cu_seqlens, dev_err), k_pages.dtype, dev)
+
+
+class Rope:
+    """A gdn_rope plus references to the tensors it points into."""
+
+    def __init__(self, c: gdn_rope, refs: tuple):
+        self.c = c
+        self.refs = refs
+        self.ref = ctypes.byref(c)
+
+
+def make_rope(*, inv_freq: torch.Tensor, interleaved: bool = False, mscale: float = 1.0,
+              positions: Optional[torch.Tensor] = None) -> Rope:
+    """inv_freq: [rot_dim / 2] fp32, radians per position (staging.rope_frequencies);
+    positions: [N_tok] int32, or None (a row's position is its place in the cache)."""
+    _check(inv_freq, "inv_freq", (torch.float32,), None)
+    _check(positions, "positions", (torch.int32,), inv_freq.device)
+    c = gdn_rope()
+    c.rot_dim, c.interleaved = 2 * inv_freq.numel(), int(bool(interleaved))
+    c.mscale, c.reserved = float(mscale), 0
+    c.inv_freq, c.positions = _ptr(inv_freq), _ptr(positions)
+    return Rope(c, (inv_freq, positions))
+
+
+def _check_rows(t: torch.Tensor, name: str, attn: Attn, heads: int) -> int:
+    """Checks a [N_tok, heads, head_dim] tensor whose rows are contiguous; its row stride."""
+    c = attn.c
+    if t.dtype is not attn.dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {attn.dtype}")
+    if t.device != attn.device:
+        raise ValueError(f"{name} is on {t.device}, expected {attn.device}")
+    if tuple(t.shape) != (c.n_tok, heads, c.head_dim):
+        raise ValueError(f"{name} must be {(c.n_tok, heads, c.head_dim)}, is {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != c.head_dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if c.n_tok > 1 else heads * c.head_dim
+
+
+def gdn_rope_append(attn: Attn, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    q_out: torch.Tensor, stream=None) -> None:
+    """q_out <- rotated q; the rotated k and the v of each row to the pages.
+    q, q_out: [N_tok, q_heads, head_dim]; k, v: [N_tok, kv_heads, head_dim]; the rows of
+    q, k and v may be slices of wider ones, q_out is contiguous."""
+    c = attn.c
+    sq = _check_rows(q, "q", attn, c.q_heads)
+    sk = _check_rows(k, "k", attn, c.kv_heads)
+    sv = _check_rows(v, "v", attn, c.kv_heads)
+    if _check_rows(q_out, "q_out", attn, c.q_heads) != c.q_heads * c.head_dim:
+        raise ValueError("q_out must be contiguous")
+    if rope.refs[0].device != attn.device:
+        raise ValueError(f"inv_freq is on {rope.refs[0].device}, expected {attn.device}")
+    if rope.refs[1] is not None and rope.refs[1].numel() != c.n_tok:
+        raise ValueError("positions must be [N_tok]")
+    _raise(lib().gdn_rope_append(attn.ref, rope.ref, q.data_ptr(), sq, k.data_ptr(), sk,
+                                 v.data_ptr(), sv, q_out.data_ptr(), _stream(stream)),
+           "gdn_rope_append")
+
+
+def gdn_paged_attn_workspace(attn: Attn) -> int:
+    """Bytes of workspace that gdn_paged_attn needs."""
+    n = int(lib().gdn_paged_attn_workspace(attn.ref))
+    if n < 0:
+        raise ValueError("gdn_paged_attn_workspace: the sizes are not valid")
+    return n
+
+
+def paged_attn_workspace(attn: Attn) -> torch.Tensor:
+    """A workspace for gdn_paged_attn, zero-filled; one per stream, kept from call to call."""
+    return torch.zeros(gdn_paged_attn_workspace(attn), dtype=torch.uint8, device=attn.device)
+
+
+def gdn_paged_attn(attn: Attn, q: torch.Tensor, o: torch.Tensor, *, workspace: torch.Tensor,
+                   lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """o <- attention of the step's rows over the cache; lse (fp32 [N_tok, q_heads], or None)
+    <- the logarithm of each row's sum.  q, o: [N_tok, q_heads, head_dim]; q's rows may be
+    slices of wider ones, o is contiguous."""
+    c = attn.c
+    sq = _check_rows(q, "q", attn, c.q_heads)
+    if _check_rows(o, "o", attn, c.q_heads) != c.q_heads * c.head_dim:
+        raise ValueError("o must be contiguous")
+    if lse is not None:
+        _check(lse, "lse", (torch.float32,), attn.device)
+        if lse.numel() != c.n_tok * c.q_heads:
+            raise ValueError("lse must be [N_tok, q_heads]")
+    if workspace.device != attn.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {attn.device}")
+    _raise(lib().gdn_paged_attn(attn.ref, q.data_ptr(), sq, o.data_ptr(), _ptr(lse),
+                                workspace.data_ptr(), workspace.nbytes, _stream(stream)),
+           "gdn_paged_attn")

@@ -1,6 +1,7 @@
 // C ABI of libgdn.so: host-side validation, kernel selection and launch.
 // Every check runs before any CUDA call, so a rejected call launches nothing
 // (and the checks work on a machine without a GPU).
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 
@@ -364,9 +365,191 @@ gdn_status run_commit_verify(const gdn_problem *p, const gdn_prev_step *prev, vo
     return GDN_OK;
 }
 
+// ------------------------------------------------------------ attention layers
+
+int64_t attn_rows(const gdn_attn *p) {
+    return p->cu_seqlens ? p->n_tok : (int64_t)p->batch * p->max_T;
+}
+
+int64_t attn_esz(const gdn_attn *p) { return p->dtype == GDN_BF16 ? 2 : 4; }
+
+// The checks on sizes (no pointers).
+gdn_status attn_sizes(const gdn_attn *p) {
+    if (p->reserved != 0 || p->batch < 0 || p->kv_heads < 1 || p->q_heads < 1 ||
+        p->q_heads % p->kv_heads != 0 || p->q_heads > 65536 || p->max_T < 0 ||
+        p->max_T > GDN_ATTN_MAX_T || p->window < 0 || p->sinks < 0 ||
+        (p->sinks > 0 && p->window == 0) || !std::isfinite(p->scale) || !(p->scale > 0.f))
+        return GDN_ERR_BAD_DIM;
+    if (p->dtype != GDN_FP32 && p->dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
+    if (p->head_dim != 32 && p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+        return GDN_ERR_UNSUPPORTED;
+    if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128 &&
+        p->page_size != 256)
+        return GDN_ERR_UNSUPPORTED;
+    // Units and rows are counted in 32-bit ints on the device.
+    const int64_t rows = (int64_t)p->max_T * (p->q_heads / p->kv_heads);
+    if (rows > (1ll << 30) || (int64_t)p->batch * p->q_heads > 0x7fffffffLL ||
+        p->batch * (rows / 16 + 1) > 0x7fffffffLL)
+        return GDN_ERR_BAD_DIM;
+    return GDN_OK;
+}
+
+struct AttnRanges {
+    Range k, v, table, len, cu, err;
+};
+
+AttnRanges attn_ranges(const gdn_attn *p) {
+    const int64_t page = (int64_t)p->kv_heads * p->page_size * p->head_dim;
+    const int64_t bytes = ((p->n_pages - 1) * p->page_stride + page) * attn_esz(p);
+    AttnRanges r;
+    r.k = range(p->k_pages, bytes);
+    r.v = range(p->v_pages, bytes);
+    r.table = range(p->page_table, (int64_t)p->batch * p->max_pages * 4);
+    r.len = range(p->kv_len, (int64_t)p->batch * 4);
+    r.cu = range(p->cu_seqlens, p->cu_seqlens ? ((int64_t)p->batch + 1) * 4 : 0);
+    r.err = range(p->dev_err, p->dev_err ? 4 : 0);
+    return r;
+}
+
+// Whether rows of `row` elements, `stride` apart, are well formed; the bytes they span.
+bool stride_ok(const gdn_attn *p, int64_t stride, int64_t row) {
+    return stride >= row && stride <= (1ll << 40) && stride * attn_esz(p) % 16 == 0;
+}
+Range rows_range(const gdn_attn *p, const void *ptr, int64_t stride, int64_t row) {
+    const int64_t n = attn_rows(p);
+    return range(ptr, n > 0 ? ((n - 1) * stride + row) * attn_esz(p) : 0);
+}
+
+// Checks shared by the two attention calls.  *empty: nothing to launch.
+gdn_status attn_validate(const gdn_attn *p, bool *empty) {
+    if (!p) return GDN_ERR_NULL_PTR;
+    const gdn_status st = attn_sizes(p);
+    if (st != GDN_OK) return st;
+    if (p->cu_seqlens && p->n_tok < 0) return GDN_ERR_BAD_DIM;
+    if (attn_rows(p) > 0x7fffffffLL) return GDN_ERR_BAD_DIM;
+    *empty = p->batch == 0 || attn_rows(p) == 0;
+    if (*empty) return GDN_OK;
+    if (p->max_pages < 1 || (int64_t)p->max_pages * p->page_size > 0x7fffffffLL || p->n_pages < 1 ||
+        p->n_pages > 0x7fffffffLL)
+        return GDN_ERR_BAD_DIM;
+    if (p->page_stride < (int64_t)p->kv_heads * p->page_size * p->head_dim ||
+        p->page_stride > (1ll << 40) || p->page_stride * attn_esz(p) % 16 != 0)
+        return GDN_ERR_BAD_DIM;
+    if (!p->k_pages || !p->v_pages || !p->page_table || !p->kv_len) return GDN_ERR_NULL_PTR;
+    if (!aligned16(p->k_pages) || !aligned16(p->v_pages) || !aligned4(p->page_table) ||
+        !aligned4(p->kv_len) || !aligned4(p->cu_seqlens) || !aligned4(p->dev_err))
+        return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+gdn::AttnArgs attn_args(const gdn_attn *p, const void *q, int64_t q_stride, void *o) {
+    gdn::AttnArgs a = {};
+    a.B = p->batch;
+    a.Hq = p->q_heads;
+    a.Hkv = p->kv_heads;
+    a.G = p->q_heads / p->kv_heads;
+    a.hd = p->head_dim;
+    a.max_T = p->max_T;
+    while ((1 << a.page_shift) < p->page_size) ++a.page_shift;
+    a.max_pages = p->max_pages;
+    a.window = p->window;
+    a.sinks = p->sinks;
+    a.scale_log2 = (float)((double)p->scale * 1.4426950408889634074);
+    a.n_tok = attn_rows(p);
+    a.cu_seqlens = p->cu_seqlens;
+    a.k = p->k_pages;
+    a.v = p->v_pages;
+    a.n_pages = p->n_pages;
+    a.page_stride = p->page_stride;
+    a.page_table = p->page_table;
+    a.kv_len = p->kv_len;
+    a.dev_err = p->dev_err;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.o = o;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, const void *q,
+                           int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, void *q_out, cudaStream_t stream) {
+    if (!rope) return GDN_ERR_NULL_PTR;
+    bool empty = false;
+    const gdn_status st = attn_validate(p, &empty);
+    if (st != GDN_OK) return st;
+    if (rope->reserved != 0 || rope->rot_dim < 16 || rope->rot_dim > p->head_dim ||
+        rope->rot_dim % 16 != 0 || (rope->interleaved != 0 && rope->interleaved != 1) ||
+        !std::isfinite(rope->mscale))
+        return GDN_ERR_BAD_DIM;
+    if (empty) return GDN_OK;
+    const int64_t qrow = (int64_t)p->q_heads * p->head_dim, krow = (int64_t)p->kv_heads * p->head_dim;
+    if (!stride_ok(p, q_stride, qrow) || !stride_ok(p, k_stride, krow) ||
+        !stride_ok(p, v_stride, krow))
+        return GDN_ERR_BAD_DIM;
+    if (!q || !k || !v || !q_out || !rope->inv_freq) return GDN_ERR_NULL_PTR;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+        !aligned4(rope->inv_freq) || !aligned4(rope->positions))
+        return GDN_ERR_ALIGN;
+    // Written: q_out and the pages.  The pages are checked against each other only by their
+    // first byte: k and v pages may interleave in one allocation.
+    const AttnRanges r = attn_ranges(p);
+    const Range rq = rows_range(p, q, q_stride, qrow), rk = rows_range(p, k, k_stride, krow),
+                rv = rows_range(p, v, v_stride, krow), ro = rows_range(p, q_out, qrow, qrow);
+    const Range rf = range(rope->inv_freq, (int64_t)rope->rot_dim * 2);
+    const Range rp = range(rope->positions, rope->positions ? attn_rows(p) * 4 : 0);
+    const Range ins[] = {rq, rk, rv, rf, rp, r.table, r.len, r.cu, r.err};
+    for (const Range &x : ins)
+        if (overlap(ro, x) || overlap(r.k, x) || overlap(r.v, x)) return GDN_ERR_ALIAS;
+    if (overlap(ro, r.k) || overlap(ro, r.v) || p->k_pages == p->v_pages) return GDN_ERR_ALIAS;
+    const cudaError_t e =
+        gdn::launch_rope(attn_args(p, q, q_stride, q_out), *rope, p->dtype == GDN_BF16, k, k_stride,
+                         v, v_stride, p->k_pages, p->v_pages, stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, "kernel launch");
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+int64_t gdn_paged_attn_workspace(const gdn_attn *p) {
+    if (!p || attn_sizes(p) != GDN_OK) return -1;
+    return gdn::attn_workspace(p->dtype == GDN_BF16, p->head_dim);
+}
+
+gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, void *o, float *lse,
+                          void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+    bool empty = false;
+    const gdn_status st = attn_validate(p, &empty);
+    if (st != GDN_OK || empty) return st;
+    const int64_t need = gdn_paged_attn_workspace(p);
+    const int64_t qrow = (int64_t)p->q_heads * p->head_dim;
+    if (!stride_ok(p, q_stride, qrow) || workspace_bytes < need) return GDN_ERR_BAD_DIM;
+    if (!q || !o || !workspace) return GDN_ERR_NULL_PTR;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(lse))
+        return GDN_ERR_ALIGN;
+    const AttnRanges r = attn_ranges(p);
+    const Range rq = rows_range(p, q, q_stride, qrow), ro = rows_range(p, o, qrow, qrow);
+    const Range rl = range(lse, lse ? attn_rows(p) * p->q_heads * 4 : 0);
+    const Range rw = range(workspace, need);
+    const Range ins[] = {rq, r.k, r.v, r.table, r.len, r.cu, r.err};
+    for (const Range &x : ins)
+        if (overlap(ro, x) || overlap(rl, x) || overlap(rw, x)) return GDN_ERR_ALIAS;
+    if (overlap(ro, rl) || overlap(ro, rw) || overlap(rl, rw)) return GDN_ERR_ALIAS;
+    gdn::AttnArgs a = attn_args(p, q, q_stride, o);
+    a.lse = lse;
+    a.desc = static_cast<int4 *>(workspace);
+    a.part = reinterpret_cast<float *>(a.desc + 2 * gdn::kAttnWorkers);
+    const cudaError_t e = gdn::launch_attn(a, p->dtype == GDN_BF16, stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, "kernel launch");
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
 
 gdn_status gdn_commit_verify(const gdn_problem *p, const gdn_prev_step *prev, void *o, float *w,
                              cudaStream_t stream) {

@@ -1,0 +1,269 @@
+// Attention of a step's rows over a paged key/value cache: the CUDA-core
+// kernel, and the kernel that joins partial results.
+//
+// The softmax runs in one pass over the keys with a running maximum m and
+// total l per row, in powers of two: with x_j = scale log2(e) q.k_j,
+//     m' = max(m, max_j x_j),  l' = l 2^(m - m') + sum_j 2^(x_j - m'),
+//     o' = o 2^(m - m') + sum_j 2^(x_j - m') v_j,
+// and o / l at the end.  m = -inf (no key seen yet) is replaced by 0 in the
+// exponents, so a row whose mask hides a whole tile, or a whole worker's
+// range, adds nothing instead of NaN.
+#include <cstdint>
+
+#include "gdn_attn.cuh"
+#include "gdn_launch.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kRows = 16;   // query rows of a unit
+constexpr int kKeys = 32;   // places of a key tile
+constexpr int kThreads = 128;
+constexpr int kMinTiles = 2;
+
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <int HD>
+struct Smem {
+    static constexpr int LD = HD + 4;  // rows 16-byte aligned, 4 banks apart
+    float q[kRows][LD];
+    float k[kKeys][LD];
+    float v[kKeys][LD];
+    float p[kRows][kKeys + 1];
+    PlanScratch plan;
+};
+
+// 16 bytes of a row -> floats in shared memory.
+template <typename T>
+__device__ __forceinline__ void put_vec(float *dst, const uint4 &w) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint4 *>(dst) = w;
+    } else {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dst[2 * e] = __uint_as_float(x[e] << 16);
+            dst[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Thread (row = tid / 8, sub = tid % 8) of the block: scores of keys sub + 8 i,
+// output columns 4 sub + 32 i.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem<HD> &s = *reinterpret_cast<Smem<HD> *>(raw);
+    constexpr int VE = 16 / (int)sizeof(T), VR = HD / VE;  // vectors of a row
+    const int tid = threadIdx.x, c = blockIdx.x, P = gridDim.x;
+    const int row = tid >> 3, sub = tid & 7;
+    Cursor cur = make_plan<kThreads, kRows, kKeys, kMinTiles>(a, c, P, &s.plan, c == 0);
+    Segment g;
+    bool any = false;
+    while (next_segment<kRows, kKeys>(a, cur, g)) {
+        any = true;
+        __syncthreads();  // the previous segment's tiles are no longer read
+        const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);
+        for (int i = tid; i < kRows * VR; i += kThreads) {
+            const int ri = i / VR, e = i % VR * VE;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (ri < rows) {
+                const int t = (g.qt * kRows + ri) / a.G, gh = (g.qt * kRows + ri) % a.G;
+                w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
+                                                     (g.req.row0 + t) * a.q_stride +
+                                                     (g.h * a.G + gh) * HD + e);
+            }
+            put_vec<T>(&s.q[ri][e], w);
+        }
+        const int place = g.req.ctx + (g.qt * kRows + row) / a.G;  // of this thread's row
+        float m = -INFINITY, l = 0.f, o[HD / 8] = {};
+        for (int i = g.i0; i < g.i1; ++i) {
+            const int j0 = tile_place<kKeys>(g.span, i);
+            __syncthreads();
+            for (int x = tid; x < kKeys * VR; x += kThreads) {
+                const int kj = x / VR, e = x % VR * VE, j = j0 + kj;
+                uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
+                if (unit_sees(a, g.span, j)) {
+                    const int page =
+                        a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
+                    if (page >= 0 && page < a.n_pages) {
+                        const long long at =
+                            (long long)page * a.page_stride +
+                            (((long long)g.h << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * HD + e;
+                        wk = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k) + at);
+                        wv = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + at);
+                    } else if (a.dev_err) {
+                        atomicOr(a.dev_err, GDN_DEVERR_PAGE);
+                    }
+                }
+                put_vec<T>(&s.k[kj][e], wk);
+                put_vec<T>(&s.v[kj][e], wv);
+            }
+            __syncthreads();
+            float x[kKeys / 8] = {};
+#pragma unroll 4
+            for (int e = 0; e < HD; e += 4) {
+                const float4 qv = *reinterpret_cast<const float4 *>(&s.q[row][e]);
+#pragma unroll
+                for (int u = 0; u < kKeys / 8; ++u) {
+                    const float4 kv = *reinterpret_cast<const float4 *>(&s.k[sub + 8 * u][e]);
+                    x[u] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, x[u]))));
+                }
+            }
+            float top = -INFINITY;
+            bool seen[kKeys / 8];
+#pragma unroll
+            for (int u = 0; u < kKeys / 8; ++u) {
+                seen[u] = row < rows && row_sees(a, place, j0 + sub + 8 * u);
+                x[u] = seen[u] ? x[u] * a.scale_log2 : -INFINITY;
+                top = fmaxf(top, x[u]);
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+            const float keep = exp2f(m - base);  // 0 while m = -inf
+            float part = 0.f;
+#pragma unroll
+            for (int u = 0; u < kKeys / 8; ++u) {
+                const float e = exp2f(x[u] - base);
+                s.p[row][sub + 8 * u] = seen[u] ? e : 0.f;
+                part += seen[u] ? e : 0.f;
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            l = l * keep + part;
+            m = mn;
+#pragma unroll
+            for (int u = 0; u < HD / 8; ++u) o[u] *= keep;
+            __syncwarp();  // the row's scores come from threads of this warp only
+            for (int kj = 0; kj < kKeys; ++kj) {
+                const float p = s.p[row][kj];
+                if (p == 0.f) continue;  // a hidden place adds nothing, whatever v holds there
+#pragma unroll
+                for (int u = 0; u < HD / 32; ++u) {
+                    const float4 vv = *reinterpret_cast<const float4 *>(&s.v[kj][4 * sub + 32 * u]);
+                    o[4 * u] = fmaf(p, vv.x, o[4 * u]);
+                    o[4 * u + 1] = fmaf(p, vv.y, o[4 * u + 1]);
+                    o[4 * u + 2] = fmaf(p, vv.z, o[4 * u + 2]);
+                    o[4 * u + 3] = fmaf(p, vv.w, o[4 * u + 3]);
+                }
+            }
+            __syncwarp();
+        }
+        if (row < rows) {
+            if (g.i0 == 0 && g.i1 == g.span.n) {
+                const int t = (g.qt * kRows + row) / a.G, gh = (g.qt * kRows + row) % a.G;
+                const long long at = (long long)(g.req.row0 + t) * a.Hq + g.h * a.G + gh;
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int u = 0; u < HD / 8; ++u)
+                    put(static_cast<T *>(a.o) + at * HD + 4 * sub + 32 * (u / 4) + u % 4, o[u] * inv);
+                if (a.lse && sub == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+            } else {
+                float *dst = a.part + (long long)part_slot(c, g) * kRows * (HD + 2);
+#pragma unroll
+                for (int u = 0; u < HD / 8; ++u)
+                    dst[row * HD + 4 * sub + 32 * (u / 4) + u % 4] = o[u];
+                if (sub == 0) {
+                    dst[kRows * HD + row] = m;
+                    dst[kRows * HD + kRows + row] = l;
+                }
+            }
+        }
+    }
+    if (tid == 0) write_desc(a, c, g, any, cur.x, s.plan.total, s.plan.workers);
+}
+
+// Joins the partials of a unit that spans workers c .. last: block (c, y) its
+// rows y * 8 .. y * 8 + 7, a warp a row.  Partials are added in the order of the
+// workers; each counts 2^(m_w - m).
+template <typename T, int ROWS, int HD>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
+    const int last = d0.x, qt = d0.y, h = d0.z, row0 = d0.w, T_r = d1.x;
+    if (last < 0 || row >= ROWS || qt * ROWS + row >= T_r * a.G) return;
+    constexpr long long kSlot = (long long)ROWS * (HD + 2);
+    auto slot = [&](int w) { return a.part + (w == c ? 2 * c + 1 : 2 * w) * kSlot; };
+    // The row's maximum: a lane a worker.
+    float m = -INFINITY;
+    for (int w = c + lane; w <= last; w += 32) m = fmaxf(m, slot(w)[ROWS * HD + row]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = m == -INFINITY ? 0.f : m;
+    constexpr int E = HD / 32;
+    float o[E] = {}, l = 0.f;
+    for (int w0 = c; w0 <= last; w0 += 32) {
+        float weight = 0.f, lw = 0.f;
+        if (w0 + lane <= last) {
+            const float *p = slot(w0 + lane) + ROWS * HD + row;
+            weight = exp2f(p[0] - base);
+            lw = p[ROWS];
+        }
+        const int n = min(32, last - w0 + 1);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float f = __shfl_sync(0xffffffffu, weight, i);
+            l = fmaf(__shfl_sync(0xffffffffu, lw, i), f, l);
+            const float *p = slot(w0 + i) + row * HD + lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(p[32 * e], f, o[e]);
+        }
+    }
+    const int t = (qt * ROWS + row) / a.G, gh = (qt * ROWS + row) % a.G;
+    const long long at = (long long)(row0 + t) * a.Hq + h * a.G + gh;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) put(static_cast<T *>(a.o) + at * HD + lane + 32 * e, o[e] * inv);
+    if (a.lse && lane == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <typename K>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs &a,
+                   cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T, int HD>
+cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<T, HD>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(Smem<HD>));
+    if (e != cudaSuccess) return e;
+    e = launch(attn_simple_kernel<T, HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a, stream);
+    if (e != cudaSuccess) return e;
+    return launch(combine_kernel<T, kRows, HD>, dim3(kAttnWorkers, kRows / 8), 256, 0, a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream) {
+    switch (a.hd) {
+        case 32: return bf16 ? launch_simple<__nv_bfloat16, 32>(a, stream) : launch_simple<float, 32>(a, stream);
+        case 64: return bf16 ? launch_simple<__nv_bfloat16, 64>(a, stream) : launch_simple<float, 64>(a, stream);
+        case 128: return bf16 ? launch_simple<__nv_bfloat16, 128>(a, stream) : launch_simple<float, 128>(a, stream);
+        default: return bf16 ? launch_simple<__nv_bfloat16, 256>(a, stream) : launch_simple<float, 256>(a, stream);
+    }
+}
+
+int64_t attn_workspace(bool, int hd) {
+    return kAttnWorkers * (2 * (int64_t)sizeof(int4) + 2ll * kRows * (hd + 2) * (int64_t)sizeof(float));
+}
+
+}  // namespace gdn

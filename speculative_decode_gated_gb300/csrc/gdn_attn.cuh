@@ -1,0 +1,290 @@
+// Shared device-side pieces of the attention calls over a paged key/value
+// cache: the kernel argument block, the division of a call's work among the
+// blocks, and the places of partial results.
+//
+// Work.  A unit is (request r, query tile qt, key head h): ROWS query rows,
+// row i of the tile being (token t, head g of the group) with qt * ROWS + i =
+// t * G + g, so that every key and value read serves all G query heads that
+// share it.  A unit's key tiles (KT places each) are those that hold a place
+// some row of it sees: under a window the tiles of the first `sinks` places,
+// then those from the first row's window to the last row's own place.  All
+// units' tiles in order (request, query tile, key head, tile) form one line of
+// N tiles, and worker c of P takes tiles [c N / P, (c + 1) N / P): equal work
+// whatever the requests' lengths, which only the device knows.  A unit that
+// lies in one worker's range is finished there; one that spans several leaves
+// a partial (unnormalised sums, running maximum, total) per worker, joined by
+// combine_kernel in the order of the workers, so results do not depend on
+// timing.  A worker has at most two partials: the end of a unit begun earlier
+// (slot 2c) and the beginning of one finished later (slot 2c + 1).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+struct AttnArgs {
+    int B, Hq, Hkv, G, hd, max_T;
+    int page_shift;          // log2 of the page size
+    int max_pages;
+    int window, sinks;       // window = 0: none
+    float scale_log2;        // scale * log2(e): the softmax runs in powers of two
+    long long n_tok;
+    const int32_t *cu_seqlens;
+    const void *k, *v;
+    long long n_pages, page_stride;  // page_stride in elements
+    const int32_t *page_table;
+    const int32_t *kv_len;
+    int32_t *dev_err;
+    const void *q;
+    long long q_stride;
+    void *o;
+    float *lse;
+    float *part;             // 2P partial slots of ROWS * (hd + 2) floats
+    int4 *desc;              // [P][2]: which unit worker c leaves unfinished
+};
+
+// One request's rows and place in the cache; ok = false: skipped.
+struct AttnReq {
+    int row0, T, ctx;
+    bool ok;
+};
+
+__device__ __forceinline__ AttnReq load_request(const AttnArgs &a, int r, bool report) {
+    AttnReq q;
+    long long c1;
+    if (a.cu_seqlens) {
+        q.row0 = a.cu_seqlens[r];
+        c1 = a.cu_seqlens[r + 1];
+    } else {
+        q.row0 = r * a.max_T;
+        c1 = (long long)q.row0 + a.max_T;
+    }
+    q.ctx = a.kv_len[r];
+    const long long T = c1 - q.row0;
+    int err = 0;
+    if (T < 0 || T > a.max_T || q.row0 < 0 || c1 > a.n_tok) err |= GDN_DEVERR_SEQLEN;
+    q.T = (int)T;
+    if (q.ctx < 0 || (!err && (long long)q.ctx + T > ((long long)a.max_pages << a.page_shift)))
+        err |= GDN_DEVERR_KV_LEN;
+    if (err && report && a.dev_err) atomicOr(a.dev_err, err);
+    q.ok = err == 0;
+    return q;
+}
+
+// Key tiles of query tile qt of a request.
+struct TileSpan {
+    int n;         // tiles, 0 when the query tile has no rows
+    int ns;        // of them at the sinks (tiles 0 .. ns - 1 of the cache)
+    int lo;        // the next one, and those after it, are cache tiles lo, lo + 1, ...
+    int pmin, pmax;  // places of the first and the last row
+};
+
+template <int ROWS, int KT>
+__device__ __forceinline__ TileSpan tile_span(const AttnArgs &a, int T, int ctx, int qt) {
+    TileSpan s;
+    const long long first = (long long)qt * ROWS, rows = (long long)T * a.G;
+    if (first >= rows) {
+        s.n = s.ns = s.lo = s.pmin = s.pmax = 0;
+        return s;
+    }
+    const long long last = (first + ROWS < rows ? first + ROWS : rows) - 1;
+    s.pmin = ctx + (int)((unsigned)first / (unsigned)a.G);
+    s.pmax = ctx + (int)((unsigned)last / (unsigned)a.G);
+    s.lo = s.ns = 0;
+    if (a.window) {
+        const int w = s.pmin - a.window + 1;
+        s.lo = w > 0 ? w / KT : 0;
+        const int st = a.sinks / KT + (a.sinks % KT != 0);
+        s.ns = st < s.lo ? st : s.lo;
+    }
+    s.n = s.ns + s.pmax / KT + 1 - s.lo;
+    return s;
+}
+
+// Place of the first key of tile i of a unit.
+template <int KT>
+__device__ __forceinline__ int tile_place(const TileSpan &s, int i) {
+    return (i < s.ns ? i : s.lo + i - s.ns) * KT;
+}
+
+__device__ __forceinline__ bool row_sees(const AttnArgs &a, int p, int j) {
+    return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+}
+
+// Whether some row of the unit sees place j: no other place is read.
+__device__ __forceinline__ bool unit_sees(const AttnArgs &a, const TileSpan &s, int j) {
+    return j <= s.pmax && (a.window == 0 || j > s.pmin - a.window || j < a.sinks);
+}
+
+// A worker's current run of tiles [i0, i1) of one unit.
+struct Segment {
+    int r, qt, h;
+    AttnReq req;
+    TileSpan span;
+    int i0, i1;
+};
+
+// Shared-memory scratch of make_plan.
+struct PlanScratch {
+    long long warp_sum[32];
+    long long x0, x1, total;
+    long long off;   // of x0 within its entry
+    int entry;       // (r, qt) that holds x0, as r * nq_max + qt
+    int workers;
+};
+
+// A worker's position on the line of tiles.
+struct Cursor {
+    long long x, x1;   // next tile, end of the range
+    long long off;     // of x within the entry
+    int r, qt;
+};
+
+// Every thread of the block calls it; ends with a barrier.  At least MIN_TILES
+// tiles to a worker: fewer, longer runs when there is little work.
+template <int NT, int ROWS, int KT, int MIN_TILES>
+__device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, PlanScratch *s,
+                                            bool report) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nqm = a.max_T ? (int)(((long long)a.max_T * a.G + ROWS - 1) / ROWS) : 1;
+    const long long E = (long long)a.B * nqm;
+    const long long chunk = (E + NT - 1) / NT;
+    const long long e0 = tid * chunk, e1 = e0 + chunk < E ? e0 + chunk : E;
+    if (tid == 0) s->entry = -1;
+
+    // Tiles of this thread's entries.
+    long long sum = 0;
+    for (long long e = e0; e < e1;) {
+        const int r = (int)(e / nqm);
+        int qt = (int)(e - (long long)r * nqm);
+        const long long rend = (long long)(r + 1) * nqm;
+        const AttnReq q = load_request(a, r, report && qt == 0);
+        if (q.ok) {
+            for (long long f = e; f < e1 && f < rend; ++f, ++qt) {
+                const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
+                if (n == 0) break;
+                sum += (long long)n * a.Hkv;
+            }
+        }
+        e = rend;
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) s->warp_sum[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const long long w = lane < NT / 32 ? s->warp_sum[lane] : 0;
+        long long wi = w;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, wi, d);
+            if (lane >= d) wi += y;
+        }
+        s->warp_sum[lane] = wi - w;
+        if (lane == 31) {
+            const long long by_size = (wi + MIN_TILES - 1) / MIN_TILES;
+            const int p = by_size < P ? (int)by_size : P;
+            s->total = wi;
+            s->workers = p;
+            s->x0 = c < p ? (long long)c * wi / p : 0;
+            s->x1 = c < p ? (long long)(c + 1) * wi / p : 0;
+        }
+    }
+    __syncthreads();
+    const long long x0 = s->x0, x1 = s->x1;
+    const long long before = s->warp_sum[warp] + incl - sum;
+    if (x1 > x0 && x0 >= before && x0 < before + sum) {  // exactly one thread
+        long long at = before;
+        for (long long e = e0; e < e1;) {
+            const int r = (int)(e / nqm);
+            int qt = (int)(e - (long long)r * nqm);
+            const long long rend = (long long)(r + 1) * nqm;
+            const AttnReq q = load_request(a, r, false);
+            if (q.ok) {
+                for (long long f = e; f < e1 && f < rend; ++f, ++qt) {
+                    const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
+                    if (n == 0) break;
+                    const long long m = (long long)n * a.Hkv;
+                    if (x0 < at + m) {
+                        s->entry = (int)f;
+                        s->off = x0 - at;
+                        e = e1;
+                        break;
+                    }
+                    at += m;
+                }
+            }
+            e = e < rend ? rend : e;
+        }
+    }
+    __syncthreads();
+    Cursor cur;
+    cur.x = x0;
+    cur.x1 = s->entry >= 0 ? x1 : x0;
+    cur.off = s->entry >= 0 ? s->off : 0;
+    cur.r = s->entry >= 0 ? s->entry / nqm : 0;
+    cur.qt = s->entry >= 0 ? s->entry % nqm : 0;
+    return cur;
+}
+
+// The next run of tiles of this worker; false when its range is done.
+template <int ROWS, int KT>
+__device__ __forceinline__ bool next_segment(const AttnArgs &a, Cursor &cur, Segment &g) {
+    if (cur.x >= cur.x1) return false;
+    for (; cur.r < a.B; ++cur.r, cur.qt = 0) {
+        g.req = load_request(a, cur.r, false);
+        if (!g.req.ok) continue;
+        g.span = tile_span<ROWS, KT>(a, g.req.T, g.req.ctx, cur.qt);
+        if (g.span.n) break;  // a query tile with rows; else the next request's first
+    }
+    if (cur.r >= a.B) return false;
+    const int n = g.span.n;
+    g.r = cur.r;
+    g.qt = cur.qt;
+    g.h = (int)(cur.off / n);
+    g.i0 = (int)(cur.off - (long long)g.h * n);
+    const long long left = cur.x1 - cur.x;
+    g.i1 = left < n - g.i0 ? g.i0 + (int)left : n;
+    const int len = g.i1 - g.i0;
+    cur.x += len;
+    cur.off += len;
+    if (cur.off >= (long long)n * a.Hkv) {
+        cur.off = 0;
+        ++cur.qt;
+    }
+    return true;
+}
+
+// The worker that holds tile g of the line of N tiles.
+__device__ __forceinline__ int worker_of(long long g, long long N, int P) {
+    return (int)(((g + 1) * P - 1) / N);
+}
+
+// Slot of a segment that does not cover its unit.
+__device__ __forceinline__ int part_slot(int c, const Segment &g) {
+    return 2 * c + (g.i0 == 0 ? 1 : 0);
+}
+
+// desc[c]: the unit whose beginning worker c holds and does not finish.  x is
+// the line position after segment g (its last segment); one thread calls it.
+__device__ __forceinline__ void write_desc(const AttnArgs &a, int c, const Segment &g, bool any,
+                                           long long x, long long N, int P) {
+    int4 d0 = make_int4(-1, 0, 0, 0), d1 = make_int4(0, 0, 0, 0);
+    if (any && g.i0 == 0 && g.i1 < g.span.n) {
+        d0 = make_int4(worker_of(x - g.i1 + g.span.n - 1, N, P), g.qt, g.h, g.req.row0);
+        d1 = make_int4(g.req.T, 0, 0, 0);
+    }
+    a.desc[2 * c] = d0;
+    a.desc[2 * c + 1] = d1;
+}
+
+}  // namespace gdn

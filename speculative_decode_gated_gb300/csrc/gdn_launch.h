@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include "gdn_attn.cuh"
 #include "gdn_device.cuh"
 
 namespace gdn {
@@ -27,5 +28,17 @@ cudaError_t launch_accept(int B, int max_T, const int32_t *cu_seqlens, long long
 // One block that waits on a barrier nothing completes, until the bounded wait
 // gives up; ORs GDN_DEVERR_TIMEOUT into *dev_err (not NULL).
 cudaError_t launch_wait_selftest(int32_t *dev_err, cudaStream_t stream);
+
+// Rotary positions and append (arguments already validated on the host; a.n_tok
+// is the number of rows for uniform input too, a.o the rotated queries).
+cudaError_t launch_rope(const AttnArgs &a, const gdn_rope &rope, bool bf16, const void *k,
+                        long long k_stride, const void *v, long long v_stride, void *k_pages,
+                        void *v_pages, cudaStream_t stream);
+
+// Chunk attention over the cache.  a.desc and a.part point into the workspace:
+// attn_workspace() bytes, the 2 * kAttnWorkers descriptors first.
+constexpr int kAttnWorkers = 304;  // blocks of the attention kernels: two on each of 152 SMs
+int64_t attn_workspace(bool bf16, int hd);
+cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream);
 
 }  // namespace gdn

@@ -5,7 +5,8 @@ placement of each request's checkpoint into its pool slot.
 """
 from __future__ import annotations
 
-from typing import Optional
+import math
+from typing import Optional, Tuple
 
 import numpy as np
 import torch
@@ -231,3 +232,36 @@ def commit_verify_launcher(d: DeviceProblem, prevs, ws, stream):
             raise binding.GdnError(st, "gdn_commit_verify")
     call.keep = (d, d.c, prevs, ws)  # the owners of the raw addresses above
     return call
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, trained: int = 4096, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, mscale) of binding.make_rope for a rotary embedding of rot_dim elements.
+
+    "none": base^(-2i / rot_dim).  Stretched to contexts `factor` times the trained one:
+    "linear" divides every frequency (position interpolation); "ntk" raises the base so
+    that the last pair is divided by `factor` and the first by 1; "yarn" divides the pairs
+    that make fewer than beta_slow turns over the `trained` positions, keeps those that
+    make more than beta_fast, blends linearly between, and scales cosine and sine by
+    0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if base <= 1.0 or factor < 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    f, mscale = base ** (-2.0 * i / rot_dim), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk needs two pairs at least")
+        f = (base * factor ** (rot_dim / (rot_dim - 2.0))) ** (-2.0 * i / rot_dim)
+    elif scaling == "yarn":
+        turns = trained * f / (2.0 * math.pi)
+        keep = np.clip((turns - beta_slow) / (beta_fast - beta_slow), 0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling != "none":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(f, dtype=torch.float32, device=device), mscale
