@@ -344,7 +344,7 @@ typedef struct gdn_attn {
     void *k_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
     void *v_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
     int64_t n_pages;             /* 1 .. 2^31 - 1 */
-    int64_t page_stride;         /* elements from a page to the next; a multiple of 16 bytes */
+    int64_t page_stride;         /* elements from a page to the next; a multiple of 16 bytes, at most 2^36 */
     const int32_t *page_table;   /* device [batch][max_pages]; entries no row needs are not read */
     const int32_t *kv_len;       /* device [batch]: tokens in the cache before this step */
     int32_t *dev_err;            /* device int32 error word (GDN_DEVERR_* bits), or NULL */

@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_recurrent.cu", "gdn_chunk.cu", "gdn_accept.cu", "gdn_selftest.cu",
-           "gdn_rope.cu", "gdn_attn.cu"]
+           "gdn_rope.cu", "gdn_attn.cu", "gdn_attn_rows.cu",
+           "gdn_attn_tc.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

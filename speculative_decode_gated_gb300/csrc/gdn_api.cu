@@ -433,7 +433,7 @@ gdn_status attn_validate(const gdn_attn *p, bool *empty) {
         p->n_pages > 0x7fffffffLL)
         return GDN_ERR_BAD_DIM;
     if (p->page_stride < (int64_t)p->kv_heads * p->page_size * p->head_dim ||
-        p->page_stride > (1ll << 40) || p->page_stride * attn_esz(p) % 16 != 0)
+        p->page_stride > (1ll << 36) || p->page_stride * attn_esz(p) % 16 != 0)
         return GDN_ERR_BAD_DIM;
     if (!p->k_pages || !p->v_pages || !p->page_table || !p->kv_len) return GDN_ERR_NULL_PTR;
     if (!aligned16(p->k_pages) || !aligned16(p->v_pages) || !aligned4(p->page_table) ||
@@ -517,7 +517,8 @@ gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, const void *
 
 int64_t gdn_paged_attn_workspace(const gdn_attn *p) {
     if (!p || attn_sizes(p) != GDN_OK) return -1;
-    return gdn::attn_workspace(p->dtype == GDN_BF16, p->head_dim);
+    return gdn::attn_workspace(p->dtype == GDN_BF16, p->head_dim,
+                               (long long)p->max_T * (p->q_heads / p->kv_heads));
 }
 
 gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, void *o, float *lse,

@@ -240,30 +240,63 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<T, HD>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Smem<HD>));
+    const cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<float, HD>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(Smem<HD>));
     if (e != cudaSuccess) return e;
-    e = launch(attn_simple_kernel<T, HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a, stream);
-    if (e != cudaSuccess) return e;
-    return launch(combine_kernel<T, kRows, HD>, dim3(kAttnWorkers, kRows / 8), 256, 0, a, stream);
+    return launch(attn_simple_kernel<float, HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a,
+                  stream);
+}
+
+// The two launches of a call: finished units and partials, then the join.
+template <int HD>
+cudaError_t launch_hd(const AttnArgs &a, bool bf16, cudaStream_t stream) {
+    const AttnKind kind = attn_kind(bf16, HD, (long long)a.max_T * a.G);
+    const auto joined = [&](cudaError_t first, auto join, int workers, int rows) {
+        return first != cudaSuccess ? first
+                                    : launch(join, dim3(workers, rows / 8), 256, 0, a, stream);
+    };
+    if (kind == kAttnSimple)
+        return joined(launch_simple<HD>(a, stream), combine_kernel<float, 16, HD>, kAttnWorkers, 16);
+    if constexpr (HD == 64 || HD == 128) {
+        if (kind == kAttnDrafts)
+            return joined(launch_attn_tc(a, false, stream), combine_kernel<__nv_bfloat16, 128, HD>,
+                          kAttnTcWorkers, 128);
+        if (kind == kAttnWide)
+            return joined(launch_attn_tc(a, true, stream), combine_kernel<__nv_bfloat16, 256, HD>,
+                          kAttnTcWorkers, 256);
+    }
+    return joined(launch_attn_rows(a, stream), combine_kernel<__nv_bfloat16, 16, HD>, kAttnWorkers, 16);
 }
 
 }  // namespace
 
 cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream) {
     switch (a.hd) {
-        case 32: return bf16 ? launch_simple<__nv_bfloat16, 32>(a, stream) : launch_simple<float, 32>(a, stream);
-        case 64: return bf16 ? launch_simple<__nv_bfloat16, 64>(a, stream) : launch_simple<float, 64>(a, stream);
-        case 128: return bf16 ? launch_simple<__nv_bfloat16, 128>(a, stream) : launch_simple<float, 128>(a, stream);
-        default: return bf16 ? launch_simple<__nv_bfloat16, 256>(a, stream) : launch_simple<float, 256>(a, stream);
+        case 32: return launch_hd<32>(a, bf16, stream);
+        case 64: return launch_hd<64>(a, bf16, stream);
+        case 128: return launch_hd<128>(a, bf16, stream);
+        default: return launch_hd<256>(a, bf16, stream);
     }
 }
 
-int64_t attn_workspace(bool, int hd) {
-    return kAttnWorkers * (2 * (int64_t)sizeof(int4) + 2ll * kRows * (hd + 2) * (int64_t)sizeof(float));
+// Which kernel runs, by type and rows a key head: float32 on the CUDA cores; up to
+// 16 rows as one mma.sync tile; more on tcgen05, in units of 128 or 256 rows, for the
+// heads whose tiles fit there.
+AttnKind attn_kind(bool bf16, int hd, long long rows) {
+    if (!bf16) return kAttnSimple;
+    if (rows <= 16 || (hd != 64 && hd != 128)) return kAttnRows;
+    return rows <= 128 ? kAttnDrafts : kAttnWide;
+}
+
+int64_t attn_workspace(bool bf16, int hd, long long rows) {
+    const AttnKind kind = attn_kind(bf16, hd, rows);
+    const int64_t workers = kind == kAttnDrafts || kind == kAttnWide ? kAttnTcWorkers : kAttnWorkers;
+    const int64_t unit = kind == kAttnWide ? 256 : kind == kAttnDrafts ? 128 : 16;
+    return 2 * kAttnWorkers * (int64_t)sizeof(int4) +
+           2 * workers * unit * (hd + 2) * (int64_t)sizeof(float);
 }
 
 }  // namespace gdn

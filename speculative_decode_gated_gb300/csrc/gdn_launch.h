@@ -37,8 +37,13 @@ cudaError_t launch_rope(const AttnArgs &a, const gdn_rope &rope, bool bf16, cons
 
 // Chunk attention over the cache.  a.desc and a.part point into the workspace:
 // attn_workspace() bytes, the 2 * kAttnWorkers descriptors first.
-constexpr int kAttnWorkers = 304;  // blocks of the attention kernels: two on each of 152 SMs
-int64_t attn_workspace(bool bf16, int hd);
+constexpr int kAttnWorkers = 304;    // blocks, two on each of 152 SMs
+constexpr int kAttnTcWorkers = 152;  // blocks of the tcgen05 kernel, one an SM
+enum AttnKind { kAttnSimple, kAttnRows, kAttnDrafts, kAttnWide };
+AttnKind attn_kind(bool bf16, int hd, long long rows);  // rows: max_T times the group
+int64_t attn_workspace(bool bf16, int hd, long long rows);
 cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t stream);  // their first launches
+cudaError_t launch_attn_tc(const AttnArgs &a, bool wide, cudaStream_t stream);
 
 }  // namespace gdn
