@@ -450,6 +450,10 @@ gdn::AttnArgs attn_args(const gdn_attn *p, const void *q, int64_t q_stride, void
     a.G = p->q_heads / p->kv_heads;
     a.hd = p->head_dim;
     a.max_T = p->max_T;
+    if (a.G > 1) {  // 2^shift < G <= 2^(shift + 1), so the quotient below fits 32 bits
+        while ((2 << a.g_shift) < a.G) ++a.g_shift;
+        a.g_magic = (uint32_t)(((1ull << (32 + a.g_shift)) + a.G - 1) / a.G);
+    }
     while ((1 << a.page_shift) < p->page_size) ++a.page_shift;
     a.max_pages = p->max_pages;
     a.window = p->window;

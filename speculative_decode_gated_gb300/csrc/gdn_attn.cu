@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
                 float *dst = a.part + (long long)part_slot(c, g) * kRows * (HD + 2);
 #pragma unroll
                 for (int u = 0; u < HD / 8; ++u)
-                    dst[row * HD + 4 * sub + 32 * (u / 4) + u % 4] = o[u];
+                    dst[part_at<kRows>(row, 4 * sub + 32 * (u / 4) + u % 4)] = o[u];
                 if (sub == 0) {
                     dst[kRows * HD + row] = m;
                     dst[kRows * HD + kRows + row] = l;
@@ -184,44 +184,53 @@ template <typename T, int ROWS, int HD>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int c = blockIdx.x;
     const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
     const int last = d0.x, qt = d0.y, h = d0.z, row0 = d0.w, T_r = d1.x;
-    if (last < 0 || row >= ROWS || qt * ROWS + row >= T_r * a.G) return;
+    const int rows = min(8, T_r * a.G - qt * ROWS - (int)blockIdx.y * 8);
+    if (last < 0 || rows <= 0) return;
     constexpr long long kSlot = (long long)ROWS * (HD + 2);
     auto slot = [&](int w) { return a.part + (w == c ? 2 * c + 1 : 2 * w) * kSlot; };
-    // The row's maximum: a lane a worker.
+    // Thread (row = tid % 8, column group = tid / 8): eight rows of four columns are a
+    // line of the partials.
+    constexpr int CG = HD / 4;              // column groups
+    constexpr int PER = (CG + 31) / 32;     // of them a thread
+    const int r = threadIdx.x & 7, cg = threadIdx.x >> 3, row = blockIdx.y * 8 + r;
     float m = -INFINITY;
-    for (int w = c + lane; w <= last; w += 32) m = fmaxf(m, slot(w)[ROWS * HD + row]);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = m == -INFINITY ? 0.f : m;
-    constexpr int E = HD / 32;
-    float o[E] = {}, l = 0.f;
-    for (int w0 = c; w0 <= last; w0 += 32) {
-        float weight = 0.f, lw = 0.f;
-        if (w0 + lane <= last) {
-            const float *p = slot(w0 + lane) + ROWS * HD + row;
-            weight = exp2f(p[0] - base);
-            lw = p[ROWS];
-        }
-        const int n = min(32, last - w0 + 1);
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float f = __shfl_sync(0xffffffffu, weight, i);
-            l = fmaf(__shfl_sync(0xffffffffu, lw, i), f, l);
-            const float *p = slot(w0 + i) + row * HD + lane;
+    for (int w = c; w <= last; ++w) m = fmaxf(m, slot(w)[ROWS * HD + row]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float4 o[PER] = {};
+    float l = 0.f;
+#pragma unroll 4
+    for (int w = c; w <= last; ++w) {
+        const float *p = slot(w);
+        const float f = exp2f(p[ROWS * HD + row] - base);
+        l = fmaf(p[ROWS * HD + ROWS + row], f, l);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(p[32 * e], f, o[e]);
+        for (int e = 0; e < PER; ++e) {
+            if (cg + 32 * e >= CG) continue;
+            const float4 x = *reinterpret_cast<const float4 *>(p + part_at<ROWS>(row, 4 * (cg + 32 * e)));
+            o[e].x = fmaf(x.x, f, o[e].x);
+            o[e].y = fmaf(x.y, f, o[e].y);
+            o[e].z = fmaf(x.z, f, o[e].z);
+            o[e].w = fmaf(x.w, f, o[e].w);
         }
     }
-    const int t = (qt * ROWS + row) / a.G, gh = (qt * ROWS + row) % a.G;
-    const long long at = (long long)(row0 + t) * a.Hq + h * a.G + gh;
+    if (r >= rows) return;
+    const int i = qt * ROWS + row, t = div_group(a, i);
+    const long long at = (long long)(row0 + t) * a.Hq + h * a.G + (i - t * a.G);
     const float inv = 1.f / l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) put(static_cast<T *>(a.o) + at * HD + lane + 32 * e, o[e] * inv);
-    if (a.lse && lane == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+    for (int e = 0; e < PER; ++e) {
+        if (cg + 32 * e >= CG) continue;
+        T *dst = static_cast<T *>(a.o) + at * HD + 4 * (cg + 32 * e);
+        put(dst, o[e].x * inv);
+        put(dst + 1, o[e].y * inv);
+        put(dst + 2, o[e].z * inv);
+        put(dst + 3, o[e].w * inv);
+    }
+    if (a.lse && cg == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <typename K>

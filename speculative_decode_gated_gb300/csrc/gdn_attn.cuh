@@ -29,6 +29,7 @@ namespace gdn {
 
 struct AttnArgs {
     int B, Hq, Hkv, G, hd, max_T;
+    uint32_t g_magic, g_shift;  // n / G = umulhi(n, g_magic) >> g_shift for n < 2^31, G > 1
     int page_shift;          // log2 of the page size
     int max_pages;
     int window, sinks;       // window = 0: none
@@ -47,6 +48,10 @@ struct AttnArgs {
     float *part;             // 2P partial slots of ROWS * (hd + 2) floats
     int4 *desc;              // [P][2]: which unit worker c leaves unfinished
 };
+
+__device__ __forceinline__ int div_group(const AttnArgs &a, int n) {
+    return a.G == 1 ? n : (int)(__umulhi((unsigned)n, a.g_magic) >> a.g_shift);
+}
 
 // One request's rows and place in the cache; ok = false: skipped.
 struct AttnReq {
@@ -87,14 +92,14 @@ struct TileSpan {
 template <int ROWS, int KT>
 __device__ __forceinline__ TileSpan tile_span(const AttnArgs &a, int T, int ctx, int qt) {
     TileSpan s;
-    const long long first = (long long)qt * ROWS, rows = (long long)T * a.G;
+    const int first = qt * ROWS, rows = T * a.G;  // below 2^31: checked on the host
     if (first >= rows) {
         s.n = s.ns = s.lo = s.pmin = s.pmax = 0;
         return s;
     }
-    const long long last = (first + ROWS < rows ? first + ROWS : rows) - 1;
-    s.pmin = ctx + (int)((unsigned)first / (unsigned)a.G);
-    s.pmax = ctx + (int)((unsigned)last / (unsigned)a.G);
+    const int last = min(ROWS, rows - first) + first - 1;
+    s.pmin = ctx + div_group(a, first);
+    s.pmax = ctx + div_group(a, last);
     s.lo = s.ns = 0;
     if (a.window) {
         const int w = s.pmin - a.window + 1;
@@ -151,21 +156,21 @@ template <int NT, int ROWS, int KT, int MIN_TILES>
 __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, PlanScratch *s,
                                             bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nqm = a.max_T ? (int)(((long long)a.max_T * a.G + ROWS - 1) / ROWS) : 1;
-    const long long E = (long long)a.B * nqm;
-    const long long chunk = (E + NT - 1) / NT;
-    const long long e0 = tid * chunk, e1 = e0 + chunk < E ? e0 + chunk : E;
+    const int nqm = a.max_T ? (a.max_T * a.G + ROWS - 1) / ROWS : 1;
+    const unsigned E = (unsigned)a.B * nqm;  // below 2^31: checked on the host
+    const unsigned chunk = (E + NT - 1) / NT;
+    const unsigned e0 = min(tid * chunk, E), e1 = min(e0 + chunk, E);
     if (tid == 0) s->entry = -1;
 
     // Tiles of this thread's entries.
     long long sum = 0;
-    for (long long e = e0; e < e1;) {
+    for (unsigned e = e0; e < e1;) {
         const int r = (int)(e / nqm);
-        int qt = (int)(e - (long long)r * nqm);
-        const long long rend = (long long)(r + 1) * nqm;
+        int qt = (int)(e - r * nqm);
+        const unsigned rend = (unsigned)(r + 1) * nqm;
         const AttnReq q = load_request(a, r, report && qt == 0);
         if (q.ok) {
-            for (long long f = e; f < e1 && f < rend; ++f, ++qt) {
+            for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
                 const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
                 if (n == 0) break;
                 sum += (long long)n * a.Hkv;
@@ -195,8 +200,13 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
             const int p = by_size < P ? (int)by_size : P;
             s->total = wi;
             s->workers = p;
-            s->x0 = c < p ? (long long)c * wi / p : 0;
-            s->x1 = c < p ? (long long)(c + 1) * wi / p : 0;
+            if (wi < (1 << 22)) {  // 32-bit products and quotients: (c + 1) below 2^10
+                s->x0 = c < p ? (unsigned)c * (unsigned)wi / (unsigned)p : 0;
+                s->x1 = c < p ? (unsigned)(c + 1) * (unsigned)wi / (unsigned)p : 0;
+            } else {
+                s->x0 = c < p ? (long long)c * wi / p : 0;
+                s->x1 = c < p ? (long long)(c + 1) * wi / p : 0;
+            }
         }
     }
     __syncthreads();
@@ -204,13 +214,13 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
     const long long before = s->warp_sum[warp] + incl - sum;
     if (x1 > x0 && x0 >= before && x0 < before + sum) {  // exactly one thread
         long long at = before;
-        for (long long e = e0; e < e1;) {
+        for (unsigned e = e0; e < e1;) {
             const int r = (int)(e / nqm);
-            int qt = (int)(e - (long long)r * nqm);
-            const long long rend = (long long)(r + 1) * nqm;
+            int qt = (int)(e - r * nqm);
+            const unsigned rend = (unsigned)(r + 1) * nqm;
             const AttnReq q = load_request(a, r, false);
             if (q.ok) {
-                for (long long f = e; f < e1 && f < rend; ++f, ++qt) {
+                for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
                     const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
                     if (n == 0) break;
                     const long long m = (long long)n * a.Hkv;
@@ -272,6 +282,14 @@ __device__ __forceinline__ int worker_of(long long g, long long N, int P) {
 // Slot of a segment that does not cover its unit.
 __device__ __forceinline__ int part_slot(int c, const Segment &g) {
     return 2 * c + (g.i0 == 0 ? 1 : 0);
+}
+
+// Within a slot of ROWS rows: element (row, col) of the output, four columns together
+// and then the next row, so that a thread a row (or a fragment) writes whole lines;
+// then the maxima and the totals.
+template <int ROWS>
+__device__ __forceinline__ int part_at(int row, int col) {
+    return ((col >> 2) * ROWS + row) * 4 + (col & 3);
 }
 
 // desc[c]: the unit whose beginning worker c holds and does not finish.  x is

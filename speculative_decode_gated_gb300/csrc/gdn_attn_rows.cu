@@ -171,22 +171,23 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
         const __nv_bfloat16 *qrow[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int i = g.qt * kRows + qr + 8 * e, t = i / a.G;
+            const int i = g.qt * kRows + qr + 8 * e, t = div_group(a, i);
             place[e] = g.req.ctx + t;
             qrow[e] = static_cast<const __nv_bfloat16 *>(a.q) + (g.req.row0 + t) * a.q_stride +
-                      (g.h * a.G + i % a.G) * HD;
+                      (g.h * a.G + i - t * a.G) * HD;
         }
         const bool has[2] = {qr < rows, qr + 8 < rows};
         uint32_t qf[C::kQInSmem ? 1 : HD / 16][4];
         if constexpr (C::kQInSmem) {
             __syncthreads();  // the previous segment's queries are no longer read
             for (int x = tid; x < kRows * (HD / 8); x += C::NT) {
-                const int r = x / (HD / 8), ch = x % (HD / 8), i = g.qt * kRows + r, t = i / a.G;
+                const int r = x / (HD / 8), ch = x % (HD / 8), i = g.qt * kRows + r;
+                const int t = div_group(a, i);
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (r < rows)
                     w = *reinterpret_cast<const uint4 *>(
                         static_cast<const __nv_bfloat16 *>(a.q) + (g.req.row0 + t) * a.q_stride +
-                        (g.h * a.G + i % a.G) * HD + ch * 8);
+                        (g.h * a.G + i - t * a.G) * HD + ch * 8);
                 *reinterpret_cast<uint4 *>(qs + chunk_at<HD>(r, ch)) = w;
             }
             __syncthreads();
@@ -390,7 +391,8 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                 if (!has[e]) continue;
                 const int row = qr + 8 * e, i = g.qt * kRows + row;
                 if (whole) {
-                    const long long at = (long long)(g.req.row0 + i / a.G) * a.Hq + g.h * a.G + i % a.G;
+                    const int t = div_group(a, i);
+                    const long long at = (long long)(g.req.row0 + t) * a.Hq + g.h * a.G + i - t * a.G;
                     const float inv = 1.f / all[e];
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) + at * HD + qc * 2;
 #pragma unroll
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                 } else {
 #pragma unroll
                     for (int n = 0; n < HD / 8; ++n)
-                        *reinterpret_cast<float2 *>(part + row * HD + n * 8 + qc * 2) =
+                        *reinterpret_cast<float2 *>(part + part_at<kRows>(row, n * 8 + qc * 2)) =
                             make_float2(o[n][2 * e], o[n][2 * e + 1]);
                     if (qc == 0) {
                         part[kRows * HD + row] = m[e];

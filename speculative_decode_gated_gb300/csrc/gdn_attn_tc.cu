@@ -43,7 +43,8 @@ namespace gdn {
 namespace {
 
 constexpr int kKT = 128;       // places of a tile
-constexpr int kThreads = 320;  // two softmax warpgroups, the TMA warp, the MMA warp
+constexpr int kThreads = 352;  // two softmax warpgroups; the TMA, the MMA and the segment warp
+constexpr int kSegs = 4;       // segments known ahead
 constexpr float kLazy = 8.f;
 constexpr uint32_t kP = 64;    // TMEM column of P_w within S_w: two weights a column
 
@@ -58,7 +59,8 @@ struct Cfg {
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_ready[2], o_full[2], q_ready[2], clean[2], joined, drain;
+    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], clean[2], joined, staged, drain;
+    unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
 struct Shared {
@@ -68,6 +70,7 @@ struct Shared {
     int dead;          // a wait gave up: every role leaves
     int poison[4];     // segment (mod 4) whose hidden places hold values that are not finite
     float m[2][kKT], l[2][kKT];
+    Segment seg[kSegs];  // r = -1: no more
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -111,11 +114,13 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes in groups of
-// eight (sbo apart), column boxes lbo apart.
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory matrix descriptors, 128-byte swizzle: rows of 128 bytes in groups of
+// eight, 1024 bytes apart; the low word is the address and the distance of the column
+// boxes (both in 16 bytes; an offset within a tile is added to it), the high one the same
+// for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+    return (addr >> 4) | (lbo >> 4) << 16;
 }
 
 // kind::f16, bf16 operands, float32 accumulator, M = 128; A K-major, B K- or MN-major.
@@ -124,18 +129,20 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t n, bool b_mn_major) {
            ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t b) {
@@ -198,54 +205,113 @@ struct Launch {
     CUtensorMap k, v;
 };
 
+// A ring slot and the parity of its round; advances through the ring.
+template <int NS>
+struct Ring {
+    uint32_t slot = 0, parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == NS) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- the segment thread
+
+// Works out the worker's segments ahead of the roles that use them (each takes loads that
+// wait on one another).
+template <bool WIDE>
+__device__ __forceinline__ void segment_role(const AttnArgs &a, Shared &s, Cursor cur) {
+    Ring<kSegs> ring;
+    for (;;) {
+        Segment g;
+        const bool more = next_segment<WIDE ? 256 : 128, kKT>(a, cur, g);
+        if (!more) g.r = -1;
+        if (!wait_one(bar(s.b.seg_empty[ring.slot]), ring.parity ^ 1, &s.dead)) return;
+        s.seg[ring.slot] = g;
+        arrive(bar(s.b.seg_full[ring.slot]));
+        if (!more) return;
+        ring.next();
+    }
+}
+
+// A role's view of the segments: the next one, or false.  Warps take part whole.
+struct SegReader {
+    Ring<kSegs> ring;
+    __device__ __forceinline__ bool next(Shared &s, Segment &g) {
+        if (!wait(bar(s.b.seg_full[ring.slot]), ring.parity, &s.dead)) return false;
+        g = s.seg[ring.slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive(bar(s.b.seg_empty[ring.slot]));
+        ring.next();
+        return g.r >= 0;
+    }
+    __device__ __forceinline__ bool next_one(Shared &s, Segment &g) {  // by a lone thread
+        if (!wait_one(bar(s.b.seg_full[ring.slot]), ring.parity, &s.dead)) return false;
+        g = s.seg[ring.slot];
+        arrive(bar(s.b.seg_empty[ring.slot]));
+        ring.next();
+        return g.r >= 0;
+    }
+};
+constexpr int kSegReaders = 8 + 1 + 1;  // arrivals a slot: softmax warps, TMA, MMA
+
 // ---------------------------------------------------------------- the TMA warp
 
 template <int HD, bool WIDE>
-__device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t ring, Cursor cur,
-                                          int lane, uint32_t &issued) {
+__device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t ring, int lane,
+                                          uint32_t &issued) {
     using C = Cfg<HD>;
-    constexpr int ROWS = WIDE ? 256 : 128;
     const AttnArgs &a = L.a;
     const int rows_box = min(1 << a.page_shift, kKT);  // places of a TMA box
     const int boxes = kKT / rows_box;
-    uint32_t pos = 0;
-    Segment g;
-    // This lane's page of tile i: its row and number, or n_pages (nothing needed, or no page).
-    auto page_of = [&](int i, int &row) -> int {
-        const int j = tile_place<kKT>(g.span, i) + lane * rows_box;
+    Ring<C::NS> at;
+    SegReader segs;
+    Segment g, gn;
+    // This lane's page of tile i of a segment: its row and number, or n_pages (nothing
+    // needed, or no page).
+    auto page_of = [&](const Segment &q, int i, int &row) -> int {
+        const int j = tile_place<kKT>(q.span, i) + lane * rows_box;
         row = j & ((1 << a.page_shift) - 1);
-        const TileSpan &sp = g.span;
-        if (lane >= boxes || i >= g.i1 || j > sp.pmax ||
+        const TileSpan &sp = q.span;
+        if (lane >= boxes || j > sp.pmax ||
             !(a.window == 0 || j + rows_box - 1 > sp.pmin - a.window || j < a.sinks))
             return (int)a.n_pages;
-        const int page = a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
+        const int page = a.page_table[(long long)q.r * a.max_pages + (j >> a.page_shift)];
         if (page >= 0 && page < a.n_pages) return page;
         if (a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
         return (int)a.n_pages;
     };
     auto issue = [&](const CUtensorMap *map, int page, int row) -> bool {
-        const uint32_t slot = pos % C::NS, round = pos / C::NS;
-        ++pos;
-        if (!wait(bar(s.b.empty[slot]), (round & 1) ^ 1, &s.dead)) return false;
-        const uint32_t f = bar(s.b.full[slot]);
+        if (!wait(bar(s.b.empty[at.slot]), at.parity ^ 1, &s.dead)) return false;
+        const uint32_t f = bar(s.b.full[at.slot]);
         if (lane == 0) arrive_expect(f, C::kTile);
         __syncwarp();
         if (lane < boxes) {
-            const uint32_t dst = ring + slot * C::kTile + lane * rows_box * 128;
+            const uint32_t dst = ring + at.slot * C::kTile + lane * rows_box * 128;
 #pragma unroll
             for (int h = 0; h < HD / 64; ++h)
                 tma_4d(dst + h * C::kBox, map, 64 * h, row, g.h, page, f);
         }
-        issued = pos;
+        at.next();
+        ++issued;
         return true;
     };
-    while (next_segment<ROWS, kKT>(a, cur, g)) {
-        int row_n, next = page_of(g.i0, row_n);
+    // Pages are looked up a tile ahead, across segments too.
+    int row_n = 0, next = 0;
+    bool more = segs.next(s, g);
+    if (more) next = page_of(g, g.i0, row_n);
+    while (more) {
         int p0 = 0, r0 = 0, p1 = 0, r1 = 0, held = 0;  // pages of tiles whose values are to come
         int ik = g.i0;
+        more = segs.next(s, gn);
         auto keys = [&]() -> bool {
             const int page = next, row = row_n;
-            next = page_of(++ik, row_n);
+            if (++ik < g.i1)
+                next = page_of(g, ik, row_n);
+            else if (more)
+                next = page_of(gn, gn.i0, row_n);
             if (held++ == 0) {
                 p0 = page;
                 r0 = row;
@@ -268,6 +334,7 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
             if (!values()) return;
             if (i + (WIDE ? 1 : 2) < g.i1 && !keys()) return;
         }
+        g = gn;
     }
 }
 
@@ -275,46 +342,60 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
 
 template <int HD, bool WIDE>
 __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
-                                         Cursor cur, uint32_t tm) {
+                                         uint32_t tm) {
     using C = Cfg<HD>;
-    constexpr int ROWS = WIDE ? 256 : 128;
     const AttnArgs &a = L.a;
-    uint32_t pos = 0, seg = 0, np[2] = {0, 0}, nc[2] = {0, 0};
+    Ring<C::NS> at;
+    SegReader segs;
+    uint32_t seg = 0, np0 = 0, np1 = 0, nc0 = 0, nc1 = 0, staged = 0;
+    uint32_t held = 0;      // ring slot the softmax warpgroups stage their output in
+    bool holding = false;
     Segment g;
+    const uint32_t q_lo = desc_lo(qbuf, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, C::kBox);
     auto next_slot = [&](uint32_t &slot) -> bool {
-        slot = pos % C::NS;
-        const uint32_t round = pos / C::NS;
-        ++pos;
-        return wait_one(bar(s.b.full[slot]), round & 1, &s.dead);
+        slot = at.slot;
+        const bool ok = wait_one(bar(s.b.full[at.slot]), at.parity, &s.dead);
+        at.next();
+        return ok;
     };
     auto scores = [&](int w, uint32_t slot) {
-        const uint32_t q = qbuf + (WIDE ? w : (seg & 1)) * C::kTile, k = ring + slot * C::kTile;
+        const uint32_t q = q_lo + (WIDE ? w : (seg & 1)) * (C::kTile >> 4);
+        const uint32_t k = k_lo + slot * (C::kTile >> 4);
         fence_after();
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
-            mma_ss(tm + w * 128, desc128(q + off, 16, 1024), desc128(k + off, 16, 1024),
-                   idesc(128, false), kk > 0);
+            const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+            mma_ss(tm + w * 128, q + off, k + off, idesc(128, false), kk > 0);
         }
         commit(bar(s.b.s_full[w]));
     };
     auto output = [&](int w, uint32_t slot, bool first) {
-        const uint32_t v = ring + slot * C::kTile;
+        const uint32_t v = v_lo + slot * (C::kTile >> 4);
+        const uint32_t acc = first ? 0u : 1u;
         fence_after();
 #pragma unroll
         for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_ts(tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8,
-                   desc128(v + kk * 2048, C::kBox, 1024), idesc(HD, true), !first || kk > 0);
+            mma_ts(tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
+                   idesc(HD, true), kk > 0 ? 1u : acc);
     };
-    while (next_segment<ROWS, kKT>(a, cur, g)) {
-        uint32_t ks;
+    // The slot of the last segment's last values goes back to the ring when the warpgroups
+    // have written their output from it.
+    auto give_back = [&]() -> bool {
+        if (!holding) return true;
+        if (!wait_one(bar(s.b.staged), staged++ & 1, &s.dead)) return false;
+        arrive(bar(s.b.empty[held]));
+        holding = false;
+        return true;
+    };
+    while (segs.next_one(s, g)) {
+        uint32_t ks, vs = 0;
         const int n = g.i1 - g.i0;
         if (!next_slot(ks)) return;
         if (WIDE) {
-            for (int w = 0; w < 2; ++w) {
-                if (!wait_one(bar(s.b.q_ready[w]), seg & 1, &s.dead)) return;
-                scores(w, ks);
-            }
+            if (!wait_one(bar(s.b.q_ready[0]), seg & 1, &s.dead)) return;
+            scores(0, ks);
+            if (!wait_one(bar(s.b.q_ready[1]), seg & 1, &s.dead)) return;
+            scores(1, ks);
             commit(bar(s.b.empty[ks]));
         } else {
             if (!wait_one(bar(s.b.q_ready[seg & 1]), (seg >> 1) & 1, &s.dead)) return;
@@ -326,39 +407,45 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
                 commit(bar(s.b.empty[ks]));
             }
         }
+        if (!give_back()) return;
         for (int i = 0; i < n; ++i) {
-            uint32_t vs;
             if (!next_slot(vs)) return;
             const bool full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i));
             if (WIDE) {
-                if (!full && !wait_one(bar(s.b.clean[0]), nc[0]++ & 1, &s.dead)) return;
-                const bool more = i + 1 < n;
-                for (int w = 0; w < 2; ++w) {
-                    if (!wait_one(bar(s.b.p_ready[w]), np[w]++ & 1, &s.dead)) return;
-                    output(w, vs, i == 0);
-                    if (w == 1) commit(bar(s.b.empty[vs]));
-                    if (!more) {
-                        commit(bar(s.b.o_full[w]));
-                        continue;
-                    }
-                    if (w == 0 && !next_slot(ks)) return;
-                    scores(w, ks);
-                    if (w == 1) commit(bar(s.b.empty[ks]));
+                if (!full && !wait_one(bar(s.b.clean[0]), nc0++ & 1, &s.dead)) return;
+                if (!wait_one(bar(s.b.p_ready[0]), np0++ & 1, &s.dead)) return;
+                output(0, vs, i == 0);
+                if (i + 1 < n) {
+                    if (!next_slot(ks)) return;
+                    scores(0, ks);
+                }
+                if (!wait_one(bar(s.b.p_ready[1]), np1++ & 1, &s.dead)) return;
+                output(1, vs, i == 0);
+                if (i + 1 < n) {
+                    commit(bar(s.b.empty[vs]));
+                    scores(1, ks);
+                    commit(bar(s.b.empty[ks]));
+                } else {  // both at once: the outputs are staged over the values
+                    commit(bar(s.b.o_full));
                 }
             } else {
                 const int w = i & 1;
-                if (!full && !wait_one(bar(s.b.clean[w]), nc[w]++ & 1, &s.dead)) return;
-                if (!wait_one(bar(s.b.p_ready[w]), np[w]++ & 1, &s.dead)) return;
+                if (!full && !wait_one(bar(s.b.clean[w]), (w ? nc1++ : nc0++) & 1, &s.dead)) return;
+                if (!wait_one(bar(s.b.p_ready[w]), (w ? np1++ : np0++) & 1, &s.dead)) return;
                 output(w, vs, i < 2);
-                commit(bar(s.b.empty[vs]));
+                if (i + 1 < n)
+                    commit(bar(s.b.empty[vs]));
+                else
+                    commit(bar(s.b.o_full));
                 if (i + 2 < n) {
                     if (!next_slot(ks)) return;
                     scores(w, ks);
                     commit(bar(s.b.empty[ks]));
                 }
-                if (i + 1 == n) commit(bar(s.b.o_full[0]));
             }
         }
+        held = vs;
+        holding = true;
         ++seg;
     }
 }
@@ -390,28 +477,31 @@ __device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, 
 
 template <int HD, bool WIDE>
 __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
-                                             Cursor cur, Segment &g, bool &any, long long &x_end,
-                                             uint32_t tm) {
+                                             Segment &g, bool &any, uint32_t tm) {
     using C = Cfg<HD>;
     constexpr int ROWS = WIDE ? 256 : 128;
     constexpr int CR = HD / 8;  // 16-byte chunks of a row
     const AttnArgs &a = L.a;
-    const int tid = threadIdx.x, w = tid >> 7, t = tid & 127;
+    const int tid = threadIdx.x, w = tid >> 7, t = tid & 127, lane = tid & 31;
     const uint32_t lane_base = (uint32_t)(t & ~31) << 16;
     const uint32_t ts = tm + w * 128 + lane_base, to = tm + C::kO + w * 128 + lane_base;
+    SegReader segs;
 
-    // This thread's share of a segment's queries on their way to shared memory.
+    // This thread's share of a segment's queries on their way to shared memory: sixteen
+    // (eight) threads a row, rows 128 / CR apart.
     auto load_queries = [&](const Segment &q, uint32_t seg) {
-        const int first = WIDE ? w * 128 : w * 64, count = WIDE ? 128 : 64;
+        constexpr int count = WIDE ? 128 : 64;
+        const int first = w * count, rows = q.req.T * a.G - q.qt * ROWS;
         const uint32_t dst = qbuf + (WIDE ? w : (seg & 1)) * C::kTile;
-        const int rows = q.req.T * a.G - q.qt * ROWS;
-        for (int x = t; x < count * CR; x += 128) {
-            const int i = first + x / CR, c = x % CR, r = i & 127;
-            const int row = q.qt * ROWS + i, tok = row / a.G;
+        const int c = t % CR;
+        const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.q) + q.h * a.G * HD + c * 8;
+#pragma unroll 4
+        for (int i = first + t / CR; i < first + count; i += 128 / CR) {
+            const int r = i & 127, row = q.qt * ROWS + i, tok = div_group(a, row);
             const uint32_t at = dst + (c >> 3) * C::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q);
             const bool has = i < rows;
-            if (has) src += (q.req.row0 + tok) * a.q_stride + (q.h * a.G + row % a.G) * HD + c * 8;
+            const __nv_bfloat16 *src =
+                base + (has ? (q.req.row0 + tok) * a.q_stride + (row - tok * a.G) * HD : 0);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(src),
                          "r"(has ? 16 : 0)
                          : "memory");
@@ -424,30 +514,35 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         arrive(bar(s.b.q_ready[WIDE ? w : (seg & 1)]));
     };
 
-    uint32_t seg = 0, base_pos = 0, n_s = 0;
+    uint32_t seg = 0, n_s = 0;
+    uint32_t base_slot = 0, base_parity = 0;  // ring position of the segment's first tile
     Segment gn;
-    bool more = next_segment<ROWS, kKT>(a, cur, gn);
+    bool more = segs.next(s, gn);
     if (more) {
         load_queries(gn, 0);
         queries_ready(0);
     }
     while (more) {
         g = gn;
-        any = true;
-        x_end = cur.x;
-        Cursor ahead = cur;
-        more = next_segment<ROWS, kKT>(a, ahead, gn);
+        more = segs.next(s, gn);
         const int n = g.i1 - g.i0;
         const TileSpan sp = g.span;
         const int row = g.qt * ROWS + (WIDE ? w * 128 : 0) + t;
-        const bool has = row < g.req.T * a.G;
-        const int place = g.req.ctx + row / a.G;
+        const int place = g.req.ctx + div_group(a, row);
+        // Ring slot and parity of the values of the segment's tile i.
+        auto value_slot = [&](int i, uint32_t &slot, uint32_t &parity) {
+            uint32_t pos = base_slot + (WIDE ? 2 * i + 1 : min(n, i + 2) + i);
+            const uint32_t rounds = pos / C::NS;
+            slot = pos - rounds * C::NS;
+            parity = base_parity ^ (rounds & 1);
+        };
         bool q_pending = false;
         if (!WIDE && more) {  // the other buffer is free: the last segment is done with it
             load_queries(gn, seg + 1);
             q_pending = true;
         }
         float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int i = WIDE ? 0 : w; i < n; i += WIDE ? 1 : 2) {
             const int j0 = tile_place<kKT>(sp, g.i0 + i);
             const bool full = tile_full(a, sp, j0);
@@ -457,53 +552,75 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 load_queries(gn, seg + 1);
                 q_pending = true;
             }
+            uint32_t x[64];
+            uint32_t mask[4];  // of the tile's places, those that the row sees
             if (!full) {
-                // Clear what must not be seen from the value tile.
-                const uint32_t pos = base_pos + (WIDE ? 2 * i + 1 : min(n, i + 2) + i);
-                const uint32_t slot = pos % C::NS, vt = ring + slot * C::kTile;
-                if (!wait(bar(s.b.full[slot]), (pos / C::NS) & 1, &s.dead)) return;
+                // Clear what must not be seen from the value tile: this thread's place (half
+                // a place) of it.
+                uint32_t slot, parity;
+                value_slot(i, slot, parity);
+                const uint32_t vt = ring + slot * C::kTile;
+                if (!wait(bar(s.b.full[slot]), parity, &s.dead)) return;
+                constexpr int NC = WIDE ? CR / 2 : CR;
                 const int r = WIDE ? w * 64 + (t >> 1) : t;
-                const int c0 = WIDE ? (t & 1) * (CR / 2) : 0, c1 = c0 + (WIDE ? CR / 2 : CR);
-                const bool seen = unit_sees(a, sp, j0 + r);
-                for (int c = c0; c < c1; ++c) {
-                    const uint32_t at = vt + (c >> 3) * C::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                    uint32_t x[4] = {0, 0, 0, 0};
-                    bool write = !seen;
-                    if (seen) {
+                const int c0 = WIDE ? (t & 1) * NC : 0, j = j0 + r;
+                auto chunk = [&](int c) {
+                    return vt + ((c0 + c) >> 3) * C::kBox + r * 128 + ((((c0 + c) & 7) ^ (r & 7)) << 4);
+                };
+                if (!unit_sees(a, sp, j)) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(c)), "r"(0)
+                                     : "memory");
+                } else if (!(j <= sp.pmin && (a.window == 0 || j > sp.pmax - a.window || j < a.sinks))) {
+                    // Seen by some rows.  An element is not finite if its exponent is all ones.
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t v[4];
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(at)
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(chunk(c))
                                      : "memory");
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u, write = true;
-                            if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0xFFFFu, write = true;
-                        }
-                        if (write) s.poison[seg & 3] = (int)seg;
+                        for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7F807F80u) + 0x00800080u;
                     }
-                    if (write)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
-                                     "r"(x[1]), "r"(x[2]), "r"(x[3])
-                                     : "memory");
+                    if (odd & 0x80008000u) {
+                        s.poison[seg & 3] = (int)seg;
+#pragma unroll 1
+                        for (int c = 0; c < NC * 4; ++c) {
+                            uint32_t v;
+                            const uint32_t at = chunk(c >> 2) + (c & 3) * 4;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+                            if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+                            if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+                        }
+                    }
                 }
                 fence_async();
                 arrive(bar(s.b.clean[WIDE ? 0 : w]));
+                // place j0 + 32 q + e is bit e of mask[q]
+                const int hi = place - j0, lo = a.window ? hi - a.window : -1, sk = a.sinks - j0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // bits below x, of 32
+                    auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
+                    mask[q] = below(hi + 1 - 32 * q) &
+                              (~below(lo + 1 - 32 * q) | below(sk - 32 * q));
+                }
             }
             // The scores, half a row at a time: the second half stays in registers from
             // the maximum to the weights, the first is read twice.
-            uint32_t x[64];
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const int hi = place - j0, lo = a.window ? hi - a.window : -1, sk = a.sinks - j0;
             auto scores = [&](int half) {
                 tmem_ld32(ts + half * 64, x);
                 tmem_ld32(ts + half * 64 + 32, x + 32);
                 wait_ld();
                 if (!full) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const int c = half * 64 + e;
-                        if (c > hi || (c <= lo && c >= sk)) x[e] = 0xff800000u;  // -inf
-                    }
+                    for (int e = 0; e < 64; ++e)
+                        if (!(mask[half * 2 + e / 32] & (1u << (e & 31)))) x[e] = 0xff800000u;  // -inf
                 }
             };
             auto maximum = [&]() {
@@ -560,12 +677,12 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         if (q_pending) queries_ready(seg + 1);
 
         // The end of the segment.
-        if (!wait(bar(s.b.o_full[WIDE ? w : 0]), seg & 1, &s.dead)) return;
+        if (!wait(bar(s.b.o_full), seg & 1, &s.dead)) return;
         fence_after();
         const bool poisoned = *(volatile int *)&s.poison[seg & 3] == (int)seg;
         const bool whole = g.i0 == 0 && g.i1 == sp.n;
+        const int rows = g.req.T * a.G;
         float f0 = 1.f, f1 = 0.f;
-        int c0 = 0, c1 = HD;
         uint32_t ta = to, tb = to;
         if (!WIDE) {
             // Join: each warpgroup writes half of the columns of both outputs.
@@ -579,64 +696,114 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             f0 = exp2_fast(m0 - base);
             f1 = exp2_fast(m1 - base);
             l = s.l[0][t] * f0 + s.l[1][t] * f1;
-            c0 = w * (HD / 2);
-            c1 = c0 + HD / 2;
             ta = tm + C::kO + lane_base;
             tb = ta + 128;
         }
-        const long long at = (long long)(g.req.row0 + row / a.G) * a.Hq + g.h * a.G + row % a.G;
-        const float inv = 1.f / l;
+        const float inv = whole ? 1.f / l : 1.f;
         float *part = a.part + (long long)part_slot(blockIdx.x, g) * ROWS * (HD + 2);
         const int prow = WIDE ? w * 128 + t : t;
+        // A finished unit's rows go through the slot of its last value tile, whose products
+        // are done, so that whole lines are written: a warp's 32 rows, half of the columns
+        // at a time.
+        constexpr int NC = HD / 2, CPR = NC / 8;  // columns, chunks of a row
+        uint32_t stage, stage_parity;
+        value_slot(n - 1, stage, stage_parity);
+        stage = ring + stage * C::kTile + (tid >> 5) * (C::kTile / 8);
+        auto stage_at = [&](int r, int c) {
+            return stage + r * NC * 2 + ((c ^ (CPR == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+        };
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-            uint32_t y[32];
-            float o[32];
-            tmem_ld32(ta + c, y);
-            wait_ld();
+        for (int rd = WIDE ? 0 : w; rd < (WIDE ? 2 : w + 1); ++rd) {
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 32) {
+                const int col = rd * NC + c;
+                uint32_t y[32];
+                tmem_ld32(ta + col, y);
+                if (!WIDE) {
+                    wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]) * f0;
-            if (!WIDE && n > 1) {  // one tile: the second warpgroup had none
-                tmem_ld32(tb + c, y);
-                wait_ld();
+                    for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f0);
+                    if (n > 1) {  // one tile: the second warpgroup had none
+                        uint32_t z[32];
+                        tmem_ld32(tb + col, z);
+                        wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(y[e]), f1, o[e]);
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = __float_as_uint(fmaf(__uint_as_float(z[e]), f1, __uint_as_float(y[e])));
+                    }
+                } else {
+                    wait_ld();
+                }
+                if (poisoned) {
+                    float o[32];
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]);
+                    add_unbounded(a, g, place, col, o);
+                    for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(o[e]);
+                }
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack_bf16(__uint_as_float(y[8 * e + 2 * k]) * inv,
+                                             __uint_as_float(y[8 * e + 2 * k + 1]) * inv);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         stage_at(lane, c / 8 + e)),
+                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                     : "memory");
+                    }
+                } else if (row < rows) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(part + part_at<ROWS>(prow, col + 4 * e)) =
+                            make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                }
             }
-            if (poisoned) add_unbounded(a, g, place, c, o);
-            if (!has) continue;
             if (whole) {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * HD + c);
+                __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                        pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                        pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                        pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-            } else {
-                float4 *dst = reinterpret_cast<float4 *>(part + (long long)prow * HD + c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (int u = 0; u < CPR; ++u) {
+                    const int r = (u * 32 + lane) / CPR, c = (u * 32 + lane) % CPR;
+                    const int i = row - lane + r, tok = div_group(a, i);
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stage_at(r, c))
+                                 : "memory");
+                    const long long at =
+                        (long long)(g.req.row0 + tok) * a.Hq + g.h * a.G + (i - tok * a.G);
+                    if (i < rows)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * HD +
+                                                   rd * NC + c * 8) = v;
+                }
+                __syncwarp();
             }
         }
-        if (has && (WIDE || w == 0)) {
-            if (whole) {
-                if (a.lse) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
-            } else {
+        fence_before();
+        fence_async();
+        arrive(bar(s.b.staged));
+        if (row < rows && (WIDE || w == 0)) {
+            if (!whole) {
                 part[ROWS * HD + prow] = m;
                 part[ROWS * HD + ROWS + prow] = l;
+            } else if (a.lse) {
+                const int tok = div_group(a, row);
+                a.lse[(long long)(g.req.row0 + tok) * a.Hq + g.h * a.G + (row - tok * a.G)] =
+                    (m + log2f(l)) * 0.69314718055994531f;
             }
         }
         if (!WIDE) {  // both outputs have been read: either may be written again
-            fence_before();
             arrive(bar(s.b.joined));
             if (!wait(bar(s.b.joined), 1, &s.dead)) return;
             fence_after();
         }
-        base_pos += 2 * n;
+        const uint32_t pos = base_slot + 2 * n, rounds = pos / C::NS;
+        base_slot = pos - rounds * C::NS;
+        base_parity ^= rounds & 1;
         ++seg;
-        cur = ahead;
     }
+    any = seg > 0;  // stays false when a wait gave up
 }
 
 template <int HD, bool WIDE>
@@ -657,11 +824,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
             mbar_init(bar(s.b.p_ready[w]), 128);
-            mbar_init(bar(s.b.o_full[w]), 1);
             mbar_init(bar(s.b.q_ready[w]), WIDE ? 128 : 256);
             mbar_init(bar(s.b.clean[w]), WIDE ? 256 : 128);
         }
+        mbar_init(bar(s.b.o_full), 1);
         mbar_init(bar(s.b.joined), 256);
+        mbar_init(bar(s.b.staged), 256);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(bar(s.b.seg_full[i]), 1);
+            mbar_init(bar(s.b.seg_empty[i]), kSegReaders);
+        }
         mbar_init(bar(s.b.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s.dead = 0;
@@ -685,22 +857,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (warp < 8) {
         Segment g;
         bool any = false;
-        long long x_end = 0;
-        softmax_role<HD, WIDE>(L, s, qbuf, ring, cur, g, any, x_end, tm);
-        if (tid == 0) write_desc(L.a, blockIdx.x, g, any, x_end, s.plan.total, s.plan.workers);
-    } else {
-        if (warp == 8) {
-            uint32_t issued = 0;
-            load_role<HD, WIDE>(L, s, ring, cur, tid & 31, issued);
-            // Every copy has landed before the block ends (the roles waited for them
-            // unless one gave up).
-            for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
-                wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
-        } else if (tid == 9 * 32) {
-            mma_role<HD, WIDE>(L, s, qbuf, ring, cur, tm);
-            commit(bar(s.b.drain));
-            wait_parity(bar(s.b.drain), 0);
-        }
+        softmax_role<HD, WIDE>(L, s, qbuf, ring, g, any, tm);
+        // x1 is the line position after the last segment
+        if (tid == 0) write_desc(L.a, blockIdx.x, g, any, s.plan.x1, s.plan.total, s.plan.workers);
+    } else if (warp == 8) {
+        uint32_t issued = 0;
+        load_role<HD, WIDE>(L, s, ring, tid & 31, issued);
+        // Every copy has landed before the block ends (the roles waited for them
+        // unless one gave up).
+        for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
+            wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
+    } else if (tid == 9 * 32) {
+        mma_role<HD, WIDE>(L, s, qbuf, ring, tm);
+        commit(bar(s.b.drain));
+        wait_parity(bar(s.b.drain), 0);
+    } else if (tid == 10 * 32) {
+        segment_role<WIDE>(L.a, s, cur);
     }
     __syncwarp();
     fence_before();
