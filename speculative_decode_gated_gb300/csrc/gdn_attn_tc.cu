@@ -59,7 +59,7 @@ struct Cfg {
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], clean[2], joined, staged, drain;
+    unsigned long long s_full[2], p_half[2], p_ready[2], o_full, q_ready[2], clean[2], joined, staged, drain;
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -80,6 +80,11 @@ __device__ __forceinline__ uint32_t bar(const unsigned long long &b) { return sm
 
 __device__ __forceinline__ void arrive(uint32_t b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(b) : "memory");
+}
+// One arrival a warp, after all its threads' work.
+__device__ __forceinline__ void arrive_warp(uint32_t b) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(b);
 }
 __device__ __forceinline__ void arrive_expect(uint32_t b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(b), "r"(bytes)
@@ -102,6 +107,7 @@ __device__ __forceinline__ bool wait_one(uint32_t b, uint32_t parity, int *dead)
 }
 // The same by all 32 threads of a warp, with one answer.
 __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity, int *dead) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
     return __all_sync(0xffffffffu, wait_one(b, parity, dead));
 }
 
@@ -129,25 +135,39 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t n, bool b_mn_major) {
            ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+// The whole warp calls these with the same arguments, so that they stay in uniform
+// registers; the thread with `lead` set issues.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t lead;
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(lead));
+    return lead;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
         " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+        "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
         " mov.b64 db, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t b) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(b)
-                 : "memory");
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t b) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(b),
+        "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
@@ -188,6 +208,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two float32 at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -247,15 +289,8 @@ struct SegReader {
         ring.next();
         return g.r >= 0;
     }
-    __device__ __forceinline__ bool next_one(Shared &s, Segment &g) {  // by a lone thread
-        if (!wait_one(bar(s.b.seg_full[ring.slot]), ring.parity, &s.dead)) return false;
-        g = s.seg[ring.slot];
-        arrive(bar(s.b.seg_empty[ring.slot]));
-        ring.next();
-        return g.r >= 0;
-    }
 };
-constexpr int kSegReaders = 8 + 1 + 1;  // arrivals a slot: softmax warps, TMA, MMA
+constexpr int kSegReaders = 8 + 1 + 1;  // arrivals a slot: softmax warps, TMA, MMA warp
 
 // ---------------------------------------------------------------- the TMA warp
 
@@ -338,7 +373,7 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
     }
 }
 
-// ---------------------------------------------------------------- the MMA thread
+// ---------------------------------------------------------------- the MMA warp
 
 template <int HD, bool WIDE>
 __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
@@ -347,14 +382,16 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
     const AttnArgs &a = L.a;
     Ring<C::NS> at;
     SegReader segs;
+    const uint32_t lead = elect();
     uint32_t seg = 0, np0 = 0, np1 = 0, nc0 = 0, nc1 = 0, staged = 0;
     uint32_t held = 0;      // ring slot the softmax warpgroups stage their output in
     bool holding = false;
     Segment g;
+    tm = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t q_lo = desc_lo(qbuf, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, C::kBox);
     auto next_slot = [&](uint32_t &slot) -> bool {
         slot = at.slot;
-        const bool ok = wait_one(bar(s.b.full[at.slot]), at.parity, &s.dead);
+        const bool ok = wait(bar(s.b.full[at.slot]), at.parity, &s.dead);
         at.next();
         return ok;
     };
@@ -365,83 +402,92 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-            mma_ss(tm + w * 128, q + off, k + off, idesc(128, false), kk > 0);
+            mma_ss(lead, tm + w * 128, q + off, k + off, idesc(128, false), kk > 0);
         }
-        commit(bar(s.b.s_full[w]));
+        commit(lead, bar(s.b.s_full[w]));
     };
-    auto output = [&](int w, uint32_t slot, bool first) {
+    // The weights of keys 64 .. 127 are there first.
+    auto output = [&](int w, uint32_t slot, bool first, uint32_t parity) -> bool {
         const uint32_t v = v_lo + slot * (C::kTile >> 4);
         const uint32_t acc = first ? 0u : 1u;
+        if (!wait(bar(s.b.p_half[w]), parity, &s.dead)) return false;
         fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_ts(tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
-                   idesc(HD, true), kk > 0 ? 1u : acc);
+        for (int kk = kKT / 32; kk < kKT / 16; ++kk)
+            mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
+                   idesc(HD, true), kk > kKT / 32 ? 1u : acc);
+        if (!wait(bar(s.b.p_ready[w]), parity, &s.dead)) return false;
+        fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kKT / 32; ++kk)
+            mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
+                   idesc(HD, true), 1u);
+        return true;
     };
     // The slot of the last segment's last values goes back to the ring when the warpgroups
     // have written their output from it.
     auto give_back = [&]() -> bool {
         if (!holding) return true;
-        if (!wait_one(bar(s.b.staged), staged++ & 1, &s.dead)) return false;
-        arrive(bar(s.b.empty[held]));
+        if (!wait(bar(s.b.staged), staged++ & 1, &s.dead)) return false;
+        if (lead) arrive(bar(s.b.empty[held]));
+        __syncwarp();
         holding = false;
         return true;
     };
-    while (segs.next_one(s, g)) {
+    while (segs.next(s, g)) {
         uint32_t ks, vs = 0;
-        const int n = g.i1 - g.i0;
+        const int n = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
         if (!next_slot(ks)) return;
         if (WIDE) {
-            if (!wait_one(bar(s.b.q_ready[0]), seg & 1, &s.dead)) return;
+            if (!wait(bar(s.b.q_ready[0]), seg & 1, &s.dead)) return;
             scores(0, ks);
-            if (!wait_one(bar(s.b.q_ready[1]), seg & 1, &s.dead)) return;
+            if (!wait(bar(s.b.q_ready[1]), seg & 1, &s.dead)) return;
             scores(1, ks);
-            commit(bar(s.b.empty[ks]));
+            commit(lead, bar(s.b.empty[ks]));
         } else {
-            if (!wait_one(bar(s.b.q_ready[seg & 1]), (seg >> 1) & 1, &s.dead)) return;
+            if (!wait(bar(s.b.q_ready[seg & 1]), (seg >> 1) & 1, &s.dead)) return;
             scores(0, ks);
-            commit(bar(s.b.empty[ks]));
+            commit(lead, bar(s.b.empty[ks]));
             if (n > 1) {
                 if (!next_slot(ks)) return;
                 scores(1, ks);
-                commit(bar(s.b.empty[ks]));
+                commit(lead, bar(s.b.empty[ks]));
             }
         }
         if (!give_back()) return;
+        bool full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0));
         for (int i = 0; i < n; ++i) {
             if (!next_slot(vs)) return;
-            const bool full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i));
             if (WIDE) {
-                if (!full && !wait_one(bar(s.b.clean[0]), nc0++ & 1, &s.dead)) return;
-                if (!wait_one(bar(s.b.p_ready[0]), np0++ & 1, &s.dead)) return;
-                output(0, vs, i == 0);
+                if (!full && !wait(bar(s.b.clean[0]), nc0++ & 1, &s.dead)) return;
+                if (!output(0, vs, i == 0, np0++ & 1)) return;
                 if (i + 1 < n) {
                     if (!next_slot(ks)) return;
                     scores(0, ks);
                 }
-                if (!wait_one(bar(s.b.p_ready[1]), np1++ & 1, &s.dead)) return;
-                output(1, vs, i == 0);
+                full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i + 1));  // the next one
+                if (!output(1, vs, i == 0, np1++ & 1)) return;
                 if (i + 1 < n) {
-                    commit(bar(s.b.empty[vs]));
+                    commit(lead, bar(s.b.empty[vs]));
                     scores(1, ks);
-                    commit(bar(s.b.empty[ks]));
+                    commit(lead, bar(s.b.empty[ks]));
                 } else {  // both at once: the outputs are staged over the values
-                    commit(bar(s.b.o_full));
+                    commit(lead, bar(s.b.o_full));
                 }
             } else {
                 const int w = i & 1;
-                if (!full && !wait_one(bar(s.b.clean[w]), (w ? nc1++ : nc0++) & 1, &s.dead)) return;
-                if (!wait_one(bar(s.b.p_ready[w]), (w ? np1++ : np0++) & 1, &s.dead)) return;
-                output(w, vs, i < 2);
+                if (!full && !wait(bar(s.b.clean[w]), (w ? nc1++ : nc0++) & 1, &s.dead)) return;
+                if (!output(w, vs, i < 2, (w ? np1++ : np0++) & 1)) return;
                 if (i + 1 < n)
-                    commit(bar(s.b.empty[vs]));
+                    commit(lead, bar(s.b.empty[vs]));
                 else
-                    commit(bar(s.b.o_full));
+                    commit(lead, bar(s.b.o_full));
                 if (i + 2 < n) {
                     if (!next_slot(ks)) return;
                     scores(w, ks);
-                    commit(bar(s.b.empty[ks]));
+                    commit(lead, bar(s.b.empty[ks]));
                 }
+                full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i + 1));
             }
         }
         held = vs;
@@ -511,7 +557,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     auto queries_ready = [&](uint32_t seg) {
         asm volatile("cp.async.wait_all;\n" ::: "memory");
         fence_async();
-        arrive(bar(s.b.q_ready[WIDE ? w : (seg & 1)]));
+        arrive_warp(bar(s.b.q_ready[WIDE ? w : (seg & 1)]));
     };
 
     uint32_t seg = 0, n_s = 0;
@@ -599,7 +645,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                     }
                 }
                 fence_async();
-                arrive(bar(s.b.clean[WIDE ? 0 : w]));
+                arrive_warp(bar(s.b.clean[WIDE ? 0 : w]));
                 // place j0 + 32 q + e is bit e of mask[q]
                 const int hi = place - j0, lo = a.window ? hi - a.window : -1, sk = a.sinks - j0;
 #pragma unroll
@@ -619,13 +665,20 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 wait_ld();
                 if (!full) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (!(mask[half * 2 + e / 32] & (1u << (e & 31)))) x[e] = 0xff800000u;  // -inf
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t seen = mask[half * 2 + q];
+                        if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen & (1u << e))) x[32 * q + e] = 0xff800000u;  // -inf
+                    }
                 }
             };
             auto maximum = [&]() {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) top4[e & 3] = fmaxf(top4[e & 3], __uint_as_float(x[e]));
+                for (int e = 0; e < 64; e += 2)
+                    top4[(e >> 1) & 3] = max3(top4[(e >> 1) & 3], __uint_as_float(x[e]),
+                                              __uint_as_float(x[e + 1]));
             };
             scores(0);
             maximum();
@@ -650,25 +703,30 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 }
             }
             const float off = m == -INFINITY ? 0.f : -m;
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), off2 = make_float2(off, off);
+            float2 sum[2] = {};
             auto weights = [&](int half) {
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
-                    const float y0 = exp2_fast(fmaf(__uint_as_float(x[e]), a.scale_log2, off));
-                    const float y1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), a.scale_log2, off));
-                    sum4[e & 2] += y0;
-                    sum4[(e & 2) + 1] += y1;
-                    x[e / 2] = pack_bf16(y0, y1);
+                    float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                    scale2, off2);
+                    y.x = exp2_fast(y.x);
+                    y.y = exp2_fast(y.y);
+                    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+                    x[e / 2] = pack_bf16(y.x, y.y);
                 }
                 tmem_st32(ts + kP + half * 32, x);  // over scores that are not needed any more
             };
             weights(1);
-            scores(0);
-            weights(0);
-            l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             wait_st();
             fence_before();
-            arrive(bar(s.b.p_ready[w]));
+            arrive_warp(bar(s.b.p_half[w]));  // the products of the second half may begin
+            scores(0);
+            weights(0);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            wait_st();
+            fence_before();
+            arrive_warp(bar(s.b.p_ready[w]));
             if (q_pending) {
                 queries_ready(seg + 1);
                 q_pending = false;
@@ -688,7 +746,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             // Join: each warpgroup writes half of the columns of both outputs.
             s.m[w][t] = m;
             s.l[w][t] = l;
-            arrive(bar(s.b.joined));
+            arrive_warp(bar(s.b.joined));
             if (!wait(bar(s.b.joined), 0, &s.dead)) return;
             const float m0 = s.m[0][t], m1 = s.m[1][t];
             m = fmaxf(m0, m1);
@@ -782,7 +840,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         }
         fence_before();
         fence_async();
-        arrive(bar(s.b.staged));
+        arrive_warp(bar(s.b.staged));
         if (row < rows && (WIDE || w == 0)) {
             if (!whole) {
                 part[ROWS * HD + prow] = m;
@@ -794,7 +852,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             }
         }
         if (!WIDE) {  // both outputs have been read: either may be written again
-            arrive(bar(s.b.joined));
+            arrive_warp(bar(s.b.joined));
             if (!wait(bar(s.b.joined), 1, &s.dead)) return;
             fence_after();
         }
@@ -815,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     Shared &s = *reinterpret_cast<Shared *>(raw + C::kTiles);
     const uint32_t base = smem_addr(raw);
     const uint32_t qbuf = base, ring = base + 2 * C::kTile;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(bar(s.b.full[i]), 1);
@@ -823,13 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
-            mbar_init(bar(s.b.p_ready[w]), 128);
-            mbar_init(bar(s.b.q_ready[w]), WIDE ? 128 : 256);
-            mbar_init(bar(s.b.clean[w]), WIDE ? 256 : 128);
+            mbar_init(bar(s.b.p_half[w]), 4);
+            mbar_init(bar(s.b.p_ready[w]), 4);
+            mbar_init(bar(s.b.q_ready[w]), WIDE ? 4 : 8);
+            mbar_init(bar(s.b.clean[w]), WIDE ? 8 : 4);
         }
         mbar_init(bar(s.b.o_full), 1);
-        mbar_init(bar(s.b.joined), 256);
-        mbar_init(bar(s.b.staged), 256);
+        mbar_init(bar(s.b.joined), 8);
+        mbar_init(bar(s.b.staged), 8);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(bar(s.b.seg_full[i]), 1);
             mbar_init(bar(s.b.seg_empty[i]), kSegReaders);
@@ -867,9 +926,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // unless one gave up).
         for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
             wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
-    } else if (tid == 9 * 32) {
+    } else if (warp == 9) {
         mma_role<HD, WIDE>(L, s, qbuf, ring, tm);
-        commit(bar(s.b.drain));
+        commit(elect(), bar(s.b.drain));
         wait_parity(bar(s.b.drain), 0);
     } else if (tid == 10 * 32) {
         segment_role<WIDE>(L.a, s, cur);
