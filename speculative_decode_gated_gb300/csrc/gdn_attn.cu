@@ -20,6 +20,7 @@ constexpr int kRows = 16;   // query rows of a unit
 constexpr int kKeys = 32;   // places of a key tile
 constexpr int kThreads = 128;
 constexpr int kMinTiles = 2;
+constexpr int kExtra = 1;   // a unit's start and end, in tiles
 
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
@@ -60,10 +61,10 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
     constexpr int VE = 16 / (int)sizeof(T), VR = HD / VE;  // vectors of a row
     const int tid = threadIdx.x, c = blockIdx.x, P = gridDim.x;
     const int row = tid >> 3, sub = tid & 7;
-    Cursor cur = make_plan<kThreads, kRows, kKeys, kMinTiles>(a, c, P, &s.plan, c == 0);
+    Cursor cur = make_plan<kThreads, kRows, kKeys, kExtra, kMinTiles>(a, c, P, &s.plan, c == 0);
     Segment g;
     bool any = false;
-    while (next_segment<kRows, kKeys>(a, cur, g)) {
+    while (next_segment<kRows, kKeys, kExtra>(a, cur, g)) {
         any = true;
         __syncthreads();  // the previous segment's tiles are no longer read
         const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);

@@ -10,7 +10,9 @@
 // then those from the first row's window to the last row's own place.  All
 // units' tiles in order (request, query tile, key head, tile) form one line of
 // N tiles, and worker c of P takes tiles [c N / P, (c + 1) N / P): equal work
-// whatever the requests' lengths, which only the device knows.  A unit that
+// whatever the requests' lengths, which only the device knows.  A unit's start and
+// end take time too, so each has EXTRA places on the line before its tiles, in
+// which nothing is done.  A unit that
 // lies in one worker's range is finished there; one that spans several leaves
 // a partial (unnormalised sums, running maximum, total) per worker, joined by
 // combine_kernel in the order of the workers, so results do not depend on
@@ -151,8 +153,8 @@ struct Cursor {
 };
 
 // Every thread of the block calls it; ends with a barrier.  At least MIN_TILES
-// tiles to a worker: fewer, longer runs when there is little work.
-template <int NT, int ROWS, int KT, int MIN_TILES>
+// places of the line to a worker: fewer, longer runs when there is little work.
+template <int NT, int ROWS, int KT, int EXTRA, int MIN_TILES>
 __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, PlanScratch *s,
                                             bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,7 +175,7 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
             for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
                 const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
                 if (n == 0) break;
-                sum += (long long)n * a.Hkv;
+                sum += (long long)(n + EXTRA) * a.Hkv;
             }
         }
         e = rend;
@@ -223,7 +225,7 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
                 for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
                     const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
                     if (n == 0) break;
-                    const long long m = (long long)n * a.Hkv;
+                    const long long m = (long long)(n + EXTRA) * a.Hkv;
                     if (x0 < at + m) {
                         s->entry = (int)f;
                         s->off = x0 - at;
@@ -246,32 +248,40 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
     return cur;
 }
 
-// The next run of tiles of this worker; false when its range is done.
-template <int ROWS, int KT>
-__device__ __forceinline__ bool next_segment(const AttnArgs &a, Cursor &cur, Segment &g) {
-    if (cur.x >= cur.x1) return false;
-    for (; cur.r < a.B; ++cur.r, cur.qt = 0) {
-        g.req = load_request(a, cur.r, false);
-        if (!g.req.ok) continue;
-        g.span = tile_span<ROWS, KT>(a, g.req.T, g.req.ctx, cur.qt);
-        if (g.span.n) break;  // a query tile with rows; else the next request's first
+// The next run of tiles of this worker; false, with g as it was, when its range is done.
+template <int ROWS, int KT, int EXTRA>
+__device__ __forceinline__ bool next_segment(const AttnArgs &a, Cursor &cur, Segment &out) {
+    while (cur.x < cur.x1) {
+        Segment g;
+        for (; cur.r < a.B; ++cur.r, cur.qt = 0) {
+            g.req = load_request(a, cur.r, false);
+            if (!g.req.ok) continue;
+            g.span = tile_span<ROWS, KT>(a, g.req.T, g.req.ctx, cur.qt);
+            if (g.span.n) break;  // a query tile with rows; else the next request's first
+        }
+        if (cur.r >= a.B) return false;
+        const int n = g.span.n, m = n + EXTRA;
+        g.r = cur.r;
+        g.qt = cur.qt;
+        g.h = (int)((unsigned long long)cur.off < (1ull << 32) ? (unsigned)cur.off / (unsigned)m
+                                                               : cur.off / m);
+        const int p0 = (int)(cur.off - (long long)g.h * m);
+        const long long left = cur.x1 - cur.x;
+        const int len = left < m - p0 ? (int)left : m - p0;
+        g.i0 = max(p0 - EXTRA, 0);
+        g.i1 = max(p0 + len - EXTRA, 0);
+        cur.x += len;
+        cur.off += len;
+        if (cur.off >= (long long)m * a.Hkv) {
+            cur.off = 0;
+            ++cur.qt;
+        }
+        if (g.i1 > g.i0) {
+            out = g;
+            return true;
+        }
     }
-    if (cur.r >= a.B) return false;
-    const int n = g.span.n;
-    g.r = cur.r;
-    g.qt = cur.qt;
-    g.h = (int)(cur.off / n);
-    g.i0 = (int)(cur.off - (long long)g.h * n);
-    const long long left = cur.x1 - cur.x;
-    g.i1 = left < n - g.i0 ? g.i0 + (int)left : n;
-    const int len = g.i1 - g.i0;
-    cur.x += len;
-    cur.off += len;
-    if (cur.off >= (long long)n * a.Hkv) {
-        cur.off = 0;
-        ++cur.qt;
-    }
-    return true;
+    return false;
 }
 
 // The worker that holds tile g of the line of N tiles.

@@ -27,6 +27,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 16;
+constexpr int kExtra = 1;   // a unit's start and end, in tiles
 
 template <int HD>
 struct Cfg {
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     unsigned char *qs = smem + C::W * C::S * 2 * C::kTile + C::kJoin;
     const uint32_t ring = smem_addr(smem) + warp * C::S * 2 * C::kTile;
 
-    Cursor ahead = make_plan<C::NT, kRows, C::KT, 2>(a, c, P, &plan, c == 0);
+    Cursor ahead = make_plan<C::NT, kRows, C::KT, kExtra, 2>(a, c, P, &plan, c == 0);
     Cursor cur = ahead;
     Segment ga, g;  // the segment being copied, and the one being used
     int ia = 0;
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     int slot_in = 0, slot_out = 0;
     auto advance = [&]() {  // one more tile on its way (or an empty group)
         if (more && ia >= ga.i1) {
-            more = next_segment<kRows, C::KT>(a, ahead, ga);
+            more = next_segment<kRows, C::KT, kExtra>(a, ahead, ga);
             ia = ga.i0;
         }
         if (more) copy_tile<HD>(a, ga, ia++, warp, lane, ring + slot_in * 2 * C::kTile);
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     // Fragment coordinates: rows qr and qr + 8, columns 2 qc, 2 qc + 1 of 8.
     const int qr = lane >> 2, qc = lane & 3;
     bool any = false;
-    while (next_segment<kRows, C::KT>(a, cur, g)) {
+    while (next_segment<kRows, C::KT, kExtra>(a, cur, g)) {
         any = true;
         const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);
         const TileSpan sp = g.span;

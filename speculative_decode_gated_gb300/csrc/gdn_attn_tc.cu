@@ -45,6 +45,8 @@ namespace {
 constexpr int kKT = 128;       // places of a tile
 constexpr int kThreads = 352;  // two softmax warpgroups; the TMA, the MMA and the segment warp
 constexpr int kSegs = 4;       // segments known ahead
+// A unit's start and end, in tiles.
+constexpr int kExtraWide = 4, kExtraDrafts = 2;
 constexpr float kLazy = 8.f;
 constexpr uint32_t kP = 64;    // TMEM column of P_w within S_w: two weights a column
 
@@ -268,7 +270,7 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, Shared &s, Curso
     Ring<kSegs> ring;
     for (;;) {
         Segment g;
-        const bool more = next_segment<WIDE ? 256 : 128, kKT>(a, cur, g);
+        const bool more = next_segment<WIDE ? 256 : 128, kKT, WIDE ? kExtraWide : kExtraDrafts>(a, cur, g);
         if (!more) g.r = -1;
         if (!wait_one(bar(s.b.seg_empty[ring.slot]), ring.parity ^ 1, &s.dead)) return;
         s.seg[ring.slot] = g;
@@ -278,16 +280,21 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, Shared &s, Curso
     }
 }
 
-// A role's view of the segments: the next one, or false.  Warps take part whole.
+// A warp's view of the segments.
 struct SegReader {
     Ring<kSegs> ring;
-    __device__ __forceinline__ bool next(Shared &s, Segment &g) {
-        if (!wait(bar(s.b.seg_full[ring.slot]), ring.parity, &s.dead)) return false;
-        g = s.seg[ring.slot];
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) arrive(bar(s.b.seg_empty[ring.slot]));
+    // The next segment, in shared memory until it is released; NULL after the last.
+    __device__ __forceinline__ const Segment *peek(Shared &s) {
+        if (!wait(bar(s.b.seg_full[ring.slot]), ring.parity, &s.dead)) return nullptr;
+        return s.seg[ring.slot].r >= 0 ? &s.seg[ring.slot] : nullptr;
+    }
+    __device__ __forceinline__ bool next(Shared &s, Segment &g) {  // a copy
+        const Segment *p = peek(s);
+        if (!p) return false;
+        g = *p;
+        arrive_warp(bar(s.b.seg_empty[ring.slot]));
         ring.next();
-        return g.r >= 0;
+        return true;
     }
 };
 constexpr int kSegReaders = 8 + 1 + 1;  // arrivals a slot: softmax warps, TMA, MMA warp
@@ -523,7 +530,7 @@ __device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, 
 
 template <int HD, bool WIDE>
 __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
-                                             Segment &g, bool &any, uint32_t tm) {
+                                             uint32_t tm) {
     using C = Cfg<HD>;
     constexpr int ROWS = WIDE ? 256 : 128;
     constexpr int CR = HD / 8;  // 16-byte chunks of a row
@@ -562,15 +569,17 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
 
     uint32_t seg = 0, n_s = 0;
     uint32_t base_slot = 0, base_parity = 0;  // ring position of the segment's first tile
-    Segment gn;
-    bool more = segs.next(s, gn);
-    if (more) {
-        load_queries(gn, 0);
+    if (tid == 0) write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);  // nothing left unfinished yet
+    const Segment *ahead = segs.peek(s);
+    if (ahead) {
+        load_queries(*ahead, 0);
         queries_ready(0);
     }
-    while (more) {
-        g = gn;
-        more = segs.next(s, gn);
+    while (ahead) {
+        const Segment &g = *ahead;
+        const uint32_t seg_slot = segs.ring.slot;
+        segs.ring.next();
+        ahead = segs.peek(s);
         const int n = g.i1 - g.i0;
         const TileSpan sp = g.span;
         const int row = g.qt * ROWS + (WIDE ? w * 128 : 0) + t;
@@ -583,8 +592,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             parity = base_parity ^ (rounds & 1);
         };
         bool q_pending = false;
-        if (!WIDE && more) {  // the other buffer is free: the last segment is done with it
-            load_queries(gn, seg + 1);
+        if (!WIDE && ahead) {  // the other buffer is free: the last segment is done with it
+            load_queries(*ahead, seg + 1);
             q_pending = true;
         }
         float m = -INFINITY, l = 0.f;
@@ -594,8 +603,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             const bool full = tile_full(a, sp, j0);
             if (!wait(bar(s.b.s_full[w]), n_s++ & 1, &s.dead)) return;
             fence_after();
-            if (WIDE && i + 1 == n && more) {  // this warpgroup's queries are no longer read
-                load_queries(gn, seg + 1);
+            if (WIDE && i + 1 == n && ahead) {  // this warpgroup's queries are no longer read
+                load_queries(*ahead, seg + 1);
                 q_pending = true;
             }
             uint32_t x[64];
@@ -860,8 +869,11 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         base_slot = pos - rounds * C::NS;
         base_parity ^= rounds & 1;
         ++seg;
+        // The last segment ends where the worker's range does.
+        if (!ahead && tid == 0)
+            write_desc(a, blockIdx.x, g, !s.dead, s.plan.x1, s.plan.total, s.plan.workers);
+        arrive_warp(bar(s.b.seg_empty[seg_slot]));
     }
-    any = seg > 0;  // stays false when a wait gave up
 }
 
 template <int HD, bool WIDE>
@@ -908,17 +920,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Cursor cur = make_plan<kThreads, ROWS, kKT, 1>(L.a, blockIdx.x, gridDim.x, &s.plan,
+    Cursor cur = make_plan<kThreads, ROWS, kKT, WIDE ? kExtraWide : kExtraDrafts, 1>(L.a, blockIdx.x, gridDim.x, &s.plan,
                                                    blockIdx.x == 0);
     fence_after();
     const uint32_t tm = *(volatile uint32_t *)&s.tmem;
 
     if (warp < 8) {
-        Segment g;
-        bool any = false;
-        softmax_role<HD, WIDE>(L, s, qbuf, ring, g, any, tm);
-        // x1 is the line position after the last segment
-        if (tid == 0) write_desc(L.a, blockIdx.x, g, any, s.plan.x1, s.plan.total, s.plan.workers);
+        softmax_role<HD, WIDE>(L, s, qbuf, ring, tm);
     } else if (warp == 8) {
         uint32_t issued = 0;
         load_role<HD, WIDE>(L, s, ring, tid & 31, issued);
