@@ -19,6 +19,7 @@ namespace {
 constexpr int kRows = 16;   // query rows of a unit
 constexpr int kKeys = 32;   // places of a key tile
 constexpr int kThreads = 128;
+constexpr int kAlign = 16;  // pages begin at multiples of it
 constexpr int kMinTiles = 2;
 constexpr int kExtra = 1;   // a unit's start and end, in tiles
 
@@ -61,10 +62,10 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
     constexpr int VE = 16 / (int)sizeof(T), VR = HD / VE;  // vectors of a row
     const int tid = threadIdx.x, c = blockIdx.x, P = gridDim.x;
     const int row = tid >> 3, sub = tid & 7;
-    Cursor cur = make_plan<kThreads, kRows, kKeys, kExtra, kMinTiles>(a, c, P, &s.plan, c == 0);
+    Cursor cur = make_plan<kThreads, kRows, kKeys, kExtra, kMinTiles>(a, c, P, kAlign, &s.plan, c == 0);
     Segment g;
     bool any = false;
-    while (next_segment<kRows, kKeys, kExtra>(a, cur, g)) {
+    while (next_segment<kRows, kKeys, kExtra>(a, kAlign, cur, g)) {
         any = true;
         __syncthreads();  // the previous segment's tiles are no longer read
         const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);
@@ -79,15 +80,16 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
             }
             put_vec<T>(&s.q[ri][e], w);
         }
-        const int place = g.req.ctx + (g.qt * kRows + row) / a.G;  // of this thread's row
+        // this thread's row's own place, as numbered in the span
+        const int own = g.req.ctx + (g.qt * kRows + row) / a.G - g.span.shift;
         float m = -INFINITY, l = 0.f, o[HD / 8] = {};
         for (int i = g.i0; i < g.i1; ++i) {
-            const int j0 = tile_place<kKeys>(g.span, i);
+            const int v0 = i * kKeys;
             __syncthreads();
             for (int x = tid; x < kKeys * VR; x += kThreads) {
-                const int kj = x / VR, e = x % VR * VE, j = j0 + kj;
+                const int kj = x / VR, e = x % VR * VE, j = place_of(g.span, v0 + kj);
                 uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
-                if (unit_sees(a, g.span, j)) {
+                if (some_see(a, g.span, v0 + kj, v0 + kj)) {
                     const int page =
                         a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
                     if (page >= 0 && page < a.n_pages) {
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
             bool seen[kKeys / 8];
 #pragma unroll
             for (int u = 0; u < kKeys / 8; ++u) {
-                seen[u] = row < rows && row_sees(a, place, j0 + sub + 8 * u);
+                seen[u] = row < rows && row_sees(a, g.span, own, v0 + sub + 8 * u);
                 x[u] = seen[u] ? x[u] * a.scale_log2 : -INFINITY;
                 top = fmaxf(top, x[u]);
             }

@@ -5,9 +5,10 @@
 // Work.  A unit is (request r, query tile qt, key head h): ROWS query rows,
 // row i of the tile being (token t, head g of the group) with qt * ROWS + i =
 // t * G + g, so that every key and value read serves all G query heads that
-// share it.  A unit's key tiles (KT places each) are those that hold a place
-// some row of it sees: under a window the tiles of the first `sinks` places,
-// then those from the first row's window to the last row's own place.  All
+// share it.  A unit's key tiles (KT places each) cover the places that some row
+// of it sees, without a gap: under a window the first `sinks` places (rounded up
+// to ALIGN of them), then those from the first row's window (rounded down) to the last
+// row's own place.  All
 // units' tiles in order (request, query tile, key head, tile) form one line of
 // N tiles, and worker c of P takes tiles [c N / P, (c + 1) N / P): equal work
 // whatever the requests' lengths, which only the device knows.  A unit's start and
@@ -83,49 +84,58 @@ __device__ __forceinline__ AttnReq load_request(const AttnArgs &a, int r, bool r
     return q;
 }
 
-// Key tiles of query tile qt of a request.
+// The places that query tile qt of a request sees, numbered without a gap: number v is
+// place v below `first`, place v + shift from there on (no window, or one that reaches
+// the sinks: shift = 0).  The rows' own places and the sinks are in these numbers too.
 struct TileSpan {
-    int n;         // tiles, 0 when the query tile has no rows
-    int ns;        // of them at the sinks (tiles 0 .. ns - 1 of the cache)
-    int lo;        // the next one, and those after it, are cache tiles lo, lo + 1, ...
-    int pmin, pmax;  // places of the first and the last row
+    int n;             // tiles of KT numbers, 0 when the query tile has no rows
+    int first, shift;
+    int pmin, pmax;    // of the first and the last row
+    int sinks;
 };
 
+// align: a power of two that divides KT and the page size (or is divided by it).
 template <int ROWS, int KT>
-__device__ __forceinline__ TileSpan tile_span(const AttnArgs &a, int T, int ctx, int qt) {
+__device__ __forceinline__ TileSpan tile_span(const AttnArgs &a, int T, int ctx, int qt, int align) {
     TileSpan s;
     const int first = qt * ROWS, rows = T * a.G;  // below 2^31: checked on the host
     if (first >= rows) {
-        s.n = s.ns = s.lo = s.pmin = s.pmax = 0;
+        s.n = s.first = s.shift = s.pmin = s.pmax = s.sinks = 0;
         return s;
     }
     const int last = min(ROWS, rows - first) + first - 1;
-    s.pmin = ctx + div_group(a, first);
-    s.pmax = ctx + div_group(a, last);
-    s.lo = s.ns = 0;
+    const int pmin = ctx + div_group(a, first), pmax = ctx + div_group(a, last);
+    s.first = s.shift = 0;
     if (a.window) {
-        const int w = s.pmin - a.window + 1;
-        s.lo = w > 0 ? w / KT : 0;
-        const int st = a.sinks / KT + (a.sinks % KT != 0);
-        s.ns = st < s.lo ? st : s.lo;
+        const int lo = max(pmin - a.window + 1, 0) & -align;
+        const int keep = (min(a.sinks, lo) + align - 1) & -align;
+        if (keep < lo) {
+            s.first = keep;
+            s.shift = lo - keep;
+        }
     }
-    s.n = s.ns + s.pmax / KT + 1 - s.lo;
+    s.pmin = pmin - s.shift;
+    s.pmax = pmax - s.shift;
+    s.sinks = a.sinks;
+    s.n = s.pmax / KT + 1;
     return s;
 }
 
-// Place of the first key of tile i of a unit.
-template <int KT>
-__device__ __forceinline__ int tile_place(const TileSpan &s, int i) {
-    return (i < s.ns ? i : s.lo + i - s.ns) * KT;
+__device__ __forceinline__ int place_of(const TileSpan &s, int v) {
+    return v + (v >= s.first ? s.shift : 0);
 }
 
-__device__ __forceinline__ bool row_sees(const AttnArgs &a, int p, int j) {
-    return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+// Whether the row whose own place is number p sees number v.
+__device__ __forceinline__ bool row_sees(const AttnArgs &a, const TileSpan &s, int p, int v) {
+    return v <= p && (a.window == 0 || v > p - a.window || v < s.sinks);
 }
 
-// Whether some row of the unit sees place j: no other place is read.
-__device__ __forceinline__ bool unit_sees(const AttnArgs &a, const TileSpan &s, int j) {
-    return j <= s.pmax && (a.window == 0 || j > s.pmin - a.window || j < a.sinks);
+// Whether some row sees some number of [v0, v1], or every row all of them.
+__device__ __forceinline__ bool some_see(const AttnArgs &a, const TileSpan &s, int v0, int v1) {
+    return v0 <= s.pmax && (a.window == 0 || v1 > s.pmin - a.window || v0 < s.sinks);
+}
+__device__ __forceinline__ bool all_see(const AttnArgs &a, const TileSpan &s, int v0, int v1) {
+    return v1 <= s.pmin && (a.window == 0 || v0 > s.pmax - a.window || v1 < s.sinks);
 }
 
 // A worker's current run of tiles [i0, i1) of one unit.
@@ -155,8 +165,8 @@ struct Cursor {
 // Every thread of the block calls it; ends with a barrier.  At least MIN_TILES
 // places of the line to a worker: fewer, longer runs when there is little work.
 template <int NT, int ROWS, int KT, int EXTRA, int MIN_TILES>
-__device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, PlanScratch *s,
-                                            bool report) {
+__device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, int align,
+                                            PlanScratch *s, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nqm = a.max_T ? (a.max_T * a.G + ROWS - 1) / ROWS : 1;
     const unsigned E = (unsigned)a.B * nqm;  // below 2^31: checked on the host
@@ -173,7 +183,7 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
         const AttnReq q = load_request(a, r, report && qt == 0);
         if (q.ok) {
             for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
-                const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
+                const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt, align).n;
                 if (n == 0) break;
                 sum += (long long)(n + EXTRA) * a.Hkv;
             }
@@ -223,7 +233,7 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
             const AttnReq q = load_request(a, r, false);
             if (q.ok) {
                 for (unsigned f = e; f < e1 && f < rend; ++f, ++qt) {
-                    const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt).n;
+                    const int n = tile_span<ROWS, KT>(a, q.T, q.ctx, qt, align).n;
                     if (n == 0) break;
                     const long long m = (long long)(n + EXTRA) * a.Hkv;
                     if (x0 < at + m) {
@@ -250,13 +260,14 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, Pla
 
 // The next run of tiles of this worker; false, with g as it was, when its range is done.
 template <int ROWS, int KT, int EXTRA>
-__device__ __forceinline__ bool next_segment(const AttnArgs &a, Cursor &cur, Segment &out) {
+__device__ __forceinline__ bool next_segment(const AttnArgs &a, int align, Cursor &cur,
+                                             Segment &out) {
     while (cur.x < cur.x1) {
         Segment g;
         for (; cur.r < a.B; ++cur.r, cur.qt = 0) {
             g.req = load_request(a, cur.r, false);
             if (!g.req.ok) continue;
-            g.span = tile_span<ROWS, KT>(a, g.req.T, g.req.ctx, cur.qt);
+            g.span = tile_span<ROWS, KT>(a, g.req.T, g.req.ctx, cur.qt, align);
             if (g.span.n) break;  // a query tile with rows; else the next request's first
         }
         if (cur.r >= a.B) return false;

@@ -27,6 +27,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 16;
+constexpr int kAlign = 16;  // a warp's places: within one page
 constexpr int kExtra = 1;   // a unit's start and end, in tiles
 
 template <int HD>
@@ -103,11 +104,10 @@ template <int HD>
 __device__ __forceinline__ void copy_tile(const AttnArgs &a, const Segment &g, int i, int warp,
                                           int lane, uint32_t kdst) {
     using C = Cfg<HD>;
-    const int j0 = tile_place<C::KT>(g.span, i) + warp * 16;
+    const int v0 = i * C::KT + warp * 16;
     const TileSpan &sp = g.span;
-    const bool needed =
-        j0 <= sp.pmax && (a.window == 0 || j0 + 15 > sp.pmin - a.window || j0 < a.sinks);
-    if (!needed) return;
+    if (!some_see(a, sp, v0, v0 + 15)) return;
+    const int j0 = place_of(sp, v0);
     const int page = a.page_table[(long long)g.r * a.max_pages + (j0 >> a.page_shift)];
     const bool page_ok = page >= 0 && page < a.n_pages;
     if (!page_ok && lane == 0 && a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
@@ -122,7 +122,7 @@ __device__ __forceinline__ void copy_tile(const AttnArgs &a, const Segment &g, i
     for (int u = 0; u < CR / 2; ++u) {
         const int x = u * 32 + lane, r = x / CR, c = x % CR;
         // a place that no row sees may hold anything: it is zeros here
-        const bool keep = page_ok && unit_sees(a, sp, j0 + r);
+        const bool keep = page_ok && some_see(a, sp, v0 + r, v0 + r);
         copy16(kdst + chunk_at<HD>(r, c), kp + (keep ? x * 16 : 0), keep);
         copy16(kdst + C::kTile + chunk_at<HD>(r, c), vp + (keep ? x * 16 : 0), keep);
     }
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     unsigned char *qs = smem + C::W * C::S * 2 * C::kTile + C::kJoin;
     const uint32_t ring = smem_addr(smem) + warp * C::S * 2 * C::kTile;
 
-    Cursor ahead = make_plan<C::NT, kRows, C::KT, kExtra, 2>(a, c, P, &plan, c == 0);
+    Cursor ahead = make_plan<C::NT, kRows, C::KT, kExtra, 2>(a, c, P, kAlign, &plan, c == 0);
     Cursor cur = ahead;
     Segment ga, g;  // the segment being copied, and the one being used
     int ia = 0;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     int slot_in = 0, slot_out = 0;
     auto advance = [&]() {  // one more tile on its way (or an empty group)
         if (more && ia >= ga.i1) {
-            more = next_segment<kRows, C::KT, kExtra>(a, ahead, ga);
+            more = next_segment<kRows, C::KT, kExtra>(a, kAlign, ahead, ga);
             ia = ga.i0;
         }
         if (more) copy_tile<HD>(a, ga, ia++, warp, lane, ring + slot_in * 2 * C::kTile);
@@ -164,16 +164,16 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     // Fragment coordinates: rows qr and qr + 8, columns 2 qc, 2 qc + 1 of 8.
     const int qr = lane >> 2, qc = lane & 3;
     bool any = false;
-    while (next_segment<kRows, C::KT, kExtra>(a, cur, g)) {
+    while (next_segment<kRows, C::KT, kExtra>(a, kAlign, cur, g)) {
         any = true;
         const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);
         const TileSpan sp = g.span;
-        int place[2];
+        int own[2];  // the rows' own places, as numbered in the span
         const __nv_bfloat16 *qrow[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = g.qt * kRows + qr + 8 * e, t = div_group(a, i);
-            place[e] = g.req.ctx + t;
+            own[e] = g.req.ctx + t - sp.shift;
             qrow[e] = static_cast<const __nv_bfloat16 *>(a.q) + (g.req.row0 + t) * a.q_stride +
                       (g.h * a.G + i - t * a.G) * HD;
         }
@@ -213,9 +213,8 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
             advance();
             const uint32_t kt = ring + slot_out * 2 * C::kTile, vt = kt + C::kTile;
             slot_out = slot_out + 1 == C::S ? 0 : slot_out + 1;
-            const int j0 = tile_place<C::KT>(sp, i) + warp * 16;
-            if (!(j0 <= sp.pmax && (a.window == 0 || j0 + 15 > sp.pmin - a.window || j0 < a.sinks)))
-                continue;
+            const int v0 = i * C::KT + warp * 16;
+            if (!some_see(a, sp, v0, v0 + 15)) continue;
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
@@ -232,14 +231,13 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                 }
             }
             // Every row sees all 16 places, or some are hidden from some rows.
-            const bool full = j0 + 15 <= sp.pmin &&
-                              (a.window == 0 || j0 > sp.pmax - a.window || j0 + 15 < a.sinks);
+            const bool full = all_see(a, sp, v0, v0 + 15);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[n][e] *= a.scale_log2;
-                    if (!full && !row_sees(a, place[e >> 1], j0 + n * 8 + qc * 2 + (e & 1)))
+                    if (!full && !row_sees(a, sp, own[e >> 1], v0 + n * 8 + qc * 2 + (e & 1)))
                         s[n][e] = -INFINITY;
                 }
             float mn[2];

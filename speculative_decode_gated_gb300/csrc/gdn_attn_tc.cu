@@ -26,8 +26,8 @@
 //
 // Places that no row sees, and values that are not finite where some rows must
 // not see them, would still reach the output as 0 * NaN.  In the tiles where
-// any row's mask hides something (the ends of a unit) the warpgroups therefore
-// clear them from the value tile first; the rows that do see such a value get it
+// any row's mask hides something (the ends of a unit) a warp therefore clears them
+// from the value tile first; the rows that do see such a value get it
 // added at the end (add_unbounded).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -43,7 +43,7 @@ namespace gdn {
 namespace {
 
 constexpr int kKT = 128;       // places of a tile
-constexpr int kThreads = 352;  // two softmax warpgroups; the TMA, the MMA and the segment warp
+constexpr int kThreads = 384;  // two softmax warpgroups; the TMA, MMA, segment and clearing warps
 constexpr int kSegs = 4;       // segments known ahead
 // A unit's start and end, in tiles.
 constexpr int kExtraWide = 4, kExtraDrafts = 2;
@@ -59,9 +59,11 @@ struct Cfg {
     static constexpr uint32_t kO = 256;            // TMEM column of O_0 (S_0 at 0, S_1 at 128)
 };
 
+constexpr int kCleans = 8;  // value tiles between the warp that clears them and their products
+
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_half[2], p_ready[2], o_full, q_ready[2], clean[2], joined, staged, drain;
+    unsigned long long s_full[2], p_half[2], p_ready[2], o_full, q_ready[2], clean[kCleans], joined, staged, drain;
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -238,11 +240,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Every row of the unit sees all places [j0, j0 + 128).
-__device__ __forceinline__ bool tile_full(const AttnArgs &a, const TileSpan &s, int j0) {
-    return j0 + kKT - 1 <= s.pmin &&
-           (a.window == 0 || j0 > s.pmax - a.window || j0 + kKT - 1 < a.sinks);
-}
+// Places of a TMA box: a page, or a tile's worth of one.
+__device__ __forceinline__ int box_rows(const AttnArgs &a) { return min(1 << a.page_shift, kKT); }
 
 struct Launch {
     AttnArgs a;
@@ -270,7 +269,8 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, Shared &s, Curso
     Ring<kSegs> ring;
     for (;;) {
         Segment g;
-        const bool more = next_segment<WIDE ? 256 : 128, kKT, WIDE ? kExtraWide : kExtraDrafts>(a, cur, g);
+        const bool more = next_segment<WIDE ? 256 : 128, kKT, WIDE ? kExtraWide : kExtraDrafts>(
+            a, box_rows(a), cur, g);
         if (!more) g.r = -1;
         if (!wait_one(bar(s.b.seg_empty[ring.slot]), ring.parity ^ 1, &s.dead)) return;
         s.seg[ring.slot] = g;
@@ -297,7 +297,7 @@ struct SegReader {
         return true;
     }
 };
-constexpr int kSegReaders = 8 + 1 + 1;  // arrivals a slot: softmax warps, TMA, MMA warp
+constexpr int kSegReaders = 8 + 1 + 1 + 1;  // arrivals a slot: softmax, TMA, MMA, clearing warps
 
 // ---------------------------------------------------------------- the TMA warp
 
@@ -306,7 +306,7 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
                                           uint32_t &issued) {
     using C = Cfg<HD>;
     const AttnArgs &a = L.a;
-    const int rows_box = min(1 << a.page_shift, kKT);  // places of a TMA box
+    const int rows_box = box_rows(a);
     const int boxes = kKT / rows_box;
     Ring<C::NS> at;
     SegReader segs;
@@ -314,12 +314,9 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
     // This lane's page of tile i of a segment: its row and number, or n_pages (nothing
     // needed, or no page).
     auto page_of = [&](const Segment &q, int i, int &row) -> int {
-        const int j = tile_place<kKT>(q.span, i) + lane * rows_box;
+        const int v = i * kKT + lane * rows_box, j = place_of(q.span, v);
         row = j & ((1 << a.page_shift) - 1);
-        const TileSpan &sp = q.span;
-        if (lane >= boxes || j > sp.pmax ||
-            !(a.window == 0 || j + rows_box - 1 > sp.pmin - a.window || j < a.sinks))
-            return (int)a.n_pages;
+        if (lane >= boxes || !some_see(a, q.span, v, v + rows_box - 1)) return (int)a.n_pages;
         const int page = a.page_table[(long long)q.r * a.max_pages + (j >> a.page_shift)];
         if (page >= 0 && page < a.n_pages) return page;
         if (a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
@@ -383,14 +380,14 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
 // ---------------------------------------------------------------- the MMA warp
 
 template <int HD, bool WIDE>
-__device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
+__device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring,
                                          uint32_t tm) {
     using C = Cfg<HD>;
-    const AttnArgs &a = L.a;
     Ring<C::NS> at;
     SegReader segs;
     const uint32_t lead = elect();
-    uint32_t seg = 0, np0 = 0, np1 = 0, nc0 = 0, nc1 = 0, staged = 0;
+    uint32_t seg = 0, np0 = 0, np1 = 0, staged = 0;
+    Ring<kCleans> clean;
     uint32_t held = 0;      // ring slot the softmax warpgroups stage their output in
     bool holding = false;
     Segment g;
@@ -400,6 +397,13 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
         slot = at.slot;
         const bool ok = wait(bar(s.b.full[at.slot]), at.parity, &s.dead);
         at.next();
+        return ok;
+    };
+    auto next_values = [&](uint32_t &slot) -> bool {  // there, and cleared of what must not be seen
+        slot = at.slot;
+        at.next();
+        const bool ok = wait(bar(s.b.clean[clean.slot]), clean.parity, &s.dead);
+        clean.next();
         return ok;
     };
     auto scores = [&](int w, uint32_t slot) {
@@ -462,17 +466,14 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
             }
         }
         if (!give_back()) return;
-        bool full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0));
         for (int i = 0; i < n; ++i) {
-            if (!next_slot(vs)) return;
+            if (!next_values(vs)) return;
             if (WIDE) {
-                if (!full && !wait(bar(s.b.clean[0]), nc0++ & 1, &s.dead)) return;
                 if (!output(0, vs, i == 0, np0++ & 1)) return;
                 if (i + 1 < n) {
                     if (!next_slot(ks)) return;
                     scores(0, ks);
                 }
-                full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i + 1));  // the next one
                 if (!output(1, vs, i == 0, np1++ & 1)) return;
                 if (i + 1 < n) {
                     commit(lead, bar(s.b.empty[vs]));
@@ -483,7 +484,6 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
                 }
             } else {
                 const int w = i & 1;
-                if (!full && !wait(bar(s.b.clean[w]), (w ? nc1++ : nc0++) & 1, &s.dead)) return;
                 if (!output(w, vs, i < 2, (w ? np1++ : np0++) & 1)) return;
                 if (i + 1 < n)
                     commit(lead, bar(s.b.empty[vs]));
@@ -494,7 +494,6 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
                     scores(w, ks);
                     commit(lead, bar(s.b.empty[ks]));
                 }
-                full = tile_full(a, g.span, tile_place<kKT>(g.span, g.i0 + i + 1));
             }
         }
         held = vs;
@@ -503,26 +502,111 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, uint32_t qb
     }
 }
 
+// ---------------------------------------------------------------- the clearing warp
+
+// Hands each value tile on to its products.  It takes part in the release of every ring
+// slot, keys too: a wait on a barrier's parity is only right for one that has seen
+// the phase before, so no slot may come round twice without it.  In value tiles that hold places hidden from some
+// row, it first clears the places that no row sees, and the elements that are not finite
+// where only some rows see them.
+template <int HD, bool WIDE>
+__device__ __forceinline__ void clear_role(const Launch &L, Shared &s, uint32_t ring, int lane) {
+    using C = Cfg<HD>;
+    constexpr int CR = HD / 8;  // 16-byte chunks of a row
+    const AttnArgs &a = L.a;
+    Ring<C::NS> at;
+    Ring<kCleans> clean;
+    SegReader segs;
+    uint32_t seg = 0;
+    Segment g;
+    while (segs.next(s, g)) {
+        const int n = g.i1 - g.i0;
+        auto keys = [&]() -> bool {
+            if (!wait(bar(s.b.full[at.slot]), at.parity, &s.dead)) return false;
+            arrive_warp(bar(s.b.empty[at.slot]));
+            at.next();
+            return true;
+        };
+        if (!keys()) return;
+        if (!WIDE && n > 1 && !keys()) return;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            if (!wait(bar(s.b.full[at.slot]), at.parity, &s.dead)) return;
+            const int v0 = (g.i0 + i) * kKT;
+            if (!all_see(a, g.span, v0, v0 + kKT - 1)) {
+                const uint32_t vt = ring + at.slot * C::kTile;
+#pragma unroll 1
+                for (int r = lane; r < kKT; r += 32) {
+                    const int v = v0 + r;
+                    if (all_see(a, g.span, v, v)) continue;
+                    auto chunk = [&](int c) {
+                        return vt + (c >> 3) * C::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    };
+                    if (!some_see(a, g.span, v, v)) {
+#pragma unroll
+                        for (int c = 0; c < CR; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(c)),
+                                         "r"(0)
+                                         : "memory");
+                        continue;
+                    }
+                    // Not finite: the exponent is all ones.
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int c = 0; c < CR; ++c) {
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(chunk(c))
+                                     : "memory");
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) odd |= (x[e] & 0x7F807F80u) + 0x00800080u;
+                    }
+                    if (odd & 0x80008000u) {
+                        s.poison[seg & 3] = (int)seg;
+#pragma unroll 1
+                        for (int c = 0; c < CR * 4; ++c) {
+                            uint32_t x;
+                            const uint32_t to = chunk(c >> 2) + (c & 3) * 4;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(to) : "memory");
+                            if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                            if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
+                        }
+                    }
+                }
+                fence_async();
+            }
+            arrive_warp(bar(s.b.clean[clean.slot]));
+            arrive_warp(bar(s.b.empty[at.slot]));
+            clean.next();
+            at.next();
+            if (i + (WIDE ? 1 : 2) < n && !keys()) return;
+        }
+        ++seg;
+    }
+}
+
 // ---------------------------------------------------------------- the softmax warpgroups
 
 // Adds the values that are not finite, at the places of the segment's masked
-// tiles that the row at `place` sees, to output columns [col, col + 32).
-__device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, int place, int col,
+// tiles that the row at number `own` sees, to output columns [col, col + 32).
+__device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, int own, int col,
                                            float *o) {
     for (int i = g.i0; i < g.i1; ++i) {
-        const int j0 = tile_place<kKT>(g.span, i);
-        if (tile_full(a, g.span, j0)) continue;
-        for (int j = j0; j < j0 + kKT; ++j) {
-            if (!unit_sees(a, g.span, j) || !row_sees(a, place, j)) continue;
+        if (all_see(a, g.span, i * kKT, i * kKT + kKT - 1)) continue;
+        for (int v = i * kKT; v < (i + 1) * kKT; ++v) {
+            if (!some_see(a, g.span, v, v) || all_see(a, g.span, v, v) || !row_sees(a, g.span, own, v))
+                continue;
+            const int j = place_of(g.span, v);
             const int page = a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
             if (page < 0 || page >= a.n_pages) continue;
-            const __nv_bfloat16 *v =
+            const __nv_bfloat16 *x =
                 static_cast<const __nv_bfloat16 *>(a.v) + (long long)page * a.page_stride +
                 (((long long)g.h << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * a.hd + col;
-#pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float x = __bfloat162float(v[e]);
-                if (!isfinite(x)) o[e] += x;
+                const float f = __bfloat162float(x[e]);
+                if (!isfinite(f)) o[e] += f;
             }
         }
     }
@@ -568,7 +652,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     };
 
     uint32_t seg = 0, n_s = 0;
-    uint32_t base_slot = 0, base_parity = 0;  // ring position of the segment's first tile
+    uint32_t base_slot = 0;  // ring slot of the segment's first tile
     if (tid == 0) write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);  // nothing left unfinished yet
     const Segment *ahead = segs.peek(s);
     if (ahead) {
@@ -583,14 +667,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         const int n = g.i1 - g.i0;
         const TileSpan sp = g.span;
         const int row = g.qt * ROWS + (WIDE ? w * 128 : 0) + t;
-        const int place = g.req.ctx + div_group(a, row);
-        // Ring slot and parity of the values of the segment's tile i.
-        auto value_slot = [&](int i, uint32_t &slot, uint32_t &parity) {
-            uint32_t pos = base_slot + (WIDE ? 2 * i + 1 : min(n, i + 2) + i);
-            const uint32_t rounds = pos / C::NS;
-            slot = pos - rounds * C::NS;
-            parity = base_parity ^ (rounds & 1);
-        };
+        const int own = g.req.ctx + div_group(a, row) - sp.shift;  // its place, as numbered in the span
         bool q_pending = false;
         if (!WIDE && ahead) {  // the other buffer is free: the last segment is done with it
             load_queries(*ahead, seg + 1);
@@ -599,8 +676,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
         for (int i = WIDE ? 0 : w; i < n; i += WIDE ? 1 : 2) {
-            const int j0 = tile_place<kKT>(sp, g.i0 + i);
-            const bool full = tile_full(a, sp, j0);
+            const int v0 = (g.i0 + i) * kKT;
+            const bool full = all_see(a, sp, v0, v0 + kKT - 1);
             if (!wait(bar(s.b.s_full[w]), n_s++ & 1, &s.dead)) return;
             fence_after();
             if (WIDE && i + 1 == n && ahead) {  // this warpgroup's queries are no longer read
@@ -610,53 +687,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             uint32_t x[64];
             uint32_t mask[4];  // of the tile's places, those that the row sees
             if (!full) {
-                // Clear what must not be seen from the value tile: this thread's place (half
-                // a place) of it.
-                uint32_t slot, parity;
-                value_slot(i, slot, parity);
-                const uint32_t vt = ring + slot * C::kTile;
-                if (!wait(bar(s.b.full[slot]), parity, &s.dead)) return;
-                constexpr int NC = WIDE ? CR / 2 : CR;
-                const int r = WIDE ? w * 64 + (t >> 1) : t;
-                const int c0 = WIDE ? (t & 1) * NC : 0, j = j0 + r;
-                auto chunk = [&](int c) {
-                    return vt + ((c0 + c) >> 3) * C::kBox + r * 128 + ((((c0 + c) & 7) ^ (r & 7)) << 4);
-                };
-                if (!unit_sees(a, sp, j)) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(c)), "r"(0)
-                                     : "memory");
-                } else if (!(j <= sp.pmin && (a.window == 0 || j > sp.pmax - a.window || j < a.sinks))) {
-                    // Seen by some rows.  An element is not finite if its exponent is all ones.
-                    uint32_t odd = 0;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        uint32_t v[4];
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                     : "r"(chunk(c))
-                                     : "memory");
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7F807F80u) + 0x00800080u;
-                    }
-                    if (odd & 0x80008000u) {
-                        s.poison[seg & 3] = (int)seg;
-#pragma unroll 1
-                        for (int c = 0; c < NC * 4; ++c) {
-                            uint32_t v;
-                            const uint32_t at = chunk(c >> 2) + (c & 3) * 4;
-                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-                            if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
-                            if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-                        }
-                    }
-                }
-                fence_async();
-                arrive_warp(bar(s.b.clean[WIDE ? 0 : w]));
-                // place j0 + 32 q + e is bit e of mask[q]
-                const int hi = place - j0, lo = a.window ? hi - a.window : -1, sk = a.sinks - j0;
+                // number v0 + 32 q + e is bit e of mask[q]
+                const int hi = own - v0, lo = a.window ? hi - a.window : -1, sk = sp.sinks - v0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     // bits below x, of 32
@@ -668,11 +700,11 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             // The scores, half a row at a time: the second half stays in registers from
             // the maximum to the weights, the first is read twice.
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto scores = [&](int half) {
+            auto scores = [&](int half, bool masked) {
                 tmem_ld32(ts + half * 64, x);
                 tmem_ld32(ts + half * 64 + 32, x + 32);
                 wait_ld();
-                if (!full) {
+                if (masked) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t seen = mask[half * 2 + q];
@@ -689,9 +721,14 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                     top4[(e >> 1) & 3] = max3(top4[(e >> 1) & 3], __uint_as_float(x[e]),
                                               __uint_as_float(x[e + 1]));
             };
-            scores(0);
+            scores(0, !full);
             maximum();
-            scores(1);
+            if (!full) {  // masked once: the second reading finds it so
+                tmem_st32(ts, x);
+                tmem_st32(ts + 32, x + 32);
+                wait_st();
+            }
+            scores(1, !full);
             maximum();
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
             if (__any_sync(0xffffffffu, top > m + kLazy)) {
@@ -730,7 +767,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             wait_st();
             fence_before();
             arrive_warp(bar(s.b.p_half[w]));  // the products of the second half may begin
-            scores(0);
+            scores(0, false);
             weights(0);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             wait_st();
@@ -773,9 +810,9 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         // are done, so that whole lines are written: a warp's 32 rows, half of the columns
         // at a time.
         constexpr int NC = HD / 2, CPR = NC / 8;  // columns, chunks of a row
-        uint32_t stage, stage_parity;
-        value_slot(n - 1, stage, stage_parity);
-        stage = ring + stage * C::kTile + (tid >> 5) * (C::kTile / 8);
+        // The segment's 2 n tiles took ring slots from base_slot on, this one the last.
+        const uint32_t stage = ring + (base_slot + 2 * n - 1) % C::NS * C::kTile +
+                               (tid >> 5) * (C::kTile / 8);
         auto stage_at = [&](int r, int c) {
             return stage + r * NC * 2 + ((c ^ (CPR == 8 ? r & 7 : (r >> 1) & 3)) << 4);
         };
@@ -804,7 +841,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 if (poisoned) {
                     float o[32];
                     for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]);
-                    add_unbounded(a, g, place, col, o);
+                    add_unbounded(a, g, own, col, o);
                     for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(o[e]);
                 }
                 if (whole) {
@@ -865,9 +902,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             if (!wait(bar(s.b.joined), 1, &s.dead)) return;
             fence_after();
         }
-        const uint32_t pos = base_slot + 2 * n, rounds = pos / C::NS;
-        base_slot = pos - rounds * C::NS;
-        base_parity ^= rounds & 1;
+        base_slot = (base_slot + 2 * n) % C::NS;
         ++seg;
         // The last segment ends where the worker's range does.
         if (!ahead && tid == 0)
@@ -889,15 +924,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(bar(s.b.full[i]), 1);
-            mbar_init(bar(s.b.empty[i]), 1);
+            mbar_init(bar(s.b.empty[i]), 2);  // its products, and the clearing warp
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
             mbar_init(bar(s.b.p_half[w]), 4);
             mbar_init(bar(s.b.p_ready[w]), 4);
             mbar_init(bar(s.b.q_ready[w]), WIDE ? 4 : 8);
-            mbar_init(bar(s.b.clean[w]), WIDE ? 8 : 4);
         }
+        for (int i = 0; i < kCleans; ++i) mbar_init(bar(s.b.clean[i]), 1);
         mbar_init(bar(s.b.o_full), 1);
         mbar_init(bar(s.b.joined), 8);
         mbar_init(bar(s.b.staged), 8);
@@ -920,8 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Cursor cur = make_plan<kThreads, ROWS, kKT, WIDE ? kExtraWide : kExtraDrafts, 1>(L.a, blockIdx.x, gridDim.x, &s.plan,
-                                                   blockIdx.x == 0);
+    Cursor cur = make_plan<kThreads, ROWS, kKT, WIDE ? kExtraWide : kExtraDrafts, 1>(L.a, blockIdx.x, gridDim.x,
+                                                   box_rows(L.a), &s.plan, blockIdx.x == 0);
     fence_after();
     const uint32_t tm = *(volatile uint32_t *)&s.tmem;
 
@@ -935,11 +970,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
             wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
     } else if (warp == 9) {
-        mma_role<HD, WIDE>(L, s, qbuf, ring, tm);
+        mma_role<HD, WIDE>(s, qbuf, ring, tm);
         commit(elect(), bar(s.b.drain));
         wait_parity(bar(s.b.drain), 0);
-    } else if (tid == 10 * 32) {
-        segment_role<WIDE>(L.a, s, cur);
+    } else if (warp == 10) {
+        if (tid == 10 * 32) segment_role<WIDE>(L.a, s, cur);
+    } else {
+        clear_role<HD, WIDE>(L, s, ring, tid & 31);
     }
     __syncwarp();
     fence_before();
