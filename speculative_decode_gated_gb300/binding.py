@@ -448,6 +448,8 @@ class Attn:
         self.c = c
         self.refs = refs
         self.dtype, self.device = dtype, device
+        self.n_tok, self.q_heads, self.kv_heads, self.head_dim = (
+            c.n_tok, c.q_heads, c.kv_heads, c.head_dim)
         self.ref = ctypes.byref(c)
 
 
@@ -525,17 +527,24 @@ def make_rope(*, inv_freq: torch.Tensor, interleaved: bool = False, mscale: floa
 
 def _check_rows(t: torch.Tensor, name: str, attn: Attn, heads: int) -> int:
     """Checks a [N_tok, heads, head_dim] tensor whose rows are contiguous; its row stride."""
-    c = attn.c
+    n, hd = attn.n_tok, attn.head_dim
     if t.dtype is not attn.dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {attn.dtype}")
     if t.device != attn.device:
         raise ValueError(f"{name} is on {t.device}, expected {attn.device}")
-    if tuple(t.shape) != (c.n_tok, heads, c.head_dim):
-        raise ValueError(f"{name} must be {(c.n_tok, heads, c.head_dim)}, is {tuple(t.shape)}")
+    if t.shape != (n, heads, hd):
+        raise ValueError(f"{name} must be {(n, heads, hd)}, is {tuple(t.shape)}")
     s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != c.head_dim):
+    if s[2] != 1 or (s[1] != hd and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if c.n_tok > 1 else heads * c.head_dim
+    return s[0] if n > 1 else heads * hd
+
+
+def _attn_stream(attn: Attn, stream) -> int:
+    """`stream`, or the current stream of the tensors' device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(attn.device.index or 0)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def gdn_rope_append(attn: Attn, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -543,19 +552,20 @@ def gdn_rope_append(attn: Attn, rope: Rope, q: torch.Tensor, k: torch.Tensor, v:
     """q_out <- rotated q; the rotated k and the v of each row to the pages.
     q, q_out: [N_tok, q_heads, head_dim]; k, v: [N_tok, kv_heads, head_dim]; the rows of
     q, k and v may be slices of wider ones, q_out is contiguous."""
-    c = attn.c
-    sq = _check_rows(q, "q", attn, c.q_heads)
-    sk = _check_rows(k, "k", attn, c.kv_heads)
-    sv = _check_rows(v, "v", attn, c.kv_heads)
-    if _check_rows(q_out, "q_out", attn, c.q_heads) != c.q_heads * c.head_dim:
+    Hq, Hkv = attn.q_heads, attn.kv_heads
+    sq, sk = _check_rows(q, "q", attn, Hq), _check_rows(k, "k", attn, Hkv)
+    sv = _check_rows(v, "v", attn, Hkv)
+    if _check_rows(q_out, "q_out", attn, Hq) != Hq * attn.head_dim:
         raise ValueError("q_out must be contiguous")
-    if rope.refs[0].device != attn.device:
-        raise ValueError(f"inv_freq is on {rope.refs[0].device}, expected {attn.device}")
-    if rope.refs[1] is not None and rope.refs[1].numel() != c.n_tok:
+    inv_freq, positions = rope.refs
+    if inv_freq.device != attn.device:
+        raise ValueError(f"inv_freq is on {inv_freq.device}, expected {attn.device}")
+    if positions is not None and positions.numel() != attn.n_tok:
         raise ValueError("positions must be [N_tok]")
-    _raise(lib().gdn_rope_append(attn.ref, rope.ref, q.data_ptr(), sq, k.data_ptr(), sk,
-                                 v.data_ptr(), sv, q_out.data_ptr(), _stream(stream)),
-           "gdn_rope_append")
+    st = lib().gdn_rope_append(attn.ref, rope.ref, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(),
+                               sv, q_out.data_ptr(), _attn_stream(attn, stream))
+    if st:
+        _raise(st, "gdn_rope_append")
 
 
 def gdn_paged_attn_workspace(attn: Attn) -> int:
@@ -576,16 +586,17 @@ def gdn_paged_attn(attn: Attn, q: torch.Tensor, o: torch.Tensor, *, workspace: t
     """o <- attention of the step's rows over the cache; lse (fp32 [N_tok, q_heads], or None)
     <- the logarithm of each row's sum.  q, o: [N_tok, q_heads, head_dim]; q's rows may be
     slices of wider ones, o is contiguous."""
-    c = attn.c
-    sq = _check_rows(q, "q", attn, c.q_heads)
-    if _check_rows(o, "o", attn, c.q_heads) != c.q_heads * c.head_dim:
+    Hq = attn.q_heads
+    sq = _check_rows(q, "q", attn, Hq)
+    if _check_rows(o, "o", attn, Hq) != Hq * attn.head_dim:
         raise ValueError("o must be contiguous")
     if lse is not None:
         _check(lse, "lse", (torch.float32,), attn.device)
-        if lse.numel() != c.n_tok * c.q_heads:
+        if lse.numel() != attn.n_tok * Hq:
             raise ValueError("lse must be [N_tok, q_heads]")
     if workspace.device != attn.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {attn.device}")
-    _raise(lib().gdn_paged_attn(attn.ref, q.data_ptr(), sq, o.data_ptr(), _ptr(lse),
-                                workspace.data_ptr(), workspace.nbytes, _stream(stream)),
-           "gdn_paged_attn")
+    st = lib().gdn_paged_attn(attn.ref, q.data_ptr(), sq, o.data_ptr(), _ptr(lse),
+                              workspace.data_ptr(), workspace.nbytes, _attn_stream(attn, stream))
+    if st:
+        _raise(st, "gdn_paged_attn")

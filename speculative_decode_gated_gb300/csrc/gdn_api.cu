@@ -547,7 +547,9 @@ gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, vo
     gdn::AttnArgs a = attn_args(p, q, q_stride, o);
     a.lse = lse;
     a.desc = static_cast<int4 *>(workspace);
-    a.part = reinterpret_cast<float *>(a.desc + 2 * gdn::kAttnWorkers);
+    a.count = reinterpret_cast<int *>(a.desc + 2 * gdn::kAttnWorkers);
+    static_assert(gdn::kAttnWorkers * (2 * sizeof(int4) + sizeof(int)) <= gdn::kAttnHeader, "header");
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + gdn::kAttnHeader);
     const cudaError_t e = gdn::launch_attn(a, p->dtype == GDN_BF16, stream);
     if (e != cudaSuccess) {
         set_cuda_error(e, "kernel launch");

@@ -8,6 +8,7 @@
 // and o / l at the end.  m = -inf (no key seen yet) is replaced by 0 in the
 // exponents, so a row whose mask hides a whole tile, or a whole worker's
 // range, adds nothing instead of NaN.
+#include <algorithm>
 #include <cstdint>
 
 #include "gdn_attn.cuh"
@@ -20,11 +21,9 @@ constexpr int kRows = 16;   // query rows of a unit
 constexpr int kKeys = 32;   // places of a key tile
 constexpr int kThreads = 128;
 constexpr int kAlign = 16;  // pages begin at multiples of it
+constexpr int kMaxParts = 48;  // joined by one block; more by a launch of their own
 constexpr int kMinTiles = 2;
 constexpr int kExtra = 1;   // a unit's start and end, in tiles
-
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 template <int HD>
 struct Smem {
@@ -34,6 +33,7 @@ struct Smem {
     float v[kKeys][LD];
     float p[kRows][kKeys + 1];
     PlanScratch plan;
+    int2 join;
 };
 
 // 16 bytes of a row -> floats in shared memory.
@@ -162,78 +162,70 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
                 const long long at = (long long)(g.req.row0 + t) * a.Hq + g.h * a.G + gh;
                 const float inv = 1.f / l;
 #pragma unroll
-                for (int u = 0; u < HD / 8; ++u)
-                    put(static_cast<T *>(a.o) + at * HD + 4 * sub + 32 * (u / 4) + u % 4, o[u] * inv);
+                for (int u = 0; u < HD / 8; u += 4)
+                    put(static_cast<T *>(a.o) + at * HD + 4 * sub + 8 * u,
+                        make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv));
                 if (a.lse && sub == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
             } else {
                 float *dst = a.part + (long long)part_slot(c, g) * kRows * (HD + 2);
 #pragma unroll
-                for (int u = 0; u < HD / 8; ++u)
-                    dst[part_at<kRows>(row, 4 * sub + 32 * (u / 4) + u % 4)] = o[u];
+                for (int u = 0; u < HD / 8; u += 4)
+                    *reinterpret_cast<float4 *>(dst + part_at<kRows>(row, 4 * sub + 8 * u)) =
+                        make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
                 if (sub == 0) {
                     dst[kRows * HD + row] = m;
                     dst[kRows * HD + kRows + row] = l;
                 }
             }
         }
+        if (a.count && !(g.i0 == 0 && g.i1 == g.span.n))
+            join_if_last<T, kRows, HD, kThreads>(a, c, g, cur.x, s.plan.total, s.plan.workers, &s.join);
     }
-    if (tid == 0) write_desc(a, c, g, any, cur.x, s.plan.total, s.plan.workers);
+    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, s.plan.total, s.plan.workers);
 }
 
-// Joins the partials of a unit that spans workers c .. last: block (c, y) its
-// rows y * 8 .. y * 8 + 7, a warp a row.  Partials are added in the order of the
-// workers; each counts 2^(m_w - m).
+// Joins the partials of a unit that spans workers c .. last: block (c, y) the eight rows and
+// CGB column groups (of four) that y names, eight rows of a group being a line.  SLICES
+// threads share a value's partials, added in the order of the workers and then of the
+// slices.
+template <int ROWS, int HD>
+struct Combine {
+    static constexpr int CG = HD / 4;
+    static constexpr int kWant = ROWS == 16 ? 8 : ROWS == 128 ? 16 : 32;
+    static constexpr int CGB = CG < kWant ? CG : kWant;
+    static constexpr int SLICES = 256 / (8 * CGB);
+    static constexpr int kBlocks = ROWS / 8 * (CG / CGB);
+};
+
 template <typename T, int ROWS, int HD>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
+    using C = Combine<ROWS, HD>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ Partial<1> part[C::SLICES][8 * C::CGB];
     const int c = blockIdx.x;
     const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
     const int last = d0.x, qt = d0.y, h = d0.z, row0 = d0.w, T_r = d1.x;
-    const int rows = min(8, T_r * a.G - qt * ROWS - (int)blockIdx.y * 8);
-    if (last < 0 || rows <= 0) return;
-    constexpr long long kSlot = (long long)ROWS * (HD + 2);
-    auto slot = [&](int w) { return a.part + (w == c ? 2 * c + 1 : 2 * w) * kSlot; };
-    // Thread (row = tid % 8, column group = tid / 8): eight rows of four columns are a
-    // line of the partials.
-    constexpr int CG = HD / 4;              // column groups
-    constexpr int PER = (CG + 31) / 32;     // of them a thread
-    const int r = threadIdx.x & 7, cg = threadIdx.x >> 3, row = blockIdx.y * 8 + r;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int w = c; w <= last; ++w) m = fmaxf(m, slot(w)[ROWS * HD + row]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float4 o[PER] = {};
-    float l = 0.f;
-#pragma unroll 4
-    for (int w = c; w <= last; ++w) {
-        const float *p = slot(w);
-        const float f = exp2f(p[ROWS * HD + row] - base);
-        l = fmaf(p[ROWS * HD + ROWS + row], f, l);
+    const int rb = (int)blockIdx.y / (C::CG / C::CGB) * 8, cb = blockIdx.y % (C::CG / C::CGB) * C::CGB;
+    if (last < 0 || qt * ROWS + rb >= T_r * a.G) return;
+    const int item = threadIdx.x % (8 * C::CGB), slice = threadIdx.x / (8 * C::CGB);
+    const int row = rb + (item & 7), cg = cb + (item >> 3), i = qt * ROWS + row;
+    Partial<1> s;
+    add_partials<ROWS, HD, 1, 1>(a, s, c, c + slice, C::SLICES, last, row, cg);
+    if (C::SLICES > 1) {
+        if (slice > 0) part[slice][item] = s;
+        __syncthreads();
+        if (slice > 0) return;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            if (cg + 32 * e >= CG) continue;
-            const float4 x = *reinterpret_cast<const float4 *>(p + part_at<ROWS>(row, 4 * (cg + 32 * e)));
-            o[e].x = fmaf(x.x, f, o[e].x);
-            o[e].y = fmaf(x.y, f, o[e].y);
-            o[e].z = fmaf(x.z, f, o[e].z);
-            o[e].w = fmaf(x.w, f, o[e].w);
-        }
+        for (int k = 1; k < C::SLICES; ++k) s.add(part[k][item].m, part[k][item].l, part[k][item].o);
     }
-    if (r >= rows) return;
-    const int i = qt * ROWS + row, t = div_group(a, i);
+    if (i >= T_r * a.G) return;
+    const int t = div_group(a, i);
     const long long at = (long long)(row0 + t) * a.Hq + h * a.G + (i - t * a.G);
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        if (cg + 32 * e >= CG) continue;
-        T *dst = static_cast<T *>(a.o) + at * HD + 4 * (cg + 32 * e);
-        put(dst, o[e].x * inv);
-        put(dst + 1, o[e].y * inv);
-        put(dst + 2, o[e].z * inv);
-        put(dst + 3, o[e].w * inv);
-    }
-    if (a.lse && cg == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+    const float inv = 1.f / s.l;
+    put(static_cast<T *>(a.o) + at * HD + 4 * cg,
+        make_float4(s.o[0].x * inv, s.o[0].y * inv, s.o[0].z * inv, s.o[0].w * inv));
+    if (a.lse && cg == 0) a.lse[at] = (s.m + log2f(s.l)) * 0.69314718055994531f;
 }
 
 template <typename K>
@@ -254,9 +246,7 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs
 
 template <int HD>
 cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<float, HD>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(Smem<HD>));
+    const cudaError_t e = allow_smem<attn_simple_kernel<float, HD>>((int)sizeof(Smem<HD>));
     if (e != cudaSuccess) return e;
     return launch(attn_simple_kernel<float, HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a,
                   stream);
@@ -266,26 +256,36 @@ cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
 template <int HD>
 cudaError_t launch_hd(const AttnArgs &a, bool bf16, cudaStream_t stream) {
     const AttnKind kind = attn_kind(bf16, HD, (long long)a.max_T * a.G);
-    const auto joined = [&](cudaError_t first, auto join, int workers, int rows) {
+    const auto joined = [&](cudaError_t first, auto join, int workers, int blocks) {
         return first != cudaSuccess ? first
-                                    : launch(join, dim3(workers, rows / 8), 256, 0, a, stream);
+                                    : launch(join, dim3(workers, blocks), 256, 0, a, stream);
     };
-    if (kind == kAttnSimple)
-        return joined(launch_simple<HD>(a, stream), combine_kernel<float, 16, HD>, kAttnWorkers, 16);
     if constexpr (HD == 64 || HD == 128) {
         if (kind == kAttnDrafts)
             return joined(launch_attn_tc(a, false, stream), combine_kernel<__nv_bfloat16, 128, HD>,
-                          kAttnTcWorkers, 128);
+                          kAttnTcWorkers, Combine<128, HD>::kBlocks);
         if (kind == kAttnWide)
             return joined(launch_attn_tc(a, true, stream), combine_kernel<__nv_bfloat16, 256, HD>,
-                          kAttnTcWorkers, 256);
+                          kAttnTcWorkers, Combine<256, HD>::kBlocks);
     }
-    return joined(launch_attn_rows(a, stream), combine_kernel<__nv_bfloat16, 16, HD>, kAttnWorkers, 16);
+    const cudaError_t e = kind == kAttnSimple ? launch_simple<HD>(a, stream) : launch_attn_rows(a, stream);
+    if (a.count) return e;
+    return kind == kAttnSimple ? joined(e, combine_kernel<float, 16, HD>, kAttnWorkers,
+                                        Combine<16, HD>::kBlocks)
+                               : joined(e, combine_kernel<__nv_bfloat16, 16, HD>, kAttnWorkers,
+                                        Combine<16, HD>::kBlocks);
 }
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream) {
+cudaError_t launch_attn(AttnArgs a, bool bf16, cudaStream_t stream) {
+    // Few partials to a unit: the block that writes the last one joins them, and the second
+    // launch is saved.  A request's key heads have equal work, so a unit spans at most
+    // workers / key heads (and a bit) of them, and no more than its tiles allow.
+    const AttnKind kind = attn_kind(bf16, a.hd, (long long)a.max_T * a.G);
+    const long long tiles = ((long long)a.max_pages << a.page_shift) / 32;
+    const long long parts = std::min<long long>(kAttnWorkers / a.Hkv, tiles / 2) + 2;
+    if (kind == kAttnDrafts || kind == kAttnWide || parts > kMaxParts) a.count = nullptr;
     switch (a.hd) {
         case 32: return launch_hd<32>(a, bf16, stream);
         case 64: return launch_hd<64>(a, bf16, stream);
@@ -307,7 +307,7 @@ int64_t attn_workspace(bool bf16, int hd, long long rows) {
     const AttnKind kind = attn_kind(bf16, hd, rows);
     const int64_t workers = kind == kAttnDrafts || kind == kAttnWide ? kAttnTcWorkers : kAttnWorkers;
     const int64_t unit = kind == kAttnWide ? 256 : kind == kAttnDrafts ? 128 : 16;
-    return 2 * kAttnWorkers * (int64_t)sizeof(int4) +
+    return kAttnHeader +
            2 * workers * unit * (hd + 2) * (int64_t)sizeof(float);
 }
 

@@ -17,7 +17,8 @@
 // lies in one worker's range is finished there; one that spans several leaves
 // a partial (unnormalised sums, running maximum, total) per worker, joined by
 // combine_kernel in the order of the workers, so results do not depend on
-// timing.  A worker has at most two partials: the end of a unit begun earlier
+// timing (in the largest calls; where a unit cannot have many partials the block that
+// writes the last of them joins them in that same order).  A worker has at most two partials: the end of a unit begun earlier
 // (slot 2c) and the beginning of one finished later (slot 2c + 1).
 #pragma once
 
@@ -50,6 +51,8 @@ struct AttnArgs {
     float *lse;
     float *part;             // 2P partial slots of ROWS * (hd + 2) floats
     int4 *desc;              // [P][2]: which unit worker c leaves unfinished
+    int *count;              // [P], zero between calls: partials of the unit that begins in
+                             // worker c; NULL: combine_kernel joins them, by desc
 };
 
 __device__ __forceinline__ int div_group(const AttnArgs &a, int n) {
@@ -324,6 +327,99 @@ __device__ __forceinline__ void write_desc(const AttnArgs &a, int c, const Segme
     }
     a.desc[2 * c] = d0;
     a.desc[2 * c + 1] = d1;
+}
+
+__device__ __forceinline__ void put(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float4 x) {  // rounded once, to nearest even
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                               *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// A running softmax state (maximum, total, outputs) and the addition of another.
+template <int PER>
+struct Partial {
+    float m = -INFINITY, l = 0.f;
+    float4 o[PER] = {};
+    // o += f x, with m, l, o taken to the larger of the two maxima first.
+    __device__ __forceinline__ void add(float xm, float xl, const float4 *x) {
+        const float top = fmaxf(m, xm), base = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - base), g = exp2f(xm - base);
+        m = top;
+        l = l * f + xl * g;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            o[e].x = o[e].x * f + x[e].x * g;
+            o[e].y = o[e].y * f + x[e].y * g;
+            o[e].z = o[e].z * f + x[e].z * g;
+            o[e].w = o[e].w * f + x[e].w * g;
+        }
+    }
+};
+
+// Partials w0, w0 + step, ... up to `last` of row `row`, PER column groups (of four) from cg on,
+// CSTEP apart; the first is worker c's slot 2c + 1.  Four are in flight at a time.
+template <int ROWS, int HD, int PER, int CSTEP>
+__device__ __forceinline__ void add_partials(const AttnArgs &a, Partial<PER> &s, int c, int w0, int step,
+                                             int last, int row, int cg) {
+    constexpr int U = PER <= 4 ? 4 : 1;
+    for (int w = w0; w <= last; w += U * step) {
+        float m[U], l[U];
+        float4 x[U][PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int wu = w + u * step;
+            m[u] = -INFINITY;
+            l[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (wu > last) continue;
+            const float *p = a.part + (long long)(wu == c ? 2 * c + 1 : 2 * wu) * ROWS * (HD + 2);
+            m[u] = __ldcg(p + ROWS * HD + row);
+            l[u] = __ldcg(p + ROWS * HD + ROWS + row);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                x[u][e] = __ldcg(reinterpret_cast<const float4 *>(
+                    p + part_at<ROWS>(row, 4 * (cg + e * CSTEP))));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) s.add(m[u], l[u], x[u]);
+    }
+}
+
+// Called by all NT threads of a block that has written its partial of segment g (x: the
+// line position after it): the block whose partial is the unit's last joins them.
+template <typename T, int ROWS, int HD, int NT>
+__device__ __forceinline__ void join_if_last(const AttnArgs &a, int c, const Segment &g, long long x,
+                                             long long N, int P, int2 *shared) {
+    __threadfence();
+    __syncthreads();
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        const long long begin = x - g.i1;  // of the unit's tiles
+        const int first = worker_of(begin, N, P), last = worker_of(begin + g.span.n - 1, N, P);
+        const bool all = atomicAdd(a.count + first, 1) == last - first;
+        if (all) a.count[first] = 0;  // for the next call
+        *shared = make_int2(all ? first : -1, last);
+    }
+    __syncthreads();
+    const int first = shared->x, last = shared->y;
+    if (first < 0) return;
+    __threadfence();
+    constexpr int PER = ROWS * HD / 4 / NT, CSTEP = NT / ROWS;
+    const int row = tid % ROWS, cg = tid / ROWS;
+    Partial<PER> s;
+    add_partials<ROWS, HD, PER, CSTEP>(a, s, first, first, 1, last, row, cg);
+    const int i = g.qt * ROWS + row;
+    if (i >= g.req.T * a.G) return;
+    const int t = div_group(a, i);
+    const long long at = (long long)(g.req.row0 + t) * a.Hq + g.h * a.G + (i - t * a.G);
+    const float inv = 1.f / s.l;
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+        put(static_cast<T *>(a.o) + at * HD + 4 * (cg + e * CSTEP),
+            make_float4(s.o[e].x * inv, s.o[e].y * inv, s.o[e].z * inv, s.o[e].w * inv));
+    if (a.lse && cg == 0) a.lse[at] = (s.m + log2f(s.l)) * 0.69314718055994531f;
 }
 
 }  // namespace gdn

@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ PlanScratch plan;
     __shared__ float top[C::W][kRows], sum[C::W][kRows];
+    __shared__ int2 joined;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = blockIdx.x, P = gridDim.x;
     float *join = reinterpret_cast<float *>(smem + C::W * C::S * 2 * C::kTile);
@@ -411,15 +412,17 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                 }
             }
         }
+        if (a.count && !(g.i0 == 0 && g.i1 == sp.n))
+            join_if_last<__nv_bfloat16, kRows, HD, C::NT>(a, c, g, cur.x, plan.total, plan.workers,
+                                                          &joined);
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-    if (tid == 0) write_desc(a, c, g, any, cur.x, plan.total, plan.workers);
+    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, plan.total, plan.workers);
 }
 
 template <int HD>
 cudaError_t launch_hd(const AttnArgs &a, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_rows_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kSmem);
+    const cudaError_t e = allow_smem<attn_rows_kernel<HD>>(Cfg<HD>::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kAttnWorkers);

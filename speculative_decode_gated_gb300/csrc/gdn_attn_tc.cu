@@ -1027,8 +1027,7 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     constexpr int smem = Cfg<HD>::kTiles + (int)sizeof(Shared);
     static_assert(smem <= 232448, "227 KB of shared memory a block");
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_tc_kernel<HD, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<attn_tc_kernel<HD, WIDE>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kAttnTcWorkers);

@@ -3,6 +3,9 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 #include "gdn_attn.cuh"
 #include "gdn_device.cuh"
 
@@ -36,13 +39,29 @@ cudaError_t launch_rope(const AttnArgs &a, const gdn_rope &rope, bool bf16, cons
                         void *v_pages, cudaStream_t stream);
 
 // Chunk attention over the cache.  a.desc and a.part point into the workspace:
-// attn_workspace() bytes, the 2 * kAttnWorkers descriptors first.
+// attn_workspace() bytes: the descriptors, the counts, then the partials.
+// Shared memory above 48 KB is asked for once a device and kernel (KERNEL names the
+// instantiation, so each has its own record).
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 constexpr int kAttnWorkers = 304;    // blocks, two on each of 152 SMs
+constexpr int kAttnHeader = 16384;   // bytes of the workspace before the partials
 constexpr int kAttnTcWorkers = 152;  // blocks of the tcgen05 kernel, one an SM
 enum AttnKind { kAttnSimple, kAttnRows, kAttnDrafts, kAttnWide };
 AttnKind attn_kind(bool bf16, int hd, long long rows);  // rows: max_T times the group
 int64_t attn_workspace(bool bf16, int hd, long long rows);
-cudaError_t launch_attn(const AttnArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn(AttnArgs a, bool bf16, cudaStream_t stream);
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t stream);  // their first launches
 cudaError_t launch_attn_tc(const AttnArgs &a, bool wide, cudaStream_t stream);
 

@@ -121,9 +121,18 @@ def test_repeatable_and_without_lse(dtype, T):
              seed=T).device()
     a = c.run().o.clone()
     ws = c.ws
-    ws.view(torch.float32).fill_(float("nan"))  # nothing a call left is read by the next
+    assert not ws[9728:16384].any()              # the counters are back at zero
+    ws[16384:].view(torch.float32).fill_(float("nan"))  # nothing else a call left is read by the next
     assert torch.equal(c.run(workspace=ws).o, a)
     assert torch.equal(c.run(lse=False, workspace=ws).o, a)
+
+
+@pytest.mark.parametrize("dtype,kv_heads,T", [("bf16", 1, 1), ("bf16", 2, 3), ("bf16", 8, 1),
+                                              ("fp32", 1, 1), ("fp32", 8, 2), ("bf16", 1, 20)])
+def test_one_long_request_among_short_ones(dtype, kv_heads, T):
+    # a unit of many partials: joined by the last block to write one, or by a launch of its own
+    Case(new=[T, 1, T], old=[9, 20011, 300], q_heads=2 * kv_heads, kv_heads=kv_heads, hd=64,
+         dtype=dtype, page=64, seed=kv_heads).device().run().check()
 
 
 def test_ragged_and_uniform_rows_agree():
