@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
             }
         }
         if (a.count && !(g.i0 == 0 && g.i1 == g.span.n))
-            join_if_last<T, kRows, HD, kThreads>(a, c, g, cur.x, s.plan.total, s.plan.workers, &s.join);
+            join_if_last<T, kRows, HD, kThreads>(a, c, g, cur.x, cur.N, cur.P, &s.join);
     }
-    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, s.plan.total, s.plan.workers);
+    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, cur.N, cur.P);
 }
 
 // Joins the partials of a unit that spans workers c .. last: block (c, y) the eight rows and

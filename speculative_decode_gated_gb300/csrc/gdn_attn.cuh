@@ -160,23 +160,66 @@ struct PlanScratch {
 
 // A worker's position on the line of tiles.
 struct Cursor {
-    long long x, x1;   // next tile, end of the range
+    long long x, x1;   // next place of the line, end of the range
     long long off;     // of x within the entry
     int r, qt;
+    int P;             // workers, and
+    long long N;       // places of the line
 };
 
-// Every thread of the block calls it; ends with a barrier.  At least MIN_TILES
-// places of the line to a worker: fewer, longer runs when there is little work.
+// The range of worker c.
+__device__ __forceinline__ void worker_range(int c, int P, long long N, long long &x0, long long &x1) {
+    if (c >= P) {
+        x0 = x1 = 0;
+    } else if (N < (1 << 22)) {  // 32-bit products and quotients: c + 1 is below 2^10
+        x0 = (unsigned)c * (unsigned)N / (unsigned)P;
+        x1 = (unsigned)(c + 1) * (unsigned)N / (unsigned)P;
+    } else {
+        x0 = c * N / P;
+        x1 = (c + 1) * N / P;
+    }
+}
+
+// Every thread of the block calls it.  At least MIN_TILES places of the line to a worker:
+// fewer, longer runs when there is little work.  Up to 32 entries (request, query tile) every
+// warp adds them up for itself, an entry a lane, without a barrier; more are spread over
+// the block.
 template <int NT, int ROWS, int KT, int EXTRA, int MIN_TILES>
 __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, int align,
                                             PlanScratch *s, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nqm = a.max_T ? (a.max_T * a.G + ROWS - 1) / ROWS : 1;
     const unsigned E = (unsigned)a.B * nqm;  // below 2^31: checked on the host
+    Cursor cur;
+    if (E <= 32) {
+        const int r = lane / nqm, qt = lane - r * nqm;
+        long long sum = 0;
+        if (lane < (int)E) {
+            const AttnReq q = load_request(a, r, report && warp == 0 && qt == 0);
+            const int n = q.ok ? tile_span<ROWS, KT>(a, q.T, q.ctx, qt, align).n : 0;
+            sum = n ? (long long)(n + EXTRA) * a.Hkv : 0;
+        }
+        long long incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        cur.N = __shfl_sync(0xffffffffu, incl, 31);
+        const long long by_size = (cur.N + MIN_TILES - 1) / MIN_TILES;
+        cur.P = by_size < P ? (int)by_size : P;
+        worker_range(c, cur.P, cur.N, cur.x, cur.x1);
+        const unsigned here = __ballot_sync(0xffffffffu, cur.x >= incl - sum && cur.x < incl);
+        const int src = here ? __ffs(here) - 1 : 0;
+        cur.off = cur.x - __shfl_sync(0xffffffffu, incl - sum, src);
+        cur.r = src / nqm;
+        cur.qt = src - cur.r * nqm;
+        return cur;
+    }
+
     const unsigned chunk = (E + NT - 1) / NT;
     const unsigned e0 = min(tid * chunk, E), e1 = min(e0 + chunk, E);
     if (tid == 0) s->entry = -1;
-
     // Tiles of this thread's entries.
     long long sum = 0;
     for (unsigned e = e0; e < e1;) {
@@ -212,16 +255,9 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, int
         s->warp_sum[lane] = wi - w;
         if (lane == 31) {
             const long long by_size = (wi + MIN_TILES - 1) / MIN_TILES;
-            const int p = by_size < P ? (int)by_size : P;
             s->total = wi;
-            s->workers = p;
-            if (wi < (1 << 22)) {  // 32-bit products and quotients: (c + 1) below 2^10
-                s->x0 = c < p ? (unsigned)c * (unsigned)wi / (unsigned)p : 0;
-                s->x1 = c < p ? (unsigned)(c + 1) * (unsigned)wi / (unsigned)p : 0;
-            } else {
-                s->x0 = c < p ? (long long)c * wi / p : 0;
-                s->x1 = c < p ? (long long)(c + 1) * wi / p : 0;
-            }
+            s->workers = by_size < P ? (int)by_size : P;
+            worker_range(c, s->workers, wi, s->x0, s->x1);
         }
     }
     __syncthreads();
@@ -252,7 +288,8 @@ __device__ __forceinline__ Cursor make_plan(const AttnArgs &a, int c, int P, int
         }
     }
     __syncthreads();
-    Cursor cur;
+    cur.N = s->total;
+    cur.P = s->workers;
     cur.x = x0;
     cur.x1 = s->entry >= 0 ? x1 : x0;
     cur.off = s->entry >= 0 ? s->off : 0;

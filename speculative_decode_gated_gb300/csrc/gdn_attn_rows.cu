@@ -99,16 +99,23 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) {
     return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
 }
 
-// Copies a warp's 16 places of tile i of segment g into its ring slot.
+// The page of a warp's 16 places of tile i, or -1 when no row sees one of them.
 template <int HD>
-__device__ __forceinline__ void copy_tile(const AttnArgs &a, const Segment &g, int i, int warp,
+__device__ __forceinline__ int page_of(const AttnArgs &a, const Segment &g, int i, int warp) {
+    const int v0 = i * Cfg<HD>::KT + warp * 16;
+    if (!some_see(a, g.span, v0, v0 + 15)) return -1;
+    return a.page_table[(long long)g.r * a.max_pages + (place_of(g.span, v0) >> a.page_shift)];
+}
+
+// Copies a warp's 16 places of tile i of segment g, in `page`, into its ring slot.
+template <int HD>
+__device__ __forceinline__ void copy_tile(const AttnArgs &a, const Segment &g, int i, int page, int warp,
                                           int lane, uint32_t kdst) {
     using C = Cfg<HD>;
     const int v0 = i * C::KT + warp * 16;
     const TileSpan &sp = g.span;
     if (!some_see(a, sp, v0, v0 + 15)) return;
     const int j0 = place_of(sp, v0);
-    const int page = a.page_table[(long long)g.r * a.max_pages + (j0 >> a.page_shift)];
     const bool page_ok = page >= 0 && page < a.n_pages;
     if (!page_ok && lane == 0 && a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
     const long long at = page_ok ? (long long)page * a.page_stride +
@@ -118,14 +125,21 @@ __device__ __forceinline__ void copy_tile(const AttnArgs &a, const Segment &g, i
     const char *kp = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.k) + at);
     const char *vp = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.v) + at);
     constexpr int CR = HD / 8;  // chunks of a row
+    // a place that no row sees may hold anything: it is zeros here
+    const bool each = v0 + 15 <= sp.pmax && (a.window == 0 || v0 > sp.pmin - a.window || v0 + 15 < sp.sinks);
+    auto copy = [&](auto keep) {
 #pragma unroll
-    for (int u = 0; u < CR / 2; ++u) {
-        const int x = u * 32 + lane, r = x / CR, c = x % CR;
-        // a place that no row sees may hold anything: it is zeros here
-        const bool keep = page_ok && some_see(a, sp, v0 + r, v0 + r);
-        copy16(kdst + chunk_at<HD>(r, c), kp + (keep ? x * 16 : 0), keep);
-        copy16(kdst + C::kTile + chunk_at<HD>(r, c), vp + (keep ? x * 16 : 0), keep);
-    }
+        for (int u = 0; u < CR / 2; ++u) {
+            const int x = u * 32 + lane, r = x / CR, c = x % CR;
+            const bool k = keep(r);
+            copy16(kdst + chunk_at<HD>(r, c), kp + (k ? x * 16 : 0), k);
+            copy16(kdst + C::kTile + chunk_at<HD>(r, c), vp + (k ? x * 16 : 0), k);
+        }
+    };
+    if (each && page_ok)
+        copy([](int) { return true; });
+    else
+        copy([&](int r) { return page_ok && some_see(a, sp, v0 + r, v0 + r); });
 }
 
 template <int HD>
@@ -143,23 +157,28 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
     unsigned char *qs = smem + C::W * C::S * 2 * C::kTile + C::kJoin;
     const uint32_t ring = smem_addr(smem) + warp * C::S * 2 * C::kTile;
 
-    Cursor ahead = make_plan<C::NT, kRows, C::KT, kExtra, 2>(a, c, P, kAlign, &plan, c == 0);
-    Cursor cur = ahead;
-    Segment ga, g;  // the segment being copied, and the one being used
-    int ia = 0;
-    ga.i1 = 0;
-    bool more = true;
+    // Two cursors over the same segments: the copies run S - 1 tiles ahead of the products,
+    // across segments of any length, with one group a tile.
+    Cursor cur = make_plan<C::NT, kRows, C::KT, kExtra, 2>(a, c, P, kAlign, &plan, c == 0);
+    Cursor in = cur;
+    Segment g, gi;        // in use, and being copied
+    int ia = 0, ia_end = 0, page = 0;  // tile to copy next, and the page it lies in
     int slot_in = 0, slot_out = 0;
-    auto advance = [&]() {  // one more tile on its way (or an empty group)
-        if (more && ia >= ga.i1) {
-            more = next_segment<kRows, C::KT, kExtra>(a, kAlign, ahead, ga);
-            ia = ga.i0;
+    auto advance = [&]() {  // one more tile on its way; at the end of the range an empty group
+        if (ia >= ia_end && next_segment<kRows, C::KT, kExtra>(a, kAlign, in, gi)) {
+            ia = gi.i0;
+            ia_end = gi.i1;
+            page = page_of<HD>(a, gi, ia, warp);
         }
-        if (more) copy_tile<HD>(a, ga, ia++, warp, lane, ring + slot_in * 2 * C::kTile);
+        if (ia < ia_end) {
+            const int here = page;
+            if (ia + 1 < ia_end) page = page_of<HD>(a, gi, ia + 1, warp);  // a tile ahead
+            copy_tile<HD>(a, gi, ia++, here, warp, lane, ring + slot_in * 2 * C::kTile);
+        }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
         slot_in = slot_in + 1 == C::S ? 0 : slot_in + 1;
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < C::S - 1; ++s) advance();
 
     // Fragment coordinates: rows qr and qr + 8, columns 2 qc, 2 qc + 1 of 8.
@@ -209,6 +228,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 
         for (int i = g.i0; i < g.i1; ++i) {
+            // No branch around this wait: the group's copies would be waited for one and all.
             asm volatile("cp.async.wait_group %0;\n" ::"n"(C::S - 2) : "memory");
             __syncwarp();
             advance();
@@ -413,11 +433,10 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
             }
         }
         if (a.count && !(g.i0 == 0 && g.i1 == sp.n))
-            join_if_last<__nv_bfloat16, kRows, HD, C::NT>(a, c, g, cur.x, plan.total, plan.workers,
-                                                          &joined);
+            join_if_last<__nv_bfloat16, kRows, HD, C::NT>(a, c, g, cur.x, cur.N, cur.P, &joined);
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, plan.total, plan.workers);
+    if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, cur.N, cur.P);
 }
 
 template <int HD>

@@ -614,7 +614,7 @@ __device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, 
 
 template <int HD, bool WIDE>
 __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
-                                             uint32_t tm) {
+                                             uint32_t tm, const Cursor &plan) {
     using C = Cfg<HD>;
     constexpr int ROWS = WIDE ? 256 : 128;
     constexpr int CR = HD / 8;  // 16-byte chunks of a row
@@ -906,7 +906,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         ++seg;
         // The last segment ends where the worker's range does.
         if (!ahead && tid == 0)
-            write_desc(a, blockIdx.x, g, !s.dead, s.plan.x1, s.plan.total, s.plan.workers);
+            write_desc(a, blockIdx.x, g, !s.dead, plan.x1, plan.N, plan.P);
         arrive_warp(bar(s.b.seg_empty[seg_slot]));
     }
 }
@@ -957,11 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Cursor cur = make_plan<kThreads, ROWS, kKT, WIDE ? kExtraWide : kExtraDrafts, 1>(L.a, blockIdx.x, gridDim.x,
                                                    box_rows(L.a), &s.plan, blockIdx.x == 0);
+    __syncthreads();  // the barriers and the tensor memory's address
     fence_after();
     const uint32_t tm = *(volatile uint32_t *)&s.tmem;
 
     if (warp < 8) {
-        softmax_role<HD, WIDE>(L, s, qbuf, ring, tm);
+        softmax_role<HD, WIDE>(L, s, qbuf, ring, tm, cur);
     } else if (warp == 8) {
         uint32_t issued = 0;
         load_role<HD, WIDE>(L, s, ring, tid & 31, issued);
