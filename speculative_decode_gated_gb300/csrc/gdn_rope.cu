@@ -4,15 +4,18 @@
 // Pair i of a head turns by the angle p * inv_freq[i].  A 32-bit product of a
 // long context's position and a frequency has lost the angle's fraction (half
 // a unit in the last place of 2^17 radians is 0.008), so the angle is kept in
-// turns as a 64-bit fraction: F = inv_freq / (2 pi) * 2^64 modulo 2^64, and p * F
-// modulo 2^64 is the position's fraction of a turn with an error below p * 2^-53
-// * inv_freq; its top 32 bits, as a float in [-1, 1) half turns, go to sincospif.
+// turns as a 64-bit fraction: F = inv_freq / (2 pi) * 2^64 modulo 2^64, from the
+// frequency's 24 bits and 128 bits of 1 / (2 pi) in integers (the reduction of
+// Payne and Hanek), and p * F modulo 2^64 is the
+// position's fraction of a turn, off by less than p * 2^-64.  Its top 32 bits, as a
+// float in [-1, 1) half turns, go to sincospif.
 //
 // Bound by memory: N (Hq + 2 Hkv) hd elements read once and written once.  One
-// block of 128 threads per row: the row's cosines and sines are computed once
-// into shared memory (the first loads are in flight meanwhile) and serve all
-// its heads; a thread moves two 16-byte vectors of a head at a time, the two
-// halves of eight (bf16) pairs, or two neighbours.
+// block of 128 threads per row: the row's loads depend on nothing but its number and go
+// out first; its request, its place and its cosines and sines (computed once, into
+// shared memory, for all heads) are found while they fly.  A thread moves two
+// 16-byte vectors of a head at a time, the two halves of eight (bf16) pairs, or two
+// neighbours.
 #include <cstdint>
 
 #include "gdn_attn.cuh"
@@ -22,7 +25,8 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxPairs = 128;  // head_dim / 2 at most
+constexpr int kMaxPairs = 128;  // head_dim / 2 at most: one a thread
+static_assert(kMaxPairs <= kThreads, "");
 constexpr int kUnroll = 4;      // vectors pairs in flight per thread
 
 template <typename T>
@@ -75,16 +79,31 @@ struct RopeArgs {
     int slot_shift;  // log2 of the vector pairs of a head
 };
 
-// cos and sin of p * f radians.
-__device__ __forceinline__ float2 turn(int p, float f) {
-    // turns per position, times 2^64, modulo 2^64 (a double holds it to 53 bits)
-    const double t = (double)f * 0.15915494309189533577;
-    const double frac = t - floor(t);
-    const unsigned long long F = (unsigned long long)(frac * 4294967296.0) << 32 |
-                                 (unsigned long long)((frac * 4294967296.0 -
-                                                       floor(frac * 4294967296.0)) *
-                                                      4294967296.0);
-    const unsigned long long phase = F * (unsigned long long)(long long)p;
+// Turns per position, times 2^64, modulo 2^64.
+__device__ __forceinline__ unsigned long long turns(float f) {
+    const uint32_t b = __float_as_uint(f);
+    const unsigned long long m = (b & 0x7FFFFFu) | 0x800000u;  // |f| = m 2^(64 - n)
+    const int n = 64 + 150 - (int)((b >> 23) & 0xFFu);
+    if (((b >> 23) & 0xFFu) == 0) return 0;  // zero (or too small to turn)
+    // m * floor(2^128 / (2 pi)), of which the bits from n on
+    constexpr unsigned long long hi = 0x28BE60DB9391054Aull, lo = 0x7F09D5F47D4D3770ull;
+    const unsigned long long p0 = m * lo, c = __umul64hi(m, lo);
+    const unsigned long long p1 = m * hi + c, p2 = __umul64hi(m, hi) + (p1 < c);
+    unsigned long long F;
+    if (n >= 128)
+        F = n < 192 ? p2 >> (n - 128) : 0;
+    else if (n > 64)
+        F = p1 >> (n - 64) | p2 << (128 - n);
+    else if (n == 64)
+        F = p1;
+    else
+        F = n > 0 ? p0 >> n | p1 << (64 - n) : p0 << (n > -64 ? -n : 63);
+    return b >> 31 ? 0 - F : F;
+}
+
+// cos and sin of p times as much.
+__device__ __forceinline__ float2 turn(int p, unsigned long long per_position) {
+    const unsigned long long phase = per_position * (unsigned long long)(long long)p;
     const float x = (float)(int)(phase >> 32) * 0x1p-31f;  // in half turns, [-1, 1]
     float2 cs;
     sincospif(x, &cs.y, &cs.x);
@@ -101,36 +120,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const AttnArgs &a = g.a;
     const int row = blockIdx.x, tid = threadIdx.x;
 
-    // The row's request.
-    int r;
-    if (a.cu_seqlens) {
-        if (row == 0)  // one block reports bad requests, those without rows among them
-            for (int i = tid; i < a.B; i += kThreads) load_request(a, i, true);
-        if (tid == 0) found = -1;
-        __syncthreads();
-        for (int i = tid; i < a.B; i += kThreads)
-            if (a.cu_seqlens[i] <= row && row < a.cu_seqlens[i + 1]) found = i;
-        __syncthreads();
-        r = found;
-        if (r < 0) return;
-    } else {
-        r = row / a.max_T;
-    }
-    const AttnReq q = load_request(a, r, tid == 0);
-    if (!q.ok) return;
-    const int place = q.ctx + (row - q.row0);
-    const int page = a.page_table[(long long)r * a.max_pages + (place >> a.page_shift)];
-    const bool page_ok = page >= 0 && page < a.n_pages;
-    if (!page_ok && tid == 0 && a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
-
     const T *qs = static_cast<const T *>(a.q) + row * a.q_stride;
     const T *ks = static_cast<const T *>(g.k_new) + row * g.k_stride;
     const T *vs = static_cast<const T *>(g.v_new) + row * g.v_stride;
-    T *qd = static_cast<T *>(a.o) + (long long)row * a.Hq * a.hd;
-    const int in_page = place & ((1 << a.page_shift) - 1);
-    const long long at = (long long)page * a.page_stride + (long long)in_page * a.hd;
-    T *kd = static_cast<T *>(g.k_pages) + at;  // + head * page size * hd
-    T *vd = static_cast<T *>(g.v_pages) + at;
 
     const int slots = 1 << g.slot_shift;          // vector pairs of a head
     const int nr = g.rot / VE;                    // rotated vectors of a head (even)
@@ -162,6 +154,37 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             w[u][1] = __ldcs(reinterpret_cast<const uint4 *>(src + v1 * VE));
         }
     };
+    const float freq = tid < g.rot / 2 ? g.inv_freq[tid] : 0.f;  // a pair a thread
+    load(0);
+    const unsigned long long per_position = turns(freq);
+
+    // The row's request.
+    int r;
+    if (a.cu_seqlens) {
+        if (row == 0)  // one block reports bad requests, those without rows among them
+            for (int i = tid; i < a.B; i += kThreads) load_request(a, i, true);
+        if (tid == 0) found = -1;
+        __syncthreads();
+        for (int i = tid; i < a.B; i += kThreads)
+            if (a.cu_seqlens[i] <= row && row < a.cu_seqlens[i + 1]) found = i;
+        __syncthreads();
+        r = found;
+        if (r < 0) return;
+    } else {
+        r = row / a.max_T;
+    }
+    const AttnReq q = load_request(a, r, tid == 0);
+    if (!q.ok) return;
+    const int place = q.ctx + (row - q.row0);
+    const int page = a.page_table[(long long)r * a.max_pages + (place >> a.page_shift)];
+    const bool page_ok = page >= 0 && page < a.n_pages;
+
+    T *qd = static_cast<T *>(a.o) + (long long)row * a.Hq * a.hd;
+    const int in_page = place & ((1 << a.page_shift) - 1);
+    const long long at = (long long)page * a.page_stride + (long long)in_page * a.hd;
+    T *kd = static_cast<T *>(g.k_pages) + at;  // + head * page size * hd
+    T *vd = static_cast<T *>(g.v_pages) + at;
+
     auto store = [&](int base) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -176,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                 if (g.interleaved) {
 #pragma unroll
                     for (int e = 0; e < VE; e += 2) {
-                        const float2 c0 = cs[(v0 * VE + e) / 2], c1 = cs[(v1 * VE + e) / 2];
+                        const float2 c0 = cs[e / 2 * nr + v0], c1 = cs[e / 2 * nr + v1];
                         const float x0 = x[e], y0 = y[e];
                         x[e] = x0 * c0.x - x[e + 1] * c0.y;
                         x[e + 1] = x0 * c0.y + x[e + 1] * c0.x;
@@ -186,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                 } else {
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
-                        const float2 c = cs[v0 * VE + e];
+                        const float2 c = cs[e * (nr / 2) + v0];
                         const float x0 = x[e];
                         x[e] = x0 * c.x - y[e] * c.y;
                         y[e] = x0 * c.y + y[e] * c.x;
@@ -209,12 +232,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     };
 
-    load(0);
     const int pos = g.positions ? g.positions[row] : place;
-    for (int i = tid; i < g.rot / 2; i += kThreads) {
-        float2 c = turn(pos, g.inv_freq[i]);
-        cs[i] = make_float2(c.x * g.mscale, c.y * g.mscale);
+    if (tid < g.rot / 2) {
+        const float2 c = turn(pos, per_position);
+        // pair e of a vector's pairs: the vectors side by side
+        const int pairs = g.interleaved ? VE / 2 : VE, vectors = g.interleaved ? nr : nr / 2;
+        cs[tid % pairs * vectors + tid / pairs] = make_float2(c.x * g.mscale, c.y * g.mscale);
     }
+    if (!page_ok && tid == 0 && a.dev_err) atomicOr(a.dev_err, GDN_DEVERR_PAGE);
     __syncthreads();
     store(0);
     for (int base = kUnroll * kThreads; base < total; base += kUnroll * kThreads) {
