@@ -63,7 +63,7 @@ constexpr int kCleans = 8;  // value tiles between the warp that clears them and
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_half[2], p_ready[2], o_full, q_ready[2], clean[kCleans], joined, staged, drain;
+    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], clean[kCleans], joined, staged, drain;
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -417,22 +417,15 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
         }
         commit(lead, bar(s.b.s_full[w]));
     };
-    // The weights of keys 64 .. 127 are there first.
     auto output = [&](int w, uint32_t slot, bool first, uint32_t parity) -> bool {
         const uint32_t v = v_lo + slot * (C::kTile >> 4);
         const uint32_t acc = first ? 0u : 1u;
-        if (!wait(bar(s.b.p_half[w]), parity, &s.dead)) return false;
-        fence_after();
-#pragma unroll
-        for (int kk = kKT / 32; kk < kKT / 16; ++kk)
-            mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
-                   idesc(HD, true), kk > kKT / 32 ? 1u : acc);
         if (!wait(bar(s.b.p_ready[w]), parity, &s.dead)) return false;
         fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kKT / 32; ++kk)
+        for (int kk = 0; kk < kKT / 16; ++kk)
             mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
-                   idesc(HD, true), 1u);
+                   idesc(HD, true), kk > 0 ? 1u : acc);
         return true;
     };
     // The slot of the last segment's last values goes back to the ring when the warpgroups
@@ -764,9 +757,6 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 tmem_st32(ts + kP + half * 32, x);  // over scores that are not needed any more
             };
             weights(1);
-            wait_st();
-            fence_before();
-            arrive_warp(bar(s.b.p_half[w]));  // the products of the second half may begin
             scores(0, false);
             weights(0);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -928,7 +918,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
-            mbar_init(bar(s.b.p_half[w]), 4);
             mbar_init(bar(s.b.p_ready[w]), 4);
             mbar_init(bar(s.b.q_ready[w]), WIDE ? 4 : 8);
         }
