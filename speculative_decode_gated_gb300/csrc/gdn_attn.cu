@@ -19,7 +19,8 @@ namespace {
 
 constexpr int kRows = 16;   // query rows of a unit
 constexpr int kKeys = 32;   // places of a key tile
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kLanes = kThreads / kRows;  // threads a row
 constexpr int kAlign = 16;  // pages begin at multiples of it
 constexpr int kMaxParts = 48;  // joined by one block; more by a launch of their own
 constexpr int kMinTiles = 2;
@@ -36,150 +37,154 @@ struct Smem {
     int2 join;
 };
 
-// 16 bytes of a row -> floats in shared memory.
-template <typename T>
-__device__ __forceinline__ void put_vec(float *dst, const uint4 &w) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<uint4 *>(dst) = w;
-    } else {
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            dst[2 * e] = __uint_as_float(x[e] << 16);
-            dst[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
-        }
-    }
-}
-
-// Thread (row = tid / 8, sub = tid % 8) of the block: scores of keys sub + 8 i,
-// output columns 4 sub + 32 i.
-template <typename T, int HD>
+// float32.  Thread (row = tid / 16, sub = tid % 16) of the block: the scores of keys sub
+// and sub + 16, the output columns 4 sub + 64 u.  Bound by shared memory's reads: a float4 of
+// queries and two of keys for eight products.  A tile is on its way to registers while the
+// one before it is used.
+template <int HD>
 __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<HD> &s = *reinterpret_cast<Smem<HD> *>(raw);
-    constexpr int VE = 16 / (int)sizeof(T), VR = HD / VE;  // vectors of a row
+    constexpr int VR = HD / 4;                         // vectors of a row
+    constexpr int PER = kKeys * VR / kThreads;         // of a tile's keys (values) a thread
+    constexpr int NC = HD >= 64 ? 4 : 2;               // neighbouring output columns of a thread
+    constexpr int NO = HD / kLanes;                    // its output columns
     const int tid = threadIdx.x, c = blockIdx.x, P = gridDim.x;
-    const int row = tid >> 3, sub = tid & 7;
+    const int row = tid / kLanes, sub = tid % kLanes;
     Cursor cur = make_plan<kThreads, kRows, kKeys, kExtra, kMinTiles>(a, c, P, kAlign, &s.plan, c == 0);
     Segment g;
     bool any = false;
     while (next_segment<kRows, kKeys, kExtra>(a, kAlign, cur, g)) {
         any = true;
+        uint4 wk[PER], wv[PER];
+        auto fetch = [&](int i) {
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int x = tid + u * kThreads, kj = x / VR, e = x % VR * 4;
+                const int v = i * kKeys + kj, j = place_of(g.span, v);
+                wk[u] = wv[u] = make_uint4(0, 0, 0, 0);
+                if (!some_see(a, g.span, v, v)) continue;
+                const int page = a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
+                if (page >= 0 && page < a.n_pages) {
+                    const long long at =
+                        (long long)page * a.page_stride +
+                        (((long long)g.h << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * HD + e;
+                    wk[u] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.k) + at);
+                    wv[u] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.v) + at);
+                } else if (a.dev_err) {
+                    atomicOr(a.dev_err, GDN_DEVERR_PAGE);
+                }
+            }
+        };
+        fetch(g.i0);
         __syncthreads();  // the previous segment's tiles are no longer read
         const int rows = min(kRows, g.req.T * a.G - g.qt * kRows);
         for (int i = tid; i < kRows * VR; i += kThreads) {
-            const int ri = i / VR, e = i % VR * VE;
+            const int ri = i / VR, e = i % VR * 4, t = div_group(a, g.qt * kRows + ri);
             uint4 w = make_uint4(0, 0, 0, 0);
-            if (ri < rows) {
-                const int t = (g.qt * kRows + ri) / a.G, gh = (g.qt * kRows + ri) % a.G;
-                w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
+            if (ri < rows)
+                w = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) +
                                                      (g.req.row0 + t) * a.q_stride +
-                                                     (g.h * a.G + gh) * HD + e);
-            }
-            put_vec<T>(&s.q[ri][e], w);
+                                                     (g.h * a.G + g.qt * kRows + ri - t * a.G) * HD + e);
+            *reinterpret_cast<uint4 *>(&s.q[ri][e]) = w;
         }
         // this thread's row's own place, as numbered in the span
-        const int own = g.req.ctx + (g.qt * kRows + row) / a.G - g.span.shift;
-        float m = -INFINITY, l = 0.f, o[HD / 8] = {};
+        const int tok = div_group(a, g.qt * kRows + row);
+        const int own = g.req.ctx + tok - g.span.shift;
+        float m = -INFINITY, l = 0.f, o[NO] = {};
         for (int i = g.i0; i < g.i1; ++i) {
             const int v0 = i * kKeys;
-            __syncthreads();
-            for (int x = tid; x < kKeys * VR; x += kThreads) {
-                const int kj = x / VR, e = x % VR * VE, j = place_of(g.span, v0 + kj);
-                uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
-                if (some_see(a, g.span, v0 + kj, v0 + kj)) {
-                    const int page =
-                        a.page_table[(long long)g.r * a.max_pages + (j >> a.page_shift)];
-                    if (page >= 0 && page < a.n_pages) {
-                        const long long at =
-                            (long long)page * a.page_stride +
-                            (((long long)g.h << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * HD + e;
-                        wk = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k) + at);
-                        wv = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + at);
-                    } else if (a.dev_err) {
-                        atomicOr(a.dev_err, GDN_DEVERR_PAGE);
-                    }
-                }
-                put_vec<T>(&s.k[kj][e], wk);
-                put_vec<T>(&s.v[kj][e], wv);
+            if (i > g.i0) __syncthreads();
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int x = tid + u * kThreads, kj = x / VR, e = x % VR * 4;
+                *reinterpret_cast<uint4 *>(&s.k[kj][e]) = wk[u];
+                *reinterpret_cast<uint4 *>(&s.v[kj][e]) = wv[u];
             }
             __syncthreads();
-            float x[kKeys / 8] = {};
-#pragma unroll 4
+            if (i + 1 < g.i1) fetch(i + 1);
+            float x[2] = {};
+#pragma unroll 8
             for (int e = 0; e < HD; e += 4) {
                 const float4 qv = *reinterpret_cast<const float4 *>(&s.q[row][e]);
 #pragma unroll
-                for (int u = 0; u < kKeys / 8; ++u) {
-                    const float4 kv = *reinterpret_cast<const float4 *>(&s.k[sub + 8 * u][e]);
+                for (int u = 0; u < 2; ++u) {
+                    const float4 kv = *reinterpret_cast<const float4 *>(&s.k[sub + kLanes * u][e]);
                     x[u] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, x[u]))));
                 }
             }
-            float top = -INFINITY;
-            bool seen[kKeys / 8];
+            bool seen[2];
 #pragma unroll
-            for (int u = 0; u < kKeys / 8; ++u) {
-                seen[u] = row < rows && row_sees(a, g.span, own, v0 + sub + 8 * u);
+            for (int u = 0; u < 2; ++u) {
+                seen[u] = row < rows && row_sees(a, g.span, own, v0 + sub + kLanes * u);
                 x[u] = seen[u] ? x[u] * a.scale_log2 : -INFINITY;
-                top = fmaxf(top, x[u]);
             }
+            float top = fmaxf(x[0], x[1]);
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
             const float keep = exp2f(m - base);  // 0 while m = -inf
             float part = 0.f;
 #pragma unroll
-            for (int u = 0; u < kKeys / 8; ++u) {
-                const float e = exp2f(x[u] - base);
-                s.p[row][sub + 8 * u] = seen[u] ? e : 0.f;
-                part += seen[u] ? e : 0.f;
+            for (int u = 0; u < 2; ++u) {
+                const float e = seen[u] ? exp2f(x[u] - base) : 0.f;
+                s.p[row][sub + kLanes * u] = e;
+                part += e;
             }
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            for (int d = 1; d < kLanes; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
             l = l * keep + part;
             m = mn;
 #pragma unroll
-            for (int u = 0; u < HD / 8; ++u) o[u] *= keep;
-            __syncwarp();  // the row's scores come from threads of this warp only
+            for (int u = 0; u < NO; ++u) o[u] *= keep;
+            __syncwarp();  // the row's weights come from threads of this warp only
+#pragma unroll 8
             for (int kj = 0; kj < kKeys; ++kj) {
                 const float p = s.p[row][kj];
-                if (p == 0.f) continue;  // a hidden place adds nothing, whatever v holds there
+                const bool adds = p != 0.f;  // a hidden place adds nothing, whatever v holds there
 #pragma unroll
-                for (int u = 0; u < HD / 32; ++u) {
-                    const float4 vv = *reinterpret_cast<const float4 *>(&s.v[kj][4 * sub + 32 * u]);
-                    o[4 * u] = fmaf(p, vv.x, o[4 * u]);
-                    o[4 * u + 1] = fmaf(p, vv.y, o[4 * u + 1]);
-                    o[4 * u + 2] = fmaf(p, vv.z, o[4 * u + 2]);
-                    o[4 * u + 3] = fmaf(p, vv.w, o[4 * u + 3]);
+                for (int u = 0; u < NO; u += NC) {
+                    const float *v = &s.v[kj][NC * sub + kLanes * u];
+                    float y[NC];
+                    if constexpr (NC == 4)
+                        *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(v);
+                    else
+                        *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(v);
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) o[u + e] = adds ? fmaf(p, y[e], o[u + e]) : o[u + e];
                 }
             }
             __syncwarp();
         }
+        const bool whole = g.i0 == 0 && g.i1 == g.span.n;
         if (row < rows) {
-            if (g.i0 == 0 && g.i1 == g.span.n) {
-                const int t = (g.qt * kRows + row) / a.G, gh = (g.qt * kRows + row) % a.G;
-                const long long at = (long long)(g.req.row0 + t) * a.Hq + g.h * a.G + gh;
-                const float inv = 1.f / l;
+            const long long at = (long long)(g.req.row0 + tok) * a.Hq + g.h * a.G +
+                                 (g.qt * kRows + row - tok * a.G);
+            const float inv = whole ? 1.f / l : 1.f;
+            float *part = a.part + (long long)part_slot(c, g) * kRows * (HD + 2);
 #pragma unroll
-                for (int u = 0; u < HD / 8; u += 4)
-                    put(static_cast<T *>(a.o) + at * HD + 4 * sub + 8 * u,
-                        make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv));
-                if (a.lse && sub == 0) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
-            } else {
-                float *dst = a.part + (long long)part_slot(c, g) * kRows * (HD + 2);
-#pragma unroll
-                for (int u = 0; u < HD / 8; u += 4)
-                    *reinterpret_cast<float4 *>(dst + part_at<kRows>(row, 4 * sub + 8 * u)) =
-                        make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
-                if (sub == 0) {
-                    dst[kRows * HD + row] = m;
-                    dst[kRows * HD + kRows + row] = l;
+            for (int u = 0; u < NO; u += NC) {
+                const int col = NC * sub + kLanes * u;
+                float *dst = whole ? static_cast<float *>(a.o) + at * HD + col
+                                   : part + part_at<kRows>(row, col);
+                if constexpr (NC == 4)
+                    put(dst, make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv));
+                else
+                    *reinterpret_cast<float2 *>(dst) = make_float2(o[u] * inv, o[u + 1] * inv);
+            }
+            if (sub == 0) {
+                if (!whole) {
+                    part[kRows * HD + row] = m;
+                    part[kRows * HD + kRows + row] = l;
+                } else if (a.lse) {
+                    a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
         }
-        if (a.count && !(g.i0 == 0 && g.i1 == g.span.n))
-            join_if_last<T, kRows, HD, kThreads>(a, c, g, cur.x, cur.N, cur.P, &s.join);
+        if (a.count && !whole)
+            join_if_last<float, kRows, HD, kThreads>(a, c, g, cur.x, cur.N, cur.P, &s.join);
     }
     if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, cur.N, cur.P);
 }
@@ -246,9 +251,9 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs
 
 template <int HD>
 cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<attn_simple_kernel<float, HD>>((int)sizeof(Smem<HD>));
+    const cudaError_t e = allow_smem<attn_simple_kernel<HD>>((int)sizeof(Smem<HD>));
     if (e != cudaSuccess) return e;
-    return launch(attn_simple_kernel<float, HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a,
+    return launch(attn_simple_kernel<HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a,
                   stream);
 }
 

@@ -443,8 +443,9 @@ __device__ __forceinline__ void join_if_last(const AttnArgs &a, int c, const Seg
     const int first = shared->x, last = shared->y;
     if (first < 0) return;
     __threadfence();
-    constexpr int PER = ROWS * HD / 4 / NT, CSTEP = NT / ROWS;
+    constexpr int PER = ROWS * HD / 4 > NT ? ROWS * HD / 4 / NT : 1, CSTEP = NT / ROWS;
     const int row = tid % ROWS, cg = tid / ROWS;
+    if (cg >= HD / 4) return;  // more threads than vectors
     Partial<PER> s;
     add_partials<ROWS, HD, PER, CSTEP>(a, s, first, first, 1, last, row, cg);
     const int i = g.qt * ROWS + row;
