@@ -369,7 +369,8 @@ typedef struct gdn_rope {
  * to its place in the pages.
  *   q      device [N_tok][q_heads][head_dim], q_stride elements from a row to the next
  *   k, v   device [N_tok][kv_heads][head_dim], k_stride and v_stride elements apart
- *          (strides >= the row, multiples of 16 bytes: slices of one projection's output)
+ *          (strides >= the row, multiples of 16 bytes, at most 2^36: slices of one
+ *          projection's output)
  *   q_out  device [N_tok][q_heads][head_dim], contiguous; overlaps nothing else of the call
  * All 16-byte aligned.  A request with a bad kv_len or bad row offsets is skipped; a row
  * whose page id is outside [0, n_pages) gets its q_out and sets GDN_DEVERR_PAGE.  No two rows

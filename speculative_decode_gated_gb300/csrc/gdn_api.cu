@@ -413,7 +413,7 @@ AttnRanges attn_ranges(const gdn_attn *p) {
 
 // Whether rows of `row` elements, `stride` apart, are well formed; the bytes they span.
 bool stride_ok(const gdn_attn *p, int64_t stride, int64_t row) {
-    return stride >= row && stride <= (1ll << 40) && stride * attn_esz(p) % 16 == 0;
+    return stride >= row && stride <= (1ll << 36) && stride * attn_esz(p) % 16 == 0;
 }
 Range rows_range(const gdn_attn *p, const void *ptr, int64_t stride, int64_t row) {
     const int64_t n = attn_rows(p);

@@ -63,7 +63,7 @@ constexpr int kCleans = 8;  // value tiles between the warp that clears them and
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], clean[kCleans], joined, staged, drain;
+    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], q_free[2], clean[kCleans], joined, staged, drain;
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -245,7 +245,8 @@ __device__ __forceinline__ int box_rows(const AttnArgs &a) { return min(1 << a.p
 
 struct Launch {
     AttnArgs a;
-    CUtensorMap k, v;
+    CUtensorMap k, v, q;
+    int q_tma;  // the queries come by TMA too: a power of two of heads a group, up to 128
 };
 
 // A ring slot and the parity of its round; advances through the ring.
@@ -302,8 +303,8 @@ constexpr int kSegReaders = 8 + 1 + 1 + 1;  // arrivals a slot: softmax, TMA, MM
 // ---------------------------------------------------------------- the TMA warp
 
 template <int HD, bool WIDE>
-__device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t ring, int lane,
-                                          uint32_t &issued) {
+__device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring, int lane,
+                                          uint32_t &issued, uint32_t &seg) {
     using C = Cfg<HD>;
     const AttnArgs &a = L.a;
     const int rows_box = box_rows(a);
@@ -335,6 +336,27 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
         }
         at.next();
         ++issued;
+        return true;
+    };
+    // The queries of segment `seg`, a 128-row tile (or two): rows of (token, head of the group).
+    // Rows past the request's are other tokens', or zeros: their results are not used.
+    auto queries = [&]() -> bool {
+        constexpr int kTiles = WIDE ? 2 : 1, kBuffers = WIDE ? 1 : 2;
+        const uint32_t b = WIDE ? 0 : seg & 1;
+        // the buffer's last user has computed its last scores
+        if (seg >= kBuffers && !wait(bar(s.b.q_free[b]), (seg / kBuffers - 1) & 1, &s.dead)) return false;
+        if (lane == 0) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const uint32_t r = bar(s.b.q_ready[WIDE ? t : b]), dst = qbuf + (WIDE ? t : b) * C::kTile;
+                const int token = g.req.row0 + div_group(a, g.qt * (128 * kTiles) + t * 128);
+                arrive_expect(r, C::kTile);
+#pragma unroll
+                for (int h = 0; h < HD / 64; ++h)
+                    tma_4d(dst + h * C::kBox, &L.q, 64 * h, 0, g.h, token, r);
+            }
+        }
+        __syncwarp();
         return true;
     };
     // Pages are looked up a tile ahead, across segments too.
@@ -369,6 +391,10 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t r
         };
         if (!keys()) return;
         if (!WIDE && g.i1 - g.i0 > 1 && !keys()) return;
+        if (L.q_tma) {
+            if (!queries()) return;
+            ++seg;
+        }
         for (int i = g.i0; i < g.i1; ++i) {
             if (!values()) return;
             if (i + (WIDE ? 1 : 2) < g.i1 && !keys()) return;
@@ -458,6 +484,7 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
                 commit(lead, bar(s.b.empty[ks]));
             }
         }
+        if (n <= (WIDE ? 1 : 2)) commit(lead, bar(s.b.q_free[WIDE ? 0 : seg & 1]));
         if (!give_back()) return;
         for (int i = 0; i < n; ++i) {
             if (!next_values(vs)) return;
@@ -472,6 +499,7 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
                     commit(lead, bar(s.b.empty[vs]));
                     scores(1, ks);
                     commit(lead, bar(s.b.empty[ks]));
+                    if (i + 2 == n) commit(lead, bar(s.b.q_free[0]));
                 } else {  // both at once: the outputs are staged over the values
                     commit(lead, bar(s.b.o_full));
                 }
@@ -486,6 +514,7 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
                     if (!next_slot(ks)) return;
                     scores(w, ks);
                     commit(lead, bar(s.b.empty[ks]));
+                    if (i + 3 == n) commit(lead, bar(s.b.q_free[seg & 1]));
                 }
             }
         }
@@ -648,7 +677,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     uint32_t base_slot = 0;  // ring slot of the segment's first tile
     if (tid == 0) write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);  // nothing left unfinished yet
     const Segment *ahead = segs.peek(s);
-    if (ahead) {
+    if (ahead && !L.q_tma) {
         load_queries(*ahead, 0);
         queries_ready(0);
     }
@@ -662,7 +691,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         const int row = g.qt * ROWS + (WIDE ? w * 128 : 0) + t;
         const int own = g.req.ctx + div_group(a, row) - sp.shift;  // its place, as numbered in the span
         bool q_pending = false;
-        if (!WIDE && ahead) {  // the other buffer is free: the last segment is done with it
+        if (!WIDE && ahead && !L.q_tma) {  // the other buffer is free: the last segment is done with it
             load_queries(*ahead, seg + 1);
             q_pending = true;
         }
@@ -673,7 +702,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             const bool full = all_see(a, sp, v0, v0 + kKT - 1);
             if (!wait(bar(s.b.s_full[w]), n_s++ & 1, &s.dead)) return;
             fence_after();
-            if (WIDE && i + 1 == n && ahead) {  // this warpgroup's queries are no longer read
+            if (WIDE && i + 1 == n && ahead && !L.q_tma) {  // this warpgroup's queries are no longer read
                 load_queries(*ahead, seg + 1);
                 q_pending = true;
             }
@@ -919,7 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
             mbar_init(bar(s.b.p_ready[w]), 4);
-            mbar_init(bar(s.b.q_ready[w]), WIDE ? 4 : 8);
+            mbar_init(bar(s.b.q_ready[w]), L.q_tma ? 1 : WIDE ? 4 : 8);
+            mbar_init(bar(s.b.q_free[w]), 1);
         }
         for (int i = 0; i < kCleans; ++i) mbar_init(bar(s.b.clean[i]), 1);
         mbar_init(bar(s.b.o_full), 1);
@@ -953,12 +983,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (warp < 8) {
         softmax_role<HD, WIDE>(L, s, qbuf, ring, tm, cur);
     } else if (warp == 8) {
-        uint32_t issued = 0;
-        load_role<HD, WIDE>(L, s, ring, tid & 31, issued);
+        uint32_t issued = 0, queries = 0;
+        load_role<HD, WIDE>(L, s, qbuf, ring, tid & 31, issued, queries);
         // Every copy has landed before the block ends (the roles waited for them
         // unless one gave up).
         for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
             wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
+        for (uint32_t p = queries > 2 ? queries - 2 : 0; s.dead && p < queries; ++p)
+            for (int w = 0; w < 2; ++w)
+                if (WIDE || w == (int)(p & 1))
+                    wait_parity(bar(s.b.q_ready[w]), (WIDE ? p : p >> 1) & 1);
     } else if (warp == 9) {
         mma_role<HD, WIDE>(s, qbuf, ring, tm);
         commit(elect(), bar(s.b.drain));
@@ -1009,12 +1043,28 @@ bool encode_pages(CUtensorMap *map, const AttnArgs &a, const void *base) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [n_tok][kv_heads][group][hd], rows q_stride apart; boxes of 64 columns by 128 rows
+// (token, head of one group).
+bool encode_queries(CUtensorMap *map, const AttnArgs &a) {
+    const cuuint64_t dims[4] = {(cuuint64_t)a.hd, (cuuint64_t)a.G, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_tok};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.G * a.hd * 2,
+                                   (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.G, 1, (cuuint32_t)(128 / a.G)};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.q), dims, strides,
+                     box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD, bool WIDE>
 cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     Launch L;
     L.a = a;
     if (!encoder() || !encode_pages(&L.k, a, a.k) || !encode_pages(&L.v, a, a.v))
         return cudaErrorInvalidValue;
+    L.q_tma = (a.G & (a.G - 1)) == 0 && a.G <= 128;
+    if (L.q_tma && !encode_queries(&L.q, a)) return cudaErrorInvalidValue;
     constexpr int smem = Cfg<HD>::kTiles + (int)sizeof(Shared);
     static_assert(smem <= 232448, "227 KB of shared memory a block");
     const cudaError_t e = allow_smem<attn_tc_kernel<HD, WIDE>>(smem);
