@@ -1,22 +1,20 @@
 // Attention over a paged cache on the tensor cores (tcgen05): drafts of many
 // query rows a key head, and prompt chunks (bf16, heads of 64 and 128).
 //
-// One block an SM, on tiles of 128 places.  A lane-parallel TMA
-// warp streams keys and values, page by page, into a ring in shared memory
-// (128-byte swizzle; a page that no row needs, or that does not exist, is asked
-// for past the tensor's end and reads as zeros without traffic).  One thread
+// A lane-parallel TMA warp streams keys and values, page by page, into a ring in
+// shared memory (128-byte swizzle; a page that no row needs, or that does not exist, is
+// asked for past the tensor's end and reads as zeros without traffic).  One thread
 // issues the products: S = Q K^T with both operands in shared memory, O += P V with
-// the weights P in tensor memory.  Two warpgroups do the softmax, a thread a row,
-// each with its own S and O in tensor memory, so that the tensor cores work for
-// one while the other is between its products:
+// the weights P in tensor memory.  A warpgroup does the softmax of 128 rows, a thread a
+// row, with its S and O in tensor memory.
 //
-//   WIDE (prompt chunks): a unit is 256 rows, 128 a warpgroup; both use each key
-//     tile.  Bound by the tensor cores: 2 * 128^2 * HD * 2 flops a tile and
-//     warpgroup.
-//   otherwise (drafts, up to 128 rows a key head): both warpgroups have the same
-//     128 rows and take the key tiles in turn, and their results are joined at the
-//     end of a segment.  Bound by the cache's bytes; rows that are not there cost
-//     tensor time that the stream leaves over.
+//   Prompt chunks: two warpgroups, 256 rows of a unit, one block an SM, tiles of 128
+//     places that both use.  The tensor cores work for one warpgroup while the other is
+//     between its products.  Bound by the tensor cores: 2 * 128^2 * HD * 2 flops a
+//     tile and warpgroup.
+//   Drafts, up to 128 rows a key head: one warpgroup, tiles of 16 KB, two blocks an
+//     SM, so that one streams while the other ends a unit.  Bound by the cache's bytes;
+//     rows that are not there cost tensor time that the stream leaves over.
 //
 // A row's maximum is replaced, and its output rescaled in tensor memory, only
 // when it has grown by more than 2^8 (kLazy): the weights then stay below 2^8,
@@ -42,28 +40,33 @@
 namespace gdn {
 namespace {
 
-constexpr int kKT = 128;       // places of a tile
-constexpr int kThreads = 384;  // two softmax warpgroups; the TMA, MMA, segment and clearing warps
 constexpr int kSegs = 4;       // segments known ahead
-// A unit's start and end, in tiles.
-constexpr int kExtraWide = 4, kExtraDrafts = 2;
 constexpr float kLazy = 8.f;
-constexpr uint32_t kP = 64;    // TMEM column of P_w within S_w: two weights a column
 
-template <int HD>
+// NWG softmax warpgroups, then the TMA, MMA, segment and clearing warps.
+template <int HD, int NWG>
 struct Cfg {
-    static constexpr int kTile = kKT * HD * 2;     // bytes of a key (value, query) tile
-    static constexpr int kBox = kKT * 128;         // bytes of 64 of its columns
-    static constexpr int NS = HD == 128 ? 5 : 12;  // ring slots
-    static constexpr int kTiles = (2 + NS) * kTile;  // queries, ring
-    static constexpr uint32_t kO = 256;            // TMEM column of O_0 (S_0 at 0, S_1 at 128)
+    static constexpr int KT = NWG == 2 || HD == 64 ? 128 : 64;  // places of a tile
+    static constexpr int ROWS = 128 * NWG;             // rows of a unit
+    static constexpr int EXTRA = 4;                    // a unit's start and end, in tiles
+    static constexpr int kThreads = 128 * NWG + 128;
+    static constexpr int kBlocks = NWG == 2 ? 1 : 2;   // an SM
+    static constexpr int kTile = KT * HD * 2;          // bytes of a key (value) tile
+    static constexpr int kBox = KT * 128;              // bytes of 64 of its columns
+    static constexpr int kQTile = 128 * HD * 2, kQBox = 128 * 128;
+    static constexpr int NS = HD == 128 ? 5 : NWG == 2 ? 12 : 6;  // ring slots
+    static constexpr int kTiles = NWG * kQTile + NS * kTile;
+    // Columns of tensor memory.  Two weights are a column; P_w lies over the second half of
+    // S_w where the columns are all needed.
+    static constexpr uint32_t kCols = NWG == 2 ? 512 : 256;
+    static constexpr uint32_t kP = 64, kO = NWG == 2 ? 256 : 128;
 };
 
 constexpr int kCleans = 8;  // value tiles between the warp that clears them and their products
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], q_free[2], clean[kCleans], joined, staged, drain;
+    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], q_free, clean[kCleans], staged, drain;
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -73,7 +76,6 @@ struct Shared {
     uint32_t tmem;
     int dead;          // a wait gave up: every role leaves
     int poison[4];     // segment (mod 4) whose hidden places hold values that are not finite
-    float m[2][kKT], l[2][kKT];
     Segment seg[kSegs];  // r = -1: no more
 };
 
@@ -241,7 +243,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 }
 
 // Places of a TMA box: a page, or a tile's worth of one.
-__device__ __forceinline__ int box_rows(const AttnArgs &a) { return min(1 << a.page_shift, kKT); }
+__host__ __device__ __forceinline__ int box_rows(const AttnArgs &a, int kt) {
+    return 1 << a.page_shift < kt ? 1 << a.page_shift : kt;
+}
 
 struct Launch {
     AttnArgs a;
@@ -265,13 +269,12 @@ struct Ring {
 
 // Works out the worker's segments ahead of the roles that use them (each takes loads that
 // wait on one another).
-template <bool WIDE>
+template <typename C>
 __device__ __forceinline__ void segment_role(const AttnArgs &a, Shared &s, Cursor cur) {
     Ring<kSegs> ring;
     for (;;) {
         Segment g;
-        const bool more = next_segment<WIDE ? 256 : 128, kKT, WIDE ? kExtraWide : kExtraDrafts>(
-            a, box_rows(a), cur, g);
+        const bool more = next_segment<C::ROWS, C::KT, C::EXTRA>(a, box_rows(a, C::KT), cur, g);
         if (!more) g.r = -1;
         if (!wait_one(bar(s.b.seg_empty[ring.slot]), ring.parity ^ 1, &s.dead)) return;
         s.seg[ring.slot] = g;
@@ -298,24 +301,23 @@ struct SegReader {
         return true;
     }
 };
-constexpr int kSegReaders = 8 + 1 + 1 + 1;  // arrivals a slot: softmax, TMA, MMA, clearing warps
 
 // ---------------------------------------------------------------- the TMA warp
 
-template <int HD, bool WIDE>
+template <int HD, int NWG>
 __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring, int lane,
                                           uint32_t &issued, uint32_t &seg) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, NWG>;
     const AttnArgs &a = L.a;
-    const int rows_box = box_rows(a);
-    const int boxes = kKT / rows_box;
+    const int rows_box = box_rows(a, C::KT);
+    const int boxes = C::KT / rows_box;
     Ring<C::NS> at;
     SegReader segs;
     Segment g, gn;
     // This lane's page of tile i of a segment: its row and number, or n_pages (nothing
     // needed, or no page).
     auto page_of = [&](const Segment &q, int i, int &row) -> int {
-        const int v = i * kKT + lane * rows_box, j = place_of(q.span, v);
+        const int v = i * C::KT + lane * rows_box, j = place_of(q.span, v);
         row = j & ((1 << a.page_shift) - 1);
         if (lane >= boxes || !some_see(a, q.span, v, v + rows_box - 1)) return (int)a.n_pages;
         const int page = a.page_table[(long long)q.r * a.max_pages + (j >> a.page_shift)];
@@ -338,25 +340,24 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t q
         ++issued;
         return true;
     };
-    // The queries of segment `seg`, a 128-row tile (or two): rows of (token, head of the group).
-    // Rows past the request's are other tokens', or zeros: their results are not used.
+    // The queries of segment `seg`, 128 rows of (token, head of the group) a warpgroup.  Rows
+    // past the request's are other tokens', or zeros: their results are not used.
     auto queries = [&]() -> bool {
-        constexpr int kTiles = WIDE ? 2 : 1, kBuffers = WIDE ? 1 : 2;
-        const uint32_t b = WIDE ? 0 : seg & 1;
-        // the buffer's last user has computed its last scores
-        if (seg >= kBuffers && !wait(bar(s.b.q_free[b]), (seg / kBuffers - 1) & 1, &s.dead)) return false;
+        // the last segment has computed its last scores
+        if (seg > 0 && !wait(bar(s.b.q_free), (seg - 1) & 1, &s.dead)) return false;
         if (lane == 0) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const uint32_t r = bar(s.b.q_ready[WIDE ? t : b]), dst = qbuf + (WIDE ? t : b) * C::kTile;
-                const int token = g.req.row0 + div_group(a, g.qt * (128 * kTiles) + t * 128);
-                arrive_expect(r, C::kTile);
+            for (int w = 0; w < NWG; ++w) {
+                const uint32_t r = bar(s.b.q_ready[w]), dst = qbuf + w * C::kQTile;
+                const int token = g.req.row0 + div_group(a, g.qt * C::ROWS + w * 128);
+                arrive_expect(r, C::kQTile);
 #pragma unroll
                 for (int h = 0; h < HD / 64; ++h)
-                    tma_4d(dst + h * C::kBox, &L.q, 64 * h, 0, g.h, token, r);
+                    tma_4d(dst + h * C::kQBox, &L.q, 64 * h, 0, g.h, token, r);
             }
         }
         __syncwarp();
+        ++seg;
         return true;
     };
     // Pages are looked up a tile ahead, across segments too.
@@ -364,40 +365,22 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t q
     bool more = segs.next(s, g);
     if (more) next = page_of(g, g.i0, row_n);
     while (more) {
-        int p0 = 0, r0 = 0, p1 = 0, r1 = 0, held = 0;  // pages of tiles whose values are to come
-        int ik = g.i0;
+        int ik = g.i0, page = 0, row = 0;  // of the tile whose values are to come
         more = segs.next(s, gn);
         auto keys = [&]() -> bool {
-            const int page = next, row = row_n;
+            page = next;
+            row = row_n;
             if (++ik < g.i1)
                 next = page_of(g, ik, row_n);
             else if (more)
                 next = page_of(gn, gn.i0, row_n);
-            if (held++ == 0) {
-                p0 = page;
-                r0 = row;
-            } else {
-                p1 = page;
-                r1 = row;
-            }
             return issue(&L.k, page, row);
         };
-        auto values = [&]() -> bool {
-            const int page = p0, row = r0;
-            p0 = p1;
-            r0 = r1;
-            --held;
-            return issue(&L.v, page, row);
-        };
         if (!keys()) return;
-        if (!WIDE && g.i1 - g.i0 > 1 && !keys()) return;
-        if (L.q_tma) {
-            if (!queries()) return;
-            ++seg;
-        }
+        if (L.q_tma && !queries()) return;
         for (int i = g.i0; i < g.i1; ++i) {
-            if (!values()) return;
-            if (i + (WIDE ? 1 : 2) < g.i1 && !keys()) return;
+            if (!issue(&L.v, page, row)) return;
+            if (i + 1 < g.i1 && !keys()) return;
         }
         g = gn;
     }
@@ -405,14 +388,14 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, uint32_t q
 
 // ---------------------------------------------------------------- the MMA warp
 
-template <int HD, bool WIDE>
+template <int HD, int NWG>
 __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring,
                                          uint32_t tm) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, NWG>;
     Ring<C::NS> at;
     SegReader segs;
     const uint32_t lead = elect();
-    uint32_t seg = 0, np0 = 0, np1 = 0, staged = 0;
+    uint32_t seg = 0, tiles = 0, staged = 0;  // so far
     Ring<kCleans> clean;
     uint32_t held = 0;      // ring slot the softmax warpgroups stage their output in
     bool holding = false;
@@ -433,24 +416,22 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
         return ok;
     };
     auto scores = [&](int w, uint32_t slot) {
-        const uint32_t q = q_lo + (WIDE ? w : (seg & 1)) * (C::kTile >> 4);
-        const uint32_t k = k_lo + slot * (C::kTile >> 4);
+        const uint32_t q = q_lo + w * (C::kQTile >> 4), k = k_lo + slot * (C::kTile >> 4);
         fence_after();
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-            mma_ss(lead, tm + w * 128, q + off, k + off, idesc(128, false), kk > 0);
-        }
+        for (int kk = 0; kk < HD / 16; ++kk)
+            mma_ss(lead, tm + w * 128, q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
+                   k + (((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4), idesc(C::KT, false), kk > 0);
         commit(lead, bar(s.b.s_full[w]));
     };
-    auto output = [&](int w, uint32_t slot, bool first, uint32_t parity) -> bool {
+    auto output = [&](int w, uint32_t slot, bool first) -> bool {
         const uint32_t v = v_lo + slot * (C::kTile >> 4);
         const uint32_t acc = first ? 0u : 1u;
-        if (!wait(bar(s.b.p_ready[w]), parity, &s.dead)) return false;
+        if (!wait(bar(s.b.p_ready[w]), tiles & 1, &s.dead)) return false;
         fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + kP + kk * 8, v + kk * (2048 >> 4),
+        for (int kk = 0; kk < C::KT / 16; ++kk)
+            mma_ts(lead, tm + C::kO + w * 128, tm + w * 128 + C::kP + kk * 8, v + kk * (2048 >> 4),
                    idesc(HD, true), kk > 0 ? 1u : acc);
         return true;
     };
@@ -468,53 +449,28 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
         uint32_t ks, vs = 0;
         const int n = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
         if (!next_slot(ks)) return;
-        if (WIDE) {
-            if (!wait(bar(s.b.q_ready[0]), seg & 1, &s.dead)) return;
-            scores(0, ks);
-            if (!wait(bar(s.b.q_ready[1]), seg & 1, &s.dead)) return;
-            scores(1, ks);
-            commit(lead, bar(s.b.empty[ks]));
-        } else {
-            if (!wait(bar(s.b.q_ready[seg & 1]), (seg >> 1) & 1, &s.dead)) return;
-            scores(0, ks);
-            commit(lead, bar(s.b.empty[ks]));
-            if (n > 1) {
-                if (!next_slot(ks)) return;
-                scores(1, ks);
-                commit(lead, bar(s.b.empty[ks]));
-            }
+#pragma unroll
+        for (int w = 0; w < NWG; ++w) {
+            if (!wait(bar(s.b.q_ready[w]), seg & 1, &s.dead)) return;
+            scores(w, ks);
         }
-        if (n <= (WIDE ? 1 : 2)) commit(lead, bar(s.b.q_free[WIDE ? 0 : seg & 1]));
+        commit(lead, bar(s.b.empty[ks]));
+        if (n == 1) commit(lead, bar(s.b.q_free));
         if (!give_back()) return;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n; ++i, ++tiles) {
             if (!next_values(vs)) return;
-            if (WIDE) {
-                if (!output(0, vs, i == 0, np0++ & 1)) return;
+#pragma unroll
+            for (int w = 0; w < NWG; ++w) {
+                if (!output(w, vs, i == 0)) return;
+                const bool last = w == NWG - 1;
                 if (i + 1 < n) {
-                    if (!next_slot(ks)) return;
-                    scores(0, ks);
-                }
-                if (!output(1, vs, i == 0, np1++ & 1)) return;
-                if (i + 1 < n) {
-                    commit(lead, bar(s.b.empty[vs]));
-                    scores(1, ks);
-                    commit(lead, bar(s.b.empty[ks]));
-                    if (i + 2 == n) commit(lead, bar(s.b.q_free[0]));
-                } else {  // both at once: the outputs are staged over the values
-                    commit(lead, bar(s.b.o_full));
-                }
-            } else {
-                const int w = i & 1;
-                if (!output(w, vs, i < 2, (w ? np1++ : np0++) & 1)) return;
-                if (i + 1 < n)
-                    commit(lead, bar(s.b.empty[vs]));
-                else
-                    commit(lead, bar(s.b.o_full));
-                if (i + 2 < n) {
-                    if (!next_slot(ks)) return;
+                    if (w == 0 && !next_slot(ks)) return;
+                    if (last) commit(lead, bar(s.b.empty[vs]));
                     scores(w, ks);
-                    commit(lead, bar(s.b.empty[ks]));
-                    if (i + 3 == n) commit(lead, bar(s.b.q_free[seg & 1]));
+                    if (last) commit(lead, bar(s.b.empty[ks]));
+                    if (last && i + 2 == n) commit(lead, bar(s.b.q_free));
+                } else if (last) {  // all at once: the outputs are staged over the values
+                    commit(lead, bar(s.b.o_full));
                 }
             }
         }
@@ -528,12 +484,12 @@ __device__ __forceinline__ void mma_role(Shared &s, uint32_t qbuf, uint32_t ring
 
 // Hands each value tile on to its products.  It takes part in the release of every ring
 // slot, keys too: a wait on a barrier's parity is only right for one that has seen
-// the phase before, so no slot may come round twice without it.  In value tiles that hold places hidden from some
-// row, it first clears the places that no row sees, and the elements that are not finite
-// where only some rows see them.
-template <int HD, bool WIDE>
+// the phase before, so no slot may come round twice without it.  In value tiles that
+// hold places hidden from some row it first clears the places that no row sees, and
+// the elements that are not finite where only some rows see them.
+template <int HD, int NWG>
 __device__ __forceinline__ void clear_role(const Launch &L, Shared &s, uint32_t ring, int lane) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, NWG>;
     constexpr int CR = HD / 8;  // 16-byte chunks of a row
     const AttnArgs &a = L.a;
     Ring<C::NS> at;
@@ -550,15 +506,14 @@ __device__ __forceinline__ void clear_role(const Launch &L, Shared &s, uint32_t 
             return true;
         };
         if (!keys()) return;
-        if (!WIDE && n > 1 && !keys()) return;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             if (!wait(bar(s.b.full[at.slot]), at.parity, &s.dead)) return;
-            const int v0 = (g.i0 + i) * kKT;
-            if (!all_see(a, g.span, v0, v0 + kKT - 1)) {
+            const int v0 = (g.i0 + i) * C::KT;
+            if (!all_see(a, g.span, v0, v0 + C::KT - 1)) {
                 const uint32_t vt = ring + at.slot * C::kTile;
 #pragma unroll 1
-                for (int r = lane; r < kKT; r += 32) {
+                for (int r = lane; r < C::KT; r += 32) {
                     const int v = v0 + r;
                     if (all_see(a, g.span, v, v)) continue;
                     auto chunk = [&](int c) {
@@ -603,7 +558,7 @@ __device__ __forceinline__ void clear_role(const Launch &L, Shared &s, uint32_t 
             arrive_warp(bar(s.b.empty[at.slot]));
             clean.next();
             at.next();
-            if (i + (WIDE ? 1 : 2) < n && !keys()) return;
+            if (i + 1 < n && !keys()) return;
         }
         ++seg;
     }
@@ -613,11 +568,11 @@ __device__ __forceinline__ void clear_role(const Launch &L, Shared &s, uint32_t 
 
 // Adds the values that are not finite, at the places of the segment's masked
 // tiles that the row at number `own` sees, to output columns [col, col + 32).
-__device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, int own, int col,
+__device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, int kt, int own, int col,
                                            float *o) {
     for (int i = g.i0; i < g.i1; ++i) {
-        if (all_see(a, g.span, i * kKT, i * kKT + kKT - 1)) continue;
-        for (int v = i * kKT; v < (i + 1) * kKT; ++v) {
+        if (all_see(a, g.span, i * kt, i * kt + kt - 1)) continue;
+        for (int v = i * kt; v < (i + 1) * kt; ++v) {
             if (!some_see(a, g.span, v, v) || all_see(a, g.span, v, v) || !row_sees(a, g.span, own, v))
                 continue;
             const int j = place_of(g.span, v);
@@ -634,11 +589,11 @@ __device__ __noinline__ void add_unbounded(const AttnArgs &a, const Segment &g, 
     }
 }
 
-template <int HD, bool WIDE>
+template <int HD, int NWG>
 __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_t qbuf, uint32_t ring,
                                              uint32_t tm, const Cursor &plan) {
-    using C = Cfg<HD>;
-    constexpr int ROWS = WIDE ? 256 : 128;
+    using C = Cfg<HD, NWG>;
+    constexpr int ROWS = C::ROWS, KT = C::KT;
     constexpr int CR = HD / 8;  // 16-byte chunks of a row
     const AttnArgs &a = L.a;
     const int tid = threadIdx.x, w = tid >> 7, t = tid & 127, lane = tid & 31;
@@ -646,19 +601,18 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     const uint32_t ts = tm + w * 128 + lane_base, to = tm + C::kO + w * 128 + lane_base;
     SegReader segs;
 
-    // This thread's share of a segment's queries on their way to shared memory: sixteen
-    // (eight) threads a row, rows 128 / CR apart.
-    auto load_queries = [&](const Segment &q, uint32_t seg) {
-        constexpr int count = WIDE ? 128 : 64;
-        const int first = w * count, rows = q.req.T * a.G - q.qt * ROWS;
-        const uint32_t dst = qbuf + (WIDE ? w : (seg & 1)) * C::kTile;
+    // This thread's share of its warpgroup's queries on their way to shared memory (where TMA
+    // does not bring them): sixteen (eight) threads a row, rows 128 / CR apart.
+    auto load_queries = [&](const Segment &q) {
+        const int rows = q.req.T * a.G - q.qt * ROWS - w * 128;
+        const uint32_t dst = qbuf + w * C::kQTile;
         const int c = t % CR;
         const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.q) + q.h * a.G * HD + c * 8;
 #pragma unroll 4
-        for (int i = first + t / CR; i < first + count; i += 128 / CR) {
-            const int r = i & 127, row = q.qt * ROWS + i, tok = div_group(a, row);
-            const uint32_t at = dst + (c >> 3) * C::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            const bool has = i < rows;
+        for (int r = t / CR; r < 128; r += 128 / CR) {
+            const int row = q.qt * ROWS + w * 128 + r, tok = div_group(a, row);
+            const uint32_t at = dst + (c >> 3) * C::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const bool has = r < rows;
             const __nv_bfloat16 *src =
                 base + (has ? (q.req.row0 + tok) * a.q_stride + (row - tok * a.G) * HD : 0);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(src),
@@ -667,10 +621,10 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    auto queries_ready = [&](uint32_t seg) {
+    auto queries_ready = [&]() {
         asm volatile("cp.async.wait_all;\n" ::: "memory");
         fence_async();
-        arrive_warp(bar(s.b.q_ready[WIDE ? w : (seg & 1)]));
+        arrive_warp(bar(s.b.q_ready[w]));
     };
 
     uint32_t seg = 0, n_s = 0;
@@ -678,8 +632,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     if (tid == 0) write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);  // nothing left unfinished yet
     const Segment *ahead = segs.peek(s);
     if (ahead && !L.q_tma) {
-        load_queries(*ahead, 0);
-        queries_ready(0);
+        load_queries(*ahead);
+        queries_ready();
     }
     while (ahead) {
         const Segment &g = *ahead;
@@ -688,39 +642,33 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         ahead = segs.peek(s);
         const int n = g.i1 - g.i0;
         const TileSpan sp = g.span;
-        const int row = g.qt * ROWS + (WIDE ? w * 128 : 0) + t;
+        const int row = g.qt * ROWS + w * 128 + t;
         const int own = g.req.ctx + div_group(a, row) - sp.shift;  // its place, as numbered in the span
-        bool q_pending = false;
-        if (!WIDE && ahead && !L.q_tma) {  // the other buffer is free: the last segment is done with it
-            load_queries(*ahead, seg + 1);
-            q_pending = true;
-        }
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-        for (int i = WIDE ? 0 : w; i < n; i += WIDE ? 1 : 2) {
-            const int v0 = (g.i0 + i) * kKT;
-            const bool full = all_see(a, sp, v0, v0 + kKT - 1);
+        for (int i = 0; i < n; ++i) {
+            const int v0 = (g.i0 + i) * KT;
+            const bool full = all_see(a, sp, v0, v0 + KT - 1);
             if (!wait(bar(s.b.s_full[w]), n_s++ & 1, &s.dead)) return;
             fence_after();
-            if (WIDE && i + 1 == n && ahead && !L.q_tma) {  // this warpgroup's queries are no longer read
-                load_queries(*ahead, seg + 1);
-                q_pending = true;
+            if (i + 1 == n && ahead && !L.q_tma) {  // this warpgroup's queries are no longer read
+                load_queries(*ahead);
             }
             uint32_t x[64];
-            uint32_t mask[4];  // of the tile's places, those that the row sees
+            uint32_t mask[KT / 32];  // of the tile's places, those that the row sees
             if (!full) {
                 // number v0 + 32 q + e is bit e of mask[q]
                 const int hi = own - v0, lo = a.window ? hi - a.window : -1, sk = sp.sinks - v0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < KT / 32; ++q) {
                     // bits below x, of 32
                     auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
                     mask[q] = below(hi + 1 - 32 * q) &
                               (~below(lo + 1 - 32 * q) | below(sk - 32 * q));
                 }
             }
-            // The scores, half a row at a time: the second half stays in registers from
-            // the maximum to the weights, the first is read twice.
+            // The scores, 64 of a row at a time.  Of 128 the second half stays in registers from
+            // the maximum to the weights, and the first is read twice.
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             auto scores = [&](int half, bool masked) {
                 tmem_ld32(ts + half * 64, x);
@@ -745,20 +693,22 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             };
             scores(0, !full);
             maximum();
-            if (!full) {  // masked once: the second reading finds it so
-                tmem_st32(ts, x);
-                tmem_st32(ts + 32, x + 32);
-                wait_st();
+            if (KT == 128) {
+                if (!full) {  // masked once: the second reading finds it so
+                    tmem_st32(ts, x);
+                    tmem_st32(ts + 32, x + 32);
+                    wait_st();
+                }
+                scores(1, !full);
+                maximum();
             }
-            scores(1, !full);
-            maximum();
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
             if (__any_sync(0xffffffffu, top > m + kLazy)) {
                 const float mn = fmaxf(m, top);
                 const float keep = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
                 m = mn;
                 l *= keep;
-                if (i >= (WIDE ? 1 : 2)) {
+                if (i > 0) {
 #pragma unroll 1
                     for (int q = 0; q < HD / 32; ++q) {
                         uint32_t y[32];
@@ -783,21 +733,19 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
                     x[e / 2] = pack_bf16(y.x, y.y);
                 }
-                tmem_st32(ts + kP + half * 32, x);  // over scores that are not needed any more
+                tmem_st32(ts + C::kP + half * 32, x);  // over scores that are not needed any more
             };
-            weights(1);
-            scores(0, false);
+            if (KT == 128) {
+                weights(1);
+                scores(0, false);
+            }
             weights(0);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             wait_st();
             fence_before();
             arrive_warp(bar(s.b.p_ready[w]));
-            if (q_pending) {
-                queries_ready(seg + 1);
-                q_pending = false;
-            }
+            if (i + 1 == n && ahead && !L.q_tma) queries_ready();
         }
-        if (q_pending) queries_ready(seg + 1);
 
         // The end of the segment.
         if (!wait(bar(s.b.o_full), seg & 1, &s.dead)) return;
@@ -805,62 +753,31 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         const bool poisoned = *(volatile int *)&s.poison[seg & 3] == (int)seg;
         const bool whole = g.i0 == 0 && g.i1 == sp.n;
         const int rows = g.req.T * a.G;
-        float f0 = 1.f, f1 = 0.f;
-        uint32_t ta = to, tb = to;
-        if (!WIDE) {
-            // Join: each warpgroup writes half of the columns of both outputs.
-            s.m[w][t] = m;
-            s.l[w][t] = l;
-            arrive_warp(bar(s.b.joined));
-            if (!wait(bar(s.b.joined), 0, &s.dead)) return;
-            const float m0 = s.m[0][t], m1 = s.m[1][t];
-            m = fmaxf(m0, m1);
-            const float base = m == -INFINITY ? 0.f : m;
-            f0 = exp2_fast(m0 - base);
-            f1 = exp2_fast(m1 - base);
-            l = s.l[0][t] * f0 + s.l[1][t] * f1;
-            ta = tm + C::kO + lane_base;
-            tb = ta + 128;
-        }
         const float inv = whole ? 1.f / l : 1.f;
         float *part = a.part + (long long)part_slot(blockIdx.x, g) * ROWS * (HD + 2);
-        const int prow = WIDE ? w * 128 + t : t;
+        const int prow = w * 128 + t;
         // A finished unit's rows go through the slot of its last value tile, whose products
         // are done, so that whole lines are written: a warp's 32 rows, half of the columns
         // at a time.
         constexpr int NC = HD / 2, CPR = NC / 8;  // columns, chunks of a row
         // The segment's 2 n tiles took ring slots from base_slot on, this one the last.
         const uint32_t stage = ring + (base_slot + 2 * n - 1) % C::NS * C::kTile +
-                               (tid >> 5) * (C::kTile / 8);
+                               (tid >> 5) * (C::kTile / (4 * NWG));
         auto stage_at = [&](int r, int c) {
             return stage + r * NC * 2 + ((c ^ (CPR == 8 ? r & 7 : (r >> 1) & 3)) << 4);
         };
 #pragma unroll 1
-        for (int rd = WIDE ? 0 : w; rd < (WIDE ? 2 : w + 1); ++rd) {
+        for (int rd = 0; rd < 2; ++rd) {
 #pragma unroll 1
             for (int c = 0; c < NC; c += 32) {
                 const int col = rd * NC + c;
                 uint32_t y[32];
-                tmem_ld32(ta + col, y);
-                if (!WIDE) {
-                    wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f0);
-                    if (n > 1) {  // one tile: the second warpgroup had none
-                        uint32_t z[32];
-                        tmem_ld32(tb + col, z);
-                        wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            y[e] = __float_as_uint(fmaf(__uint_as_float(z[e]), f1, __uint_as_float(y[e])));
-                    }
-                } else {
-                    wait_ld();
-                }
+                tmem_ld32(to + col, y);
+                wait_ld();
                 if (poisoned) {
                     float o[32];
                     for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]);
-                    add_unbounded(a, g, own, col, o);
+                    add_unbounded(a, g, C::KT, own, col, o);
                     for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(o[e]);
                 }
                 if (whole) {
@@ -906,7 +823,7 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
         fence_before();
         fence_async();
         arrive_warp(bar(s.b.staged));
-        if (row < rows && (WIDE || w == 0)) {
+        if (row < rows) {
             if (!whole) {
                 part[ROWS * HD + prow] = m;
                 part[ROWS * HD + ROWS + prow] = l;
@@ -915,11 +832,6 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                 a.lse[(long long)(g.req.row0 + tok) * a.Hq + g.h * a.G + (row - tok * a.G)] =
                     (m + log2f(l)) * 0.69314718055994531f;
             }
-        }
-        if (!WIDE) {  // both outputs have been read: either may be written again
-            arrive_warp(bar(s.b.joined));
-            if (!wait(bar(s.b.joined), 1, &s.dead)) return;
-            fence_after();
         }
         base_slot = (base_slot + 2 * n) % C::NS;
         ++seg;
@@ -930,34 +842,33 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
     }
 }
 
-template <int HD, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Launch L) {
-    using C = Cfg<HD>;
-    constexpr int ROWS = WIDE ? 256 : 128;
+template <int HD, int NWG>
+__global__ void __launch_bounds__(Cfg<HD, NWG>::kThreads, Cfg<HD, NWG>::kBlocks)
+    attn_tc_kernel(const __grid_constant__ Launch L) {
+    using C = Cfg<HD, NWG>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char raw[];  // the tiles first: whole swizzle atoms
     Shared &s = *reinterpret_cast<Shared *>(raw + C::kTiles);
     const uint32_t base = smem_addr(raw);
-    const uint32_t qbuf = base, ring = base + 2 * C::kTile;
+    const uint32_t qbuf = base, ring = base + NWG * C::kQTile;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(bar(s.b.full[i]), 1);
             mbar_init(bar(s.b.empty[i]), 2);  // its products, and the clearing warp
         }
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NWG; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
             mbar_init(bar(s.b.p_ready[w]), 4);
-            mbar_init(bar(s.b.q_ready[w]), L.q_tma ? 1 : WIDE ? 4 : 8);
-            mbar_init(bar(s.b.q_free[w]), 1);
+            mbar_init(bar(s.b.q_ready[w]), L.q_tma ? 1 : 4);
         }
+        mbar_init(bar(s.b.q_free), 1);
         for (int i = 0; i < kCleans; ++i) mbar_init(bar(s.b.clean[i]), 1);
         mbar_init(bar(s.b.o_full), 1);
-        mbar_init(bar(s.b.joined), 8);
-        mbar_init(bar(s.b.staged), 8);
+        mbar_init(bar(s.b.staged), 4 * NWG);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(bar(s.b.seg_full[i]), 1);
-            mbar_init(bar(s.b.seg_empty[i]), kSegReaders);
+            mbar_init(bar(s.b.seg_empty[i]), 4 * NWG + 3);  // all but the segment warp
         }
         mbar_init(bar(s.b.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -966,49 +877,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&L.k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&L.v)) : "memory");
     }
-    if (warp == 9) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-                         smem_addr(&s.tmem))
+    constexpr int kFirst = 4 * NWG;  // the TMA warp, then the others
+    if (warp == kFirst + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                         smem_addr(&s.tmem)),
+                     "n"(C::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Cursor cur = make_plan<kThreads, ROWS, kKT, WIDE ? kExtraWide : kExtraDrafts, 1>(L.a, blockIdx.x, gridDim.x,
-                                                   box_rows(L.a), &s.plan, blockIdx.x == 0);
+    const Cursor cur = make_plan<C::kThreads, C::ROWS, C::KT, C::EXTRA, 1>(
+        L.a, blockIdx.x, gridDim.x, box_rows(L.a, C::KT), &s.plan, blockIdx.x == 0);
     __syncthreads();  // the barriers and the tensor memory's address
     fence_after();
     const uint32_t tm = *(volatile uint32_t *)&s.tmem;
 
-    if (warp < 8) {
-        softmax_role<HD, WIDE>(L, s, qbuf, ring, tm, cur);
-    } else if (warp == 8) {
+    if (warp < kFirst) {
+        softmax_role<HD, NWG>(L, s, qbuf, ring, tm, cur);
+    } else if (warp == kFirst) {
         uint32_t issued = 0, queries = 0;
-        load_role<HD, WIDE>(L, s, qbuf, ring, tid & 31, issued, queries);
+        load_role<HD, NWG>(L, s, qbuf, ring, tid & 31, issued, queries);
         // Every copy has landed before the block ends (the roles waited for them
         // unless one gave up).
         for (uint32_t p = issued > C::NS ? issued - C::NS : 0; p < issued; ++p)
             wait_parity(bar(s.b.full[p % C::NS]), (p / C::NS) & 1);
-        for (uint32_t p = queries > 2 ? queries - 2 : 0; s.dead && p < queries; ++p)
-            for (int w = 0; w < 2; ++w)
-                if (WIDE || w == (int)(p & 1))
-                    wait_parity(bar(s.b.q_ready[w]), (WIDE ? p : p >> 1) & 1);
-    } else if (warp == 9) {
-        mma_role<HD, WIDE>(s, qbuf, ring, tm);
+        for (int w = 0; s.dead && queries > 0 && w < NWG; ++w)
+            wait_parity(bar(s.b.q_ready[w]), (queries - 1) & 1);
+    } else if (warp == kFirst + 1) {
+        mma_role<HD, NWG>(s, qbuf, ring, tm);
         commit(elect(), bar(s.b.drain));
         wait_parity(bar(s.b.drain), 0);
-    } else if (warp == 10) {
-        if (tid == 10 * 32) segment_role<WIDE>(L.a, s, cur);
+    } else if (warp == kFirst + 2) {
+        if ((tid & 31) == 0) segment_role<C>(L.a, s, cur);
     } else {
-        clear_role<HD, WIDE>(L, s, ring, tid & 31);
+        clear_role<HD, NWG>(L, s, ring, tid & 31);
     }
     __syncwarp();
     fence_before();
     __syncthreads();
     if (tid == 0 && s.dead && L.a.dev_err) atomicOr(L.a.dev_err, GDN_DEVERR_TIMEOUT);
-    if (warp == 9) {
+    if (warp == kFirst + 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tm) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tm), "n"(C::kCols)
+                     : "memory");
     }
 }
 
@@ -1028,14 +940,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// Pages [n_pages][kv_heads][page][hd]; boxes of 64 columns by up to 128 places of one
-// head of one page.  Pages past the end read as zeros.
-bool encode_pages(CUtensorMap *map, const AttnArgs &a, const void *base) {
+// Pages [n_pages][kv_heads][page][hd]; boxes of 64 columns by up to a tile's places of
+// one head of one page.  Pages past the end read as zeros.
+bool encode_pages(CUtensorMap *map, const AttnArgs &a, const void *base, int kt) {
     const cuuint64_t page = 1ull << a.page_shift;
     const cuuint64_t dims[4] = {(cuuint64_t)a.hd, page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)a.hd * 2, page * a.hd * 2,
                                    (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(page < kKT ? page : kKT), 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows(a, kt), 1, 1};
     const cuuint32_t elem[4] = {1, 1, 1, 1};
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
                      strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1057,21 +969,22 @@ bool encode_queries(CUtensorMap *map, const AttnArgs &a) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, bool WIDE>
+template <int HD, int NWG>
 cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
+    using C = Cfg<HD, NWG>;
     Launch L;
     L.a = a;
-    if (!encoder() || !encode_pages(&L.k, a, a.k) || !encode_pages(&L.v, a, a.v))
+    if (!encoder() || !encode_pages(&L.k, a, a.k, C::KT) || !encode_pages(&L.v, a, a.v, C::KT))
         return cudaErrorInvalidValue;
     L.q_tma = (a.G & (a.G - 1)) == 0 && a.G <= 128;
     if (L.q_tma && !encode_queries(&L.q, a)) return cudaErrorInvalidValue;
-    constexpr int smem = Cfg<HD>::kTiles + (int)sizeof(Shared);
-    static_assert(smem <= 232448, "227 KB of shared memory a block");
-    const cudaError_t e = allow_smem<attn_tc_kernel<HD, WIDE>>(smem);
+    constexpr int smem = C::kTiles + (int)sizeof(Shared);
+    static_assert(C::kBlocks * (smem + 1024) <= 233472, "228 KB of shared memory an SM");
+    const cudaError_t e = allow_smem<attn_tc_kernel<HD, NWG>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kAttnTcWorkers);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(NWG == 2 ? kAttnTcWorkers : kAttnWorkers);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1079,14 +992,14 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<HD, WIDE>, L);
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<HD, NWG>, L);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tc(const AttnArgs &a, bool wide, cudaStream_t stream) {
-    if (a.hd == 64) return wide ? launch_tc<64, true>(a, stream) : launch_tc<64, false>(a, stream);
-    return wide ? launch_tc<128, true>(a, stream) : launch_tc<128, false>(a, stream);
+    if (a.hd == 64) return wide ? launch_tc<64, 2>(a, stream) : launch_tc<64, 1>(a, stream);
+    return wide ? launch_tc<128, 2>(a, stream) : launch_tc<128, 1>(a, stream);
 }
 
 }  // namespace gdn
