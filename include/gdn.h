@@ -390,8 +390,9 @@ GDN_API gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, cons
  *   lse  device float32 [N_tok][q_heads]: m + log(sum_j e_j), or NULL
  *   workspace  device, 16-byte aligned, at least gdn_paged_attn_workspace(p)
  *        bytes, zero when it is first used; one per stream.  Its first 16
- *        KB hold counters that every call leaves at zero; calls leave
- *        nothing else in it that a later call reads.
+ *        KB hold counters that every call leaves at zero (zero them again
+ *        after a GDN_DEVERR_TIMEOUT); calls leave nothing else in it that a
+ *        later call reads.
  * o, lse and the workspace overlap nothing else of the call.  Sums and the
  * softmax's statistics are 32-bit.  Keys and values at places that no row of a
  * request sees are never used, whatever they hold.  A request with a

@@ -189,32 +189,46 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
     if (tid == 0 && !a.count) write_desc(a, c, g, any, cur.x, cur.N, cur.P);
 }
 
-// Joins the partials of a unit that spans workers c .. last: block (c, y) its rows y * RB
-// on.  A thread takes PER column groups (of four) of a row, CL apart, four partials at a
-// time; the rows of a group lie side by side, so a warp reads whole lines.  SLICES threads
-// share a value's partials, added in the order of the workers and then of the slices.  Few
-// and large blocks: ten thousand of eight rows each took 15 us where these take 5.
+// Joins the partials of the units that several workers hold: block (u, y) the rows y * RB
+// on of the u-th of them.  A thread takes PER column groups (of four) of a row, CL apart, four
+// partials at a time; the rows of a group lie side by side, so a warp reads whole lines.
+// SLICES threads share a value's partials, added in the order of the workers and then of
+// the slices.  The calls that come here have few units and many partials to each: small
+// row blocks spread them over the SMs (16 drafts over 131072 places, 38 partials of
+// 128 rows for each of eight units: 65.9 us a call with 32 rows a block, 62.5 with 16, 60.9 with 8).
 template <int ROWS, int HD>
 struct Combine {
     static constexpr int kThreads = 512;
-    static constexpr int RB = ROWS < 32 ? ROWS : 32;
+    static constexpr int RB = 8;
     static constexpr int CL = HD == 256 ? 16 : 8;
     static constexpr int PER = HD / 4 / CL;
     static constexpr int SLICES = kThreads / (RB * CL);
-    static constexpr int kBlocks = ROWS / RB;
 };
 
 template <typename T, int ROWS, int HD>
-__global__ void __launch_bounds__(512) combine_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(512) combine_kernel(const __grid_constant__ AttnArgs a, int workers) {
     using C = Combine<ROWS, HD>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ __align__(16) unsigned char raw[sizeof(Partial<C::PER>) * (C::SLICES - 1) * C::RB * C::CL];
     Partial<C::PER>(*part)[C::RB * C::CL] = reinterpret_cast<Partial<C::PER>(*)[C::RB * C::CL]>(raw);
-    const int c = blockIdx.x;
+    // The unit of this block: the blockIdx.x-th worker that a unit to join begins in.
+    __shared__ int found[C::kThreads / 32], unit;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const bool begins = (int)threadIdx.x < workers && a.desc[2 * threadIdx.x].x >= 0;
+    const unsigned ballot = __ballot_sync(0xffffffffu, begins);
+    if (lane == 0) found[warp] = __popc(ballot);
+    if (threadIdx.x == 0) unit = -1;
+    __syncthreads();
+    int rank = __popc(ballot & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) rank += found[w];
+    if (begins && rank == (int)blockIdx.x) unit = threadIdx.x;
+    __syncthreads();
+    const int c = unit;
+    if (c < 0) return;
     const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
     const int last = d0.x, qt = d0.y, h = d0.z, row0 = d0.w, T_r = d1.x, rb = blockIdx.y * C::RB;
-    if (last < 0 || qt * ROWS + rb >= T_r * a.G) return;
+    if (qt * ROWS + rb >= T_r * a.G) return;
     const int item = threadIdx.x % (C::RB * C::CL), slice = threadIdx.x / (C::RB * C::CL);
     const int row = rb + item % C::RB, cg = item / C::RB, i = qt * ROWS + row;
     Partial<C::PER> s;
@@ -234,9 +248,9 @@ __global__ void __launch_bounds__(512) combine_kernel(const __grid_constant__ At
     if (a.lse && cg == 0) a.lse[at] = (s.m + log2f(s.l)) * 0.69314718055994531f;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs &a,
-                   cudaStream_t stream) {
+template <typename K, typename... More>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                   const AttnArgs &a, More... more) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -247,39 +261,41 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const AttnArgs
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
 template <int HD>
 cudaError_t launch_simple(const AttnArgs &a, cudaStream_t stream) {
     const cudaError_t e = allow_smem<attn_simple_kernel<HD>>((int)sizeof(Smem<HD>));
     if (e != cudaSuccess) return e;
-    return launch(attn_simple_kernel<HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>), a,
-                  stream);
+    return launch(attn_simple_kernel<HD>, dim3(kAttnWorkers), kThreads, sizeof(Smem<HD>),
+                  stream, a);
 }
 
-// The two launches of a call: finished units and partials, then the join.
+template <typename T, int ROWS, int HD>
+cudaError_t launch_combine(const AttnArgs &a, int workers, cudaStream_t stream) {
+    using C = Combine<ROWS, HD>;
+    const long long units = (long long)a.B * a.Hkv * (((long long)a.max_T * a.G + ROWS - 1) / ROWS);
+    return launch(combine_kernel<T, ROWS, HD>, dim3((unsigned)std::min<long long>(units, workers), ROWS / C::RB),
+                  C::kThreads, 0, stream, a, workers);
+}
+
+// The launches of a call: finished units and partials, then the join where the first
+// kernel does not do it.
 template <int HD>
-cudaError_t launch_hd(const AttnArgs &a, bool bf16, cudaStream_t stream) {
-    const AttnKind kind = attn_kind(bf16, HD, (long long)a.max_T * a.G);
-    const auto joined = [&](cudaError_t first, auto join, int workers, int blocks) {
-        return first != cudaSuccess ? first
-                                    : launch(join, dim3(workers, blocks), 512, 0, a, stream);
-    };
+cudaError_t launch_hd(const AttnArgs &a, AttnKind kind, cudaStream_t stream) {
     if constexpr (HD == 64 || HD == 128) {
-        if (kind == kAttnDrafts)
-            return joined(launch_attn_tc(a, false, stream), combine_kernel<__nv_bfloat16, 128, HD>,
-                          kAttnWorkers, Combine<128, HD>::kBlocks);
-        if (kind == kAttnWide)
-            return joined(launch_attn_tc(a, true, stream), combine_kernel<__nv_bfloat16, 256, HD>,
-                          kAttnTcWorkers, Combine<256, HD>::kBlocks);
+        if (kind == kAttnDrafts || kind == kAttnWide) {
+            const cudaError_t e = launch_attn_tc(a, kind == kAttnWide, stream);
+            if (e != cudaSuccess || a.count) return e;
+            return kind == kAttnWide ? launch_combine<__nv_bfloat16, 256, HD>(a, kAttnTcWorkers, stream)
+                                     : launch_combine<__nv_bfloat16, 128, HD>(a, kAttnWorkers, stream);
+        }
     }
     const cudaError_t e = kind == kAttnSimple ? launch_simple<HD>(a, stream) : launch_attn_rows(a, stream);
-    if (a.count) return e;
-    return kind == kAttnSimple ? joined(e, combine_kernel<float, 16, HD>, kAttnWorkers,
-                                        Combine<16, HD>::kBlocks)
-                               : joined(e, combine_kernel<__nv_bfloat16, 16, HD>, kAttnWorkers,
-                                        Combine<16, HD>::kBlocks);
+    if (e != cudaSuccess || a.count) return e;
+    return kind == kAttnSimple ? launch_combine<float, 16, HD>(a, kAttnWorkers, stream)
+                               : launch_combine<__nv_bfloat16, 16, HD>(a, kAttnWorkers, stream);
 }
 
 }  // namespace
@@ -287,16 +303,24 @@ cudaError_t launch_hd(const AttnArgs &a, bool bf16, cudaStream_t stream) {
 cudaError_t launch_attn(AttnArgs a, bool bf16, cudaStream_t stream) {
     // Few partials to a unit: the block that writes the last one joins them, and the second
     // launch is saved.  A request's key heads have equal work, so a unit spans at most
-    // workers / key heads (and a bit) of them, and no more than its tiles allow.
+    // workers / key heads (and a bit) of them, and no more than its tiles allow.  On the tensor
+    // cores a unit has many rows and a join is longer, so fewer partials are few; but with
+    // units enough to keep every fourth worker busy most units lie in one or two workers, whatever
+    // the bound says (64 requests' 16 drafts: 127.5 us joined by a launch, 124.5 so; 128 requests
+    // behind a window: 75 and 72).
     const AttnKind kind = attn_kind(bf16, a.hd, (long long)a.max_T * a.G);
-    const long long tiles = ((long long)a.max_pages << a.page_shift) / 32;
-    const long long parts = std::min<long long>(kAttnWorkers / a.Hkv, tiles / 2) + 2;
-    if (kind == kAttnDrafts || kind == kAttnWide || parts > kMaxParts) a.count = nullptr;
+    const bool tc = kind == kAttnDrafts || kind == kAttnWide;
+    const int workers = kind == kAttnWide ? kAttnTcWorkers : kAttnWorkers;
+    const int unit = kind == kAttnWide ? 256 : kind == kAttnDrafts ? 128 : 16;
+    const long long tiles = ((long long)a.max_pages << a.page_shift) / (tc ? 64 : 32);
+    const long long parts = std::min<long long>(workers / a.Hkv, tiles / 2) + 2;
+    const long long units = (long long)a.B * a.Hkv * (((long long)a.max_T * a.G + unit - 1) / unit);
+    if (parts > (tc ? 8 : kMaxParts) && !(tc && units * 4 >= workers)) a.count = nullptr;
     switch (a.hd) {
-        case 32: return launch_hd<32>(a, bf16, stream);
-        case 64: return launch_hd<64>(a, bf16, stream);
-        case 128: return launch_hd<128>(a, bf16, stream);
-        default: return launch_hd<256>(a, bf16, stream);
+        case 32: return launch_hd<32>(a, kind, stream);
+        case 64: return launch_hd<64>(a, kind, stream);
+        case 128: return launch_hd<128>(a, kind, stream);
+        default: return launch_hd<256>(a, kind, stream);
     }
 }
 

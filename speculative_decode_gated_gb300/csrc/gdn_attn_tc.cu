@@ -49,6 +49,7 @@ struct Cfg {
     static constexpr int KT = NWG == 2 || HD == 64 ? 128 : 64;  // places of a tile
     static constexpr int ROWS = 128 * NWG;             // rows of a unit
     static constexpr int EXTRA = 4;                    // a unit's start and end, in tiles
+    static constexpr int kMin = 6;                     // places of the line a worker has at least
     static constexpr int kThreads = 128 * NWG + 128;
     static constexpr int kBlocks = NWG == 2 ? 1 : 2;   // an SM
     static constexpr int kTile = KT * HD * 2;          // bytes of a key (value) tile
@@ -66,7 +67,7 @@ constexpr int kCleans = 8;  // value tiles between the warp that clears them and
 
 struct Bars {
     unsigned long long full[12], empty[12];
-    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], q_free, clean[kCleans], staged, drain;
+    unsigned long long s_full[2], p_ready[2], o_full, q_ready[2], q_free, clean[kCleans], staged, drain, joined[2];
     unsigned long long seg_full[kSegs], seg_empty[kSegs];
 };
 
@@ -76,6 +77,7 @@ struct Shared {
     uint32_t tmem;
     int dead;          // a wait gave up: every role leaves
     int poison[4];     // segment (mod 4) whose hidden places hold values that are not finite
+    int2 join[2];      // first (or -1) and last worker of a unit that a warpgroup is to join
     Segment seg[kSegs];  // r = -1: no more
 };
 
@@ -629,7 +631,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
 
     uint32_t seg = 0, n_s = 0;
     uint32_t base_slot = 0;  // ring slot of the segment's first tile
-    if (tid == 0) write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);  // nothing left unfinished yet
+    if (!a.count && tid == 0)  // nothing left unfinished yet
+        write_desc(a, blockIdx.x, s.seg[0], false, 0, 1, 1);
     const Segment *ahead = segs.peek(s);
     if (ahead && !L.q_tma) {
         load_queries(*ahead);
@@ -833,10 +836,71 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                     (m + log2f(l)) * 0.69314718055994531f;
             }
         }
+        if (a.count && !whole) {
+            // A unit of few partials: the warpgroup that writes the last one joins them, in the
+            // order of the workers, while the next segment streams in.
+            __threadfence();
+            arrive_warp(bar(s.b.joined[w]));
+            if (!wait(bar(s.b.joined[w]), 0, &s.dead)) return;
+            if (t == 0) {
+                // the unit's first tile on the line: a worker's range begins or ends in it
+                const long long begin = g.i0 > 0 ? plan.x - g.i0 : plan.x1 - g.i1;
+                const int first = worker_of(begin, plan.N, plan.P);
+                const int last = worker_of(begin + sp.n - 1, plan.N, plan.P);
+                int *count = a.count + first * NWG + w;
+                const bool all = atomicAdd(count, 1) == last - first;
+                if (all) *count = 0;  // for the next call
+                s.join[w] = make_int2(all ? first : -1, last);
+            }
+            arrive_warp(bar(s.b.joined[w]));
+            if (!wait(bar(s.b.joined[w]), 1, &s.dead)) return;
+            const int first = s.join[w].x, last = s.join[w].y;
+            if (first >= 0 && row < rows) {
+                __threadfence();
+                auto slot = [&](int k) {
+                    return a.part + (long long)(k == first ? 2 * k + 1 : 2 * k) * ROWS * (HD + 2);
+                };
+                float top = -INFINITY, total = 0.f;
+                for (int k = first; k <= last; ++k) top = fmaxf(top, __ldcg(slot(k) + ROWS * HD + prow));
+                const float base = top == -INFINITY ? 0.f : top;
+                const int tok = div_group(a, row);
+                const long long at = (long long)(g.req.row0 + tok) * a.Hq + g.h * a.G + (row - tok * a.G);
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    float o[32] = {};
+                    float sum = 0.f;
+#pragma unroll 2
+                    for (int k = first; k <= last; ++k) {
+                        const float *p = slot(k);
+                        const float f = exp2f(__ldcg(p + ROWS * HD + prow) - base);
+                        sum = fmaf(__ldcg(p + ROWS * HD + ROWS + prow), f, sum);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(
+                                p + part_at<ROWS>(prow, c + 4 * e)));
+                            o[4 * e] = fmaf(y.x, f, o[4 * e]);
+                            o[4 * e + 1] = fmaf(y.y, f, o[4 * e + 1]);
+                            o[4 * e + 2] = fmaf(y.z, f, o[4 * e + 2]);
+                            o[4 * e + 3] = fmaf(y.w, f, o[4 * e + 3]);
+                        }
+                    }
+                    total = sum;
+                    const float inv = 1.f / sum;
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * HD + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                            pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                            pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                            pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+                if (a.lse) a.lse[at] = (top + log2f(total)) * 0.69314718055994531f;
+            }
+        }
         base_slot = (base_slot + 2 * n) % C::NS;
         ++seg;
         // The last segment ends where the worker's range does.
-        if (!ahead && tid == 0)
+        if (!a.count && !ahead && tid == 0)
             write_desc(a, blockIdx.x, g, !s.dead, plan.x1, plan.N, plan.P);
         arrive_warp(bar(s.b.seg_empty[seg_slot]));
     }
@@ -860,6 +924,7 @@ __global__ void __launch_bounds__(Cfg<HD, NWG>::kThreads, Cfg<HD, NWG>::kBlocks)
         for (int w = 0; w < NWG; ++w) {
             mbar_init(bar(s.b.s_full[w]), 1);
             mbar_init(bar(s.b.p_ready[w]), 4);
+            mbar_init(bar(s.b.joined[w]), 4);
             mbar_init(bar(s.b.q_ready[w]), L.q_tma ? 1 : 4);
         }
         mbar_init(bar(s.b.q_free), 1);
@@ -887,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<HD, NWG>::kThreads, Cfg<HD, NWG>::kBlocks)
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Cursor cur = make_plan<C::kThreads, C::ROWS, C::KT, C::EXTRA, 1>(
+    const Cursor cur = make_plan<C::kThreads, C::ROWS, C::KT, C::EXTRA, C::kMin>(
         L.a, blockIdx.x, gridDim.x, box_rows(L.a, C::KT), &s.plan, blockIdx.x == 0);
     __syncthreads();  // the barriers and the tensor memory's address
     fence_after();
