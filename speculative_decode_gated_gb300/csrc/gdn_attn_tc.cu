@@ -58,8 +58,8 @@ struct Cfg {
     static constexpr int KT = NWG == 2 || HD == 64 ? 128 : 64;  // places of a tile
     static constexpr int ROWS = 128 * NWG;             // rows of a unit
     // A unit's start and end, in tiles, and the places of the line that a worker has at least.
-    // With 2 or 9 tiles the drafts and prompts measured stay within 3%, with 1 or 12 heads
-    // of 64 lose 14% (3829 rows: 353 us, 403 and 401).  With 10, 16 or 24 places the smallest
+    // With 2 tiles the drafts and prompts measured stay within 3%; with 1 or 12 heads of 64
+    // lose 14% (3829 rows: 353 us, 403 and 401).  With 10, 16 or 24 places the smallest
     // calls lose 3 to 14 us (13 requests of up to 32 rows over 640 places: 16 us, 19, 23 and 27).
     static constexpr int EXTRA = 4, kMin = 6;
     static constexpr int kThreads = 128 * NWG + 128;
