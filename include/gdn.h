@@ -395,9 +395,12 @@ GDN_API gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, cons
  *        later call reads.
  * o, lse and the workspace overlap nothing else of the call.  Sums and the
  * softmax's statistics are 32-bit.  Keys and values at places that no row of a
- * request sees are never used, whatever they hold.  A request with a
- * bad kv_len or bad row offsets is skipped (nothing is written for it); a page
- * whose id is outside [0, n_pages) sets GDN_DEVERR_PAGE and reads as zeros. */
+ * request sees are never used, whatever they hold.  An infinite value at a place
+ * that a row sees makes that element of the row's output infinite; a NaN, or
+ * infinities of both signs, make it NaN, and so may an infinite value whose
+ * weight is below 2^-126.  A request with a bad kv_len or bad row offsets is
+ * skipped (nothing is written for it); a page whose id is outside [0, n_pages)
+ * sets GDN_DEVERR_PAGE and reads as zeros. */
 GDN_API gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, void *o,
                                   float *lse, void *workspace, int64_t workspace_bytes,
                                   cudaStream_t stream);

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float e = seen[u] ? exp2f(x[u] - base) : 0.f;
-                s.p[row][sub + kLanes * u] = e;
+                s.p[row][sub + kLanes * u] = seen[u] ? e : -1.f;  // no weight is negative
                 part += e;
             }
 #pragma unroll
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) attn_simple_kernel(const __grid_cons
 #pragma unroll 8
             for (int kj = 0; kj < kKeys; ++kj) {
                 const float p = s.p[row][kj];
-                const bool adds = p != 0.f;  // a hidden place adds nothing, whatever v holds there
+                const bool adds = !(p < 0.f);  // a hidden place adds nothing, whatever v holds there
 #pragma unroll
                 for (int u = 0; u < NO; u += NC) {
                     const float *v = &s.v[kj][NC * sub + kLanes * u];

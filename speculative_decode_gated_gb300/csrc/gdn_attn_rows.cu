@@ -15,10 +15,11 @@
 // The products are mma.sync m16n8k16: 16 rows fill its M, where a 128-row
 // tcgen05 tile would be seven eighths padding, and the fragments of the scores
 // are those of the weights, so nothing goes through memory in between.  The
-// weights enter the second product as two bf16 terms (w = hi + lo, 2^-17 w
+// weights enter the second product as two bf16 terms (w = hi + lo, 2^-16 w
 // left): the tensor cores have the time while the cache streams, and the result
 // is then as exact as one with float32 weights (error against 64 bits 0.0017, that of the
-// rounded output alone).
+// rounded output alone).  hi is w cut off, so that lo is not negative, and lo of a weight
+// that is not zero is kept above zero: both terms of an infinite value then have its sign.
 //
 // Measured: 64 requests' single tokens over contexts of up to 8191 places, 8 key heads
 // of 128: 1.33 GB in 207 us, 6.4 TB/s, 94% of a plain copy's rate, with the tensor pipe
@@ -98,6 +99,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The two bf16 terms of weights x, y >= 0 (or NaN).  lo is raised to 2^-126, of which no more
+// than that part of a value is added; it stays 0 for a weight of 0.
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t &hi, uint32_t &lo) {
+    constexpr float kTiny = 0x1p-126f;
+    hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    lo = pack_bf16(fmaxf(x - __uint_as_float(hi << 16), fminf(x, kTiny)),
+                   fmaxf(y - __uint_as_float(hi & 0xFFFF0000u), fminf(y, kTiny)));
 }
 
 // Whether one of the two bf16 is infinite or NaN.
@@ -298,7 +308,8 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                     l[e >> 1] += s[n][e];
                 }
             // Where some rows must not see a value that is not finite, a product with
-            // its zero weight would still be NaN: such tiles are added value by value.
+            // its zero weight would still be NaN: such tiles are added value by value, to the rows
+            // that see it.
             bool odd = false;
             if (!full) {
 #pragma unroll
@@ -312,12 +323,8 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
             if (!odd) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = s[e >> 1][(e & 1) * 2], y = s[e >> 1][(e & 1) * 2 + 1];
-                    hi[e] = pack_bf16(x, y);
-                    lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16),
-                                      y - __uint_as_float(hi[e] & 0xFFFF0000u));
-                }
+                for (int e = 0; e < 4; ++e)
+                    split_weights(s[e >> 1][(e & 1) * 2], s[e >> 1][(e & 1) * 2 + 1], hi[e], lo[e]);
 #pragma unroll
                 for (int n = 0; n < HD / 16; ++n) {
                     uint32_t b[4];
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                     const int from = (lane & ~3) | ((j & 7) >> 1);
                     const float p0 = __shfl_sync(0xffffffffu, s[j >> 3][j & 1], from);
                     const float p1 = __shfl_sync(0xffffffffu, s[j >> 3][2 + (j & 1)], from);
+                    const bool adds[2] = {row_sees(a, sp, own[0], v0 + j), row_sees(a, sp, own[1], v0 + j)};
 #pragma unroll
                     for (int n = 0; n < HD / 8; ++n) {
                         uint32_t v;
@@ -340,14 +348,14 @@ __global__ void __launch_bounds__(Cfg<HD>::NT, 2) attn_rows_kernel(const __grid_
                                      : "=r"(v)
                                      : "r"(vt + chunk_at<HD>(j, n) + qc * 4)
                                      : "memory");
-                        const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xFFFF0000u);
-                        if (p0 != 0.f) {
-                            o[n][0] = fmaf(p0, v0, o[n][0]);
-                            o[n][1] = fmaf(p0, v1, o[n][1]);
+                        const float x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xFFFF0000u);
+                        if (adds[0]) {
+                            o[n][0] = fmaf(p0, x, o[n][0]);
+                            o[n][1] = fmaf(p0, y, o[n][1]);
                         }
-                        if (p1 != 0.f) {
-                            o[n][2] = fmaf(p1, v0, o[n][2]);
-                            o[n][3] = fmaf(p1, v1, o[n][3]);
+                        if (adds[1]) {
+                            o[n][2] = fmaf(p1, x, o[n][2]);
+                            o[n][3] = fmaf(p1, y, o[n][3]);
                         }
                     }
                 }
