@@ -278,6 +278,7 @@ template <typename T, int ROWS, int HD>
 cudaError_t launch_combine(const AttnArgs &a, int workers, cudaStream_t stream) {
     using C = Combine<ROWS, HD>;
     const long long units = (long long)a.B * a.Hkv * (((long long)a.max_T * a.G + ROWS - 1) / ROWS);
+    if (units == 0) return cudaSuccess;  // max_T = 0: the rows are no request's
     return launch(combine_kernel<T, ROWS, HD>, dim3((unsigned)std::min<long long>(units, workers), ROWS / C::RB),
                   C::kThreads, 0, stream, a, workers);
 }
