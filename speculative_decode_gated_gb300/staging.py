@@ -243,8 +243,11 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     "linear" divides every frequency (position interpolation); "ntk" raises the base so
     that the last pair is divided by `factor` and the first by 1; "yarn" divides the pairs
     that make fewer than beta_slow turns over the `trained` positions, keeps those that
-    make more than beta_fast, blends linearly between, and scales cosine and sine by
-    0.1 ln(factor) + 1."""
+    make more than beta_fast, blends between, and scales cosine and sine by
+    0.1 ln(factor) + 1.  The blend is linear in the pair's index, from the index of
+    beta_fast turns rounded down to that of beta_slow turns rounded up (each within
+    0 .. rot_dim - 1), as checkpoints are trained and loaded; "yarn_turns" blends linearly
+    in the number of turns instead, the ramp that the method's paper writes down."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even")
     if base <= 1.0 or factor < 1.0:
@@ -257,9 +260,20 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
         if rot_dim < 4:
             raise ValueError("ntk needs two pairs at least")
         f = (base * factor ** (rot_dim / (rot_dim - 2.0))) ** (-2.0 * i / rot_dim)
-    elif scaling == "yarn":
-        turns = trained * f / (2.0 * math.pi)
-        keep = np.clip((turns - beta_slow) / (beta_fast - beta_slow), 0.0, 1.0)
+    elif scaling in ("yarn", "yarn_turns"):
+        if not (beta_fast > beta_slow > 0.0 and trained > 2.0 * math.pi * beta_slow):
+            raise ValueError("yarn needs beta_fast above beta_slow above 0, and beta_slow turns of "
+                             "the first pair within the trained positions")
+        if scaling == "yarn":
+            # base^(-2i / rot_dim) trained / (2 pi) = turns, solved for i
+            at = [rot_dim * math.log(trained / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+                  for turns in (beta_fast, beta_slow)]
+            first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
+            # first >= last only where both lie behind the last pair: all are kept
+            keep = 1.0 - np.clip((i - first) / max(last - first, 1), 0.0, 1.0)
+        else:
+            turns = trained * f / (2.0 * math.pi)
+            keep = np.clip((turns - beta_slow) / (beta_fast - beta_slow), 0.0, 1.0)
         f = f * keep + f / factor * (1.0 - keep)
         mscale = 0.1 * math.log(factor) + 1.0
     elif scaling != "none":
