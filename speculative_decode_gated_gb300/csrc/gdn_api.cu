@@ -548,7 +548,8 @@ gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_stride, vo
     a.lse = lse;
     a.desc = static_cast<int4 *>(workspace);
     a.count = reinterpret_cast<int *>(a.desc + 2 * gdn::kAttnWorkers);
-    static_assert(gdn::kAttnWorkers * (2 * sizeof(int4) + sizeof(int)) <= gdn::kAttnHeader, "header");
+    static_assert(gdn::kAttnWorkers * (2 * sizeof(int4) + gdn::kAttnLevels * sizeof(int)) <=
+                      gdn::kAttnHeader, "header");
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + gdn::kAttnHeader);
     const cudaError_t e = gdn::launch_attn(a, p->dtype == GDN_BF16, stream);
     if (e != cudaSuccess) {

@@ -15,11 +15,12 @@
 // end take time too, so each has EXTRA places on the line before its tiles, in
 // which nothing is done.  A unit that
 // lies in one worker's range is finished there; one that spans several leaves
-// a partial (unnormalised sums, running maximum, total) per worker, joined by
-// combine_kernel in the order of the workers, so results do not depend on
-// timing (in the largest calls; where a unit cannot have many partials the block that
-// writes the last of them joins them in that same order).  A worker has at most two partials: the end of a unit begun earlier
-// (slot 2c) and the beginning of one finished later (slot 2c + 1).
+// a partial (unnormalised sums, running maximum, total) per worker.  They are joined
+// by the block that writes the last of them (on the tensor cores in groups, level by
+// level) or by combine_kernel, as launch_attn chooses; in the order of the workers
+// either way, so results do not depend on timing.  A worker has at most two partials:
+// the end of a unit begun earlier (slot 2c) and the beginning of one finished later
+// (slot 2c + 1).
 #pragma once
 
 #include <cstdint>
@@ -51,8 +52,9 @@ struct AttnArgs {
     float *lse;
     float *part;             // 2P partial slots of ROWS * (hd + 2) floats
     int4 *desc;              // [P][2]: which unit worker c leaves unfinished
-    int *count;              // [P], zero between calls: partials of the unit that begins in
-                             // worker c; NULL: combine_kernel joins them, by desc
+    int *count;              // [kAttnLevels][P], zero between calls: partials written of the unit
+                             // that begins in worker c (on tensor cores, of the group that
+                             // does, by level); NULL: combine_kernel joins them, by desc
 };
 
 __device__ __forceinline__ int div_group(const AttnArgs &a, int n) {

@@ -51,6 +51,8 @@ namespace {
 
 constexpr int kSegs = 4;       // segments known ahead
 constexpr float kLazy = 8.f;
+constexpr int kGroup = 8;      // partials joined at a time
+static_assert(kGroup * kGroup * kGroup >= kAttnWorkers && kAttnLevels == 3, "levels of groups");
 
 // NWG softmax warpgroups, then the TMA, MMA, segment and clearing warps.
 template <int HD, int NWG>
@@ -89,7 +91,7 @@ struct Shared {
     uint32_t tmem;
     int dead;          // a wait gave up: every role leaves
     int poison[4];     // segment (mod 4) whose hidden places hold values that are not finite
-    int2 join[2];      // first (or -1) and last worker of a unit that a warpgroup is to join
+    int join[2];       // whether a warpgroup is to join a group of partials
     Segment seg[kSegs];  // r = -1: no more
 };
 
@@ -849,32 +851,43 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
             }
         }
         if (a.count && !whole) {
-            // A unit of few partials: the warpgroup that writes the last one joins them, in the
-            // order of the workers, while the next segment streams in.
-            __threadfence();
-            arrive_warp(bar(s.b.joined[w]));
-            if (!wait(bar(s.b.joined[w]), 0, &s.dead)) return;
-            if (t == 0) {
-                // the unit's first tile on the line: a worker's range begins or ends in it
-                const long long begin = g.i0 > 0 ? plan.x - g.i0 : plan.x1 - g.i1;
-                const int first = worker_of(begin, plan.N, plan.P);
-                const int last = worker_of(begin + sp.n - 1, plan.N, plan.P);
-                int *count = a.count + first * NWG + w;
-                const bool all = atomicAdd(count, 1) == last - first;
-                if (all) *count = 0;  // for the next call
-                s.join[w] = make_int2(all ? first : -1, last);
-            }
-            arrive_warp(bar(s.b.joined[w]));
-            if (!wait(bar(s.b.joined[w]), 1, &s.dead)) return;
-            const int first = s.join[w].x, last = s.join[w].y;
-            if (first >= 0 && row < rows) {
+            // The unit's partials are joined, kGroup at a time and in the order of the workers, by
+            // the warpgroup that writes a group's last one, while the next segment streams in;
+            // a group's sum takes the place of its first partial and is one of the next level's.
+            // Few partials, as most units have, are one group.  A unit of a long request among
+            // short ones lies in half of the workers: its groups are joined side by side.
+            // the unit's first tile on the line: a worker's range begins or ends in it
+            const long long begin = g.i0 > 0 ? plan.x - g.i0 : plan.x1 - g.i1;
+            const int first = worker_of(begin, plan.N, plan.P);
+            const int parts = worker_of(begin + sp.n - 1, plan.N, plan.P) - first + 1;
+            int *count = a.count + w;
+            for (int step = 1; step < parts; step *= kGroup, count += kAttnWorkers) {
+                const int lo = (int)(blockIdx.x - first) / (step * kGroup) * (step * kGroup);
+                const int members = min(kGroup, (parts - lo + step - 1) / step);
+                if (members == 1) continue;  // its sum lies there already
                 __threadfence();
-                auto slot = [&](int k) {
+                arrive_warp(bar(s.b.joined[w]));
+                if (!wait(bar(s.b.joined[w]), 0, &s.dead)) return;
+                if (t == 0) {
+                    // No other unit's group of several begins in this worker.
+                    int *here = count + (first + lo) * NWG;
+                    __threadfence();
+                    s.join[w] = atomicAdd(here, 1) == members - 1;
+                    if (s.join[w]) *here = 0;  // for the next call
+                }
+                arrive_warp(bar(s.b.joined[w]));
+                if (!wait(bar(s.b.joined[w]), 1, &s.dead)) return;
+                if (!s.join[w]) break;  // whoever writes the group's last one goes on
+                if (row >= rows) continue;
+                __threadfence();
+                auto slot = [&](int i) {
+                    const int k = first + lo + i * step;
                     return a.part + (long long)(k == first ? 2 * k + 1 : 2 * k) * ROWS * (HD + 2);
                 };
                 float top = -INFINITY, total = 0.f;
-                for (int k = first; k <= last; ++k) top = fmaxf(top, __ldcg(slot(k) + ROWS * HD + prow));
+                for (int i = 0; i < members; ++i) top = fmaxf(top, __ldcg(slot(i) + ROWS * HD + prow));
                 const float base = top == -INFINITY ? 0.f : top;
+                const bool all = step * kGroup >= parts;  // the unit's output, else a group's sum
                 const int tok = div_group(a, row);
                 const long long at = (long long)(g.req.row0 + tok) * a.Hq + g.h * a.G + (row - tok * a.G);
 #pragma unroll 1
@@ -882,8 +895,8 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                     float o[32] = {};
                     float sum = 0.f;
 #pragma unroll 2
-                    for (int k = first; k <= last; ++k) {
-                        const float *p = slot(k);
+                    for (int i = 0; i < members; ++i) {
+                        const float *p = slot(i);
                         const float f = exp2f(__ldcg(p + ROWS * HD + prow) - base);
                         sum = fmaf(__ldcg(p + ROWS * HD + ROWS + prow), f, sum);
 #pragma unroll
@@ -897,16 +910,30 @@ __device__ __forceinline__ void softmax_role(const Launch &L, Shared &s, uint32_
                         }
                     }
                     total = sum;
-                    const float inv = 1.f / sum;
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * HD + c);
+                    if (all) {
+                        const float inv = 1.f / sum;
+                        uint4 *dst =
+                            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * HD + c);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                            pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                            pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                            pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    } else {
+                        float *dst = slot(0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            put(dst + part_at<ROWS>(prow, c + 4 * e),
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                    }
                 }
-                if (a.lse) a.lse[at] = (top + log2f(total)) * 0.69314718055994531f;
+                if (!all) {
+                    slot(0)[ROWS * HD + prow] = top;
+                    slot(0)[ROWS * HD + ROWS + prow] = total;
+                } else if (a.lse) {
+                    a.lse[at] = (top + log2f(total)) * 0.69314718055994531f;
+                }
             }
         }
         base_slot = (base_slot + 2 * n) % C::NS;

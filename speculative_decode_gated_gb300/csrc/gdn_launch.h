@@ -57,6 +57,7 @@ cudaError_t allow_smem(int bytes) {
 
 constexpr int kAttnWorkers = 304;    // blocks, two on each of 152 SMs
 constexpr int kAttnHeader = 16384;   // bytes of the workspace before the partials
+constexpr int kAttnLevels = 3;       // of counters
 constexpr int kAttnTcWorkers = 152;  // one an SM: the tcgen05 kernel on prompt chunks
 enum AttnKind { kAttnSimple, kAttnRows, kAttnDrafts, kAttnWide };
 AttnKind attn_kind(bool bf16, int hd, long long rows);  // rows: max_T times the group
