@@ -448,6 +448,7 @@ class Attn:
         self.c = c
         self.refs = refs
         self.dtype, self.device = dtype, device
+        self.index = device.index if device.type == "cuda" else None
         self.n_tok, self.q_heads, self.kv_heads, self.head_dim = (
             c.n_tok, c.q_heads, c.kv_heads, c.head_dim)
         self.ref = ctypes.byref(c)
@@ -540,10 +541,17 @@ def _check_rows(t: torch.Tensor, name: str, attn: Attn, heads: int) -> int:
     return s[0] if n > 1 else heads * hd
 
 
+def _elsewhere(attn: Attn) -> bool:
+    """Whether another device than the tensors' is current, where the kernels would go."""
+    return attn.index is not None and torch._C._cuda_getDevice() != attn.index
+
+
 def _attn_stream(attn: Attn, stream) -> int:
-    """`stream`, or the current stream of the tensors' device."""
+    """`stream`, or the current stream of the tensors' device, which is the current device."""
+    if attn.index is None:
+        raise ValueError(f"the tensors are on {attn.device}, expected a CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(attn.device.index or 0)
+        return torch._C._cuda_getCurrentRawStream(attn.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -552,6 +560,9 @@ def gdn_rope_append(attn: Attn, rope: Rope, q: torch.Tensor, k: torch.Tensor, v:
     """q_out <- rotated q; the rotated k and the v of each row to the pages.
     q, q_out: [N_tok, q_heads, head_dim]; k, v: [N_tok, kv_heads, head_dim]; the rows of
     q, k and v may be slices of wider ones, q_out is contiguous."""
+    if _elsewhere(attn):
+        with torch.cuda.device(attn.index):
+            return gdn_rope_append(attn, rope, q, k, v, q_out, stream)
     Hq, Hkv = attn.q_heads, attn.kv_heads
     sq, sk = _check_rows(q, "q", attn, Hq), _check_rows(k, "k", attn, Hkv)
     sv = _check_rows(v, "v", attn, Hkv)
@@ -586,6 +597,9 @@ def gdn_paged_attn(attn: Attn, q: torch.Tensor, o: torch.Tensor, *, workspace: t
     """o <- attention of the step's rows over the cache; lse (fp32 [N_tok, q_heads], or None)
     <- the logarithm of each row's sum.  q, o: [N_tok, q_heads, head_dim]; q's rows may be
     slices of wider ones, o is contiguous."""
+    if _elsewhere(attn):
+        with torch.cuda.device(attn.index):
+            return gdn_paged_attn(attn, q, o, workspace=workspace, lse=lse, stream=stream)
     Hq = attn.q_heads
     sq = _check_rows(q, "q", attn, Hq)
     if _check_rows(o, "o", attn, Hq) != Hq * attn.head_dim:
