@@ -476,7 +476,8 @@ def make_attn(*, q_heads: int, k_pages: torch.Tensor, v_pages: torch.Tensor,
     for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if t.device != dev:
             raise ValueError(f"{n} is on {t.device}, expected {dev}")
-        if t.stride()[1:] != (page * hd, hd, 1):
+        # (the distance of a single head's rows from the next head's has no meaning)
+        if t.stride()[2:] != (hd, 1) or (t.stride(1) != page * hd and kv_heads > 1):
             raise ValueError(f"a page of {n} must be contiguous")
     if n_pages > 1 and v_pages.stride(0) != k_pages.stride(0):
         raise ValueError("k_pages and v_pages must have the same page stride")
