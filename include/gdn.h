@@ -344,7 +344,8 @@ typedef struct gdn_attn {
     void *k_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
     void *v_pages;               /* device, 16-byte aligned; written by gdn_rope_append only */
     int64_t n_pages;             /* 1 .. 2^31 - 1 */
-    int64_t page_stride;         /* elements from a page to the next; a multiple of 16 bytes, at most 2^36 */
+    int64_t page_stride;         /* elements from a page to the next; a multiple of 16 bytes, at most 2^36,
+                                    and n_pages * page_stride at most 2^56 */
     const int32_t *page_table;   /* device [batch][max_pages]; entries no row needs are not read */
     const int32_t *kv_len;       /* device [batch]: tokens in the cache before this step */
     int32_t *dev_err;            /* device int32 error word (GDN_DEVERR_* bits), or NULL */
@@ -369,8 +370,8 @@ typedef struct gdn_rope {
  * to its place in the pages.
  *   q      device [N_tok][q_heads][head_dim], q_stride elements from a row to the next
  *   k, v   device [N_tok][kv_heads][head_dim], k_stride and v_stride elements apart
- *          (strides >= the row, multiples of 16 bytes, at most 2^36: slices of one
- *          projection's output)
+ *          (strides >= the row, multiples of 16 bytes, at most 2^36, and N_tok times a
+ *          stride at most 2^56: slices of one projection's output)
  *   q_out  device [N_tok][q_heads][head_dim], contiguous; overlaps nothing else of the call
  * All 16-byte aligned.  A request with a bad kv_len or bad row offsets is skipped; a row
  * whose page id is outside [0, n_pages) gets its q_out and sets GDN_DEVERR_PAGE.  No two rows

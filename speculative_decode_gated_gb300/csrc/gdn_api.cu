@@ -411,9 +411,15 @@ AttnRanges attn_ranges(const gdn_attn *p) {
     return r;
 }
 
+// Arrays of n rows (pages), `stride` elements apart, span less than this many elements: their
+// bytes fit the ranges below, as every address does.
+constexpr int64_t kMaxSpan = 1ll << 56;
+bool span_ok(int64_t n, int64_t stride) { return n < 1 || stride <= kMaxSpan / n; }
+
 // Whether rows of `row` elements, `stride` apart, are well formed; the bytes they span.
 bool stride_ok(const gdn_attn *p, int64_t stride, int64_t row) {
-    return stride >= row && stride <= (1ll << 36) && stride * attn_esz(p) % 16 == 0;
+    return stride >= row && stride <= (1ll << 36) && stride * attn_esz(p) % 16 == 0 &&
+           span_ok(attn_rows(p), stride);
 }
 Range rows_range(const gdn_attn *p, const void *ptr, int64_t stride, int64_t row) {
     const int64_t n = attn_rows(p);
@@ -433,7 +439,8 @@ gdn_status attn_validate(const gdn_attn *p, bool *empty) {
         p->n_pages > 0x7fffffffLL)
         return GDN_ERR_BAD_DIM;
     if (p->page_stride < (int64_t)p->kv_heads * p->page_size * p->head_dim ||
-        p->page_stride > (1ll << 36) || p->page_stride * attn_esz(p) % 16 != 0)
+        p->page_stride > (1ll << 36) || p->page_stride * attn_esz(p) % 16 != 0 ||
+        !span_ok(p->n_pages, p->page_stride))
         return GDN_ERR_BAD_DIM;
     if (!p->k_pages || !p->v_pages || !p->page_table || !p->kv_len) return GDN_ERR_NULL_PTR;
     if (!aligned16(p->k_pages) || !aligned16(p->v_pages) || !aligned4(p->page_table) ||
