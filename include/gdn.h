@@ -53,6 +53,7 @@
  *   gdn_paged_attn           attention of the step's rows over that cache, all
  *                            of it or a sliding window with first tokens that
  *                            stay visible.
+ *   gdn_read_attn_error      the device error word of an attention layer's step.
  *   gdn_selftest_wait_timeout  runs the bounded wait to its expiry (diagnostic).
  *
  * Device-side argument errors (a slot id outside [0, pool_slots), a_r outside
@@ -88,7 +89,7 @@ typedef enum gdn_status {
                                  batch*max_T or n_tok, above 2^31 - 1), or unknown flags */
     GDN_ERR_BAD_DTYPE = 3,    /* qkv_dtype is not a gdn_dtype */
     GDN_ERR_UNSUPPORTED = 4,  /* dk/dv (or a forced algo) not supported */
-    GDN_ERR_DEVICE_ARG = 5,   /* reported by gdn_read_device_error only */
+    GDN_ERR_DEVICE_ARG = 5,   /* reported by gdn_read_device_error and gdn_read_attn_error only */
     GDN_ERR_CUDA = 6,         /* a CUDA call failed; see gdn_last_error_string */
     GDN_ERR_ALIGN = 7,        /* a pointer is not aligned (16 bytes for q/k/v/pool/o) */
     GDN_ERR_ALIAS = 8,        /* o overlaps an input, or the pool overlaps q/k/v/o */
@@ -415,6 +416,9 @@ GDN_API int64_t gdn_paged_attn_workspace(const gdn_attn *p);
  * Returns GDN_ERR_DEVICE_ARG when the word is non-zero, GDN_OK when it is zero. */
 GDN_API gdn_status gdn_read_device_error(const gdn_problem *p, cudaStream_t stream,
                                          int32_t *host_code);
+
+/* The same for the attention calls: of *p only dev_err is read. */
+GDN_API gdn_status gdn_read_attn_error(const gdn_attn *p, cudaStream_t stream, int32_t *host_code);
 
 /* Self-check of the bounded waits (diagnostic; not part of a decode step).
  * The chunked kernel waits on shared-memory barriers for its copies and

@@ -35,7 +35,7 @@ EXPORTED = (
     "gdn_accept_prefix", "gdn_replay_verify", "gdn_replay_commit", "gdn_commit_verify",
     "gdn_read_device_error", "gdn_selftest_wait_timeout",
     "gdn_select_algo", "gdn_status_string", "gdn_last_error_string", "gdn_version",
-    "gdn_rope_append", "gdn_paged_attn", "gdn_paged_attn_workspace",
+    "gdn_rope_append", "gdn_paged_attn", "gdn_paged_attn_workspace", "gdn_read_attn_error",
 )
 
 
@@ -138,6 +138,7 @@ def lib() -> ctypes.CDLL:
         h.gdn_paged_attn_workspace.argtypes = [A]
         h.gdn_paged_attn_workspace.restype = I64
         h.gdn_read_device_error.argtypes = [P, S, ctypes.POINTER(ctypes.c_int32)]
+        h.gdn_read_attn_error.argtypes = [A, S, ctypes.POINTER(ctypes.c_int32)]
         h.gdn_selftest_wait_timeout.argtypes = [S, S]
         h.gdn_select_algo.argtypes = [P]
         h.gdn_status_string.argtypes = [ctypes.c_int]
@@ -145,7 +146,8 @@ def lib() -> ctypes.CDLL:
                      "gdn_verify_layers", "gdn_commit_layers", "gdn_verify_commit_fused_layers",
                      "gdn_accept_prefix", "gdn_replay_verify", "gdn_replay_commit",
                      "gdn_commit_verify", "gdn_read_device_error", "gdn_selftest_wait_timeout",
-                     "gdn_select_algo", "gdn_rope_append", "gdn_paged_attn"):
+                     "gdn_select_algo", "gdn_rope_append", "gdn_paged_attn",
+                     "gdn_read_attn_error"):
             getattr(h, name).restype = ctypes.c_int
         for name in ("gdn_status_string", "gdn_last_error_string", "gdn_version"):
             getattr(h, name).restype = ctypes.c_char_p
@@ -615,3 +617,15 @@ def gdn_paged_attn(attn: Attn, q: torch.Tensor, o: torch.Tensor, *, workspace: t
                               workspace.data_ptr(), workspace.nbytes, _attn_stream(attn, stream))
     if st:
         _raise(st, "gdn_paged_attn")
+
+
+def gdn_read_attn_error(attn: Attn, stream=None) -> int:
+    """Waits for the stream and returns the error word of `attn` (GDN_DEVERR_* bits, 0: none)."""
+    if _elsewhere(attn):
+        with torch.cuda.device(attn.index):
+            return gdn_read_attn_error(attn, stream)
+    code = ctypes.c_int32(0)
+    st = lib().gdn_read_attn_error(attn.ref, _attn_stream(attn, stream), ctypes.byref(code))
+    if st not in (GDN_OK, GDN_ERR_DEVICE_ARG):
+        _raise(st, "gdn_read_attn_error")
+    return code.value

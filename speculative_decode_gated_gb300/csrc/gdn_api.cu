@@ -365,6 +365,21 @@ gdn_status run_commit_verify(const gdn_problem *p, const gdn_prev_step *prev, vo
     return GDN_OK;
 }
 
+gdn_status read_error_word(const int32_t *dev_err, cudaStream_t stream, int32_t *host_code,
+                           const char *where) {
+    *host_code = 0;
+    if (!dev_err) return GDN_OK;
+    int32_t word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, dev_err, sizeof(word), cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, where);
+        return GDN_ERR_CUDA;
+    }
+    *host_code = word;
+    return word ? GDN_ERR_DEVICE_ARG : GDN_OK;
+}
+
 // ------------------------------------------------------------ attention layers
 
 int64_t attn_rows(const gdn_attn *p) {
@@ -650,17 +665,12 @@ gdn_status gdn_selftest_wait_timeout(int32_t *dev_err, cudaStream_t stream) {
 
 gdn_status gdn_read_device_error(const gdn_problem *p, cudaStream_t stream, int32_t *host_code) {
     if (!p || !host_code) return GDN_ERR_NULL_PTR;
-    *host_code = 0;
-    if (!p->dev_err) return GDN_OK;
-    int32_t word = 0;
-    cudaError_t e = cudaMemcpyAsync(&word, p->dev_err, sizeof(word), cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e != cudaSuccess) {
-        set_cuda_error(e, "gdn_read_device_error");
-        return GDN_ERR_CUDA;
-    }
-    *host_code = word;
-    return word ? GDN_ERR_DEVICE_ARG : GDN_OK;
+    return read_error_word(p->dev_err, stream, host_code, "gdn_read_device_error");
+}
+
+gdn_status gdn_read_attn_error(const gdn_attn *p, cudaStream_t stream, int32_t *host_code) {
+    if (!p || !host_code) return GDN_ERR_NULL_PTR;
+    return read_error_word(p->dev_err, stream, host_code, "gdn_read_attn_error");
 }
 
 int32_t gdn_select_algo(const gdn_problem *p) {
