@@ -329,16 +329,17 @@ GDN_API gdn_status gdn_commit_verify(const gdn_problem *p, const gdn_prev_step *
 
 typedef struct gdn_attn {
     int32_t batch;               /* B >= 0 requests (B = 0: calls return GDN_OK, no launch) */
-    int32_t q_heads;             /* a multiple of kv_heads */
+    int32_t q_heads;             /* a multiple of kv_heads, at most 65536; max_T * (q_heads / kv_heads) at most 2^30 */
     int32_t kv_heads;            /* >= 1 */
     int32_t head_dim;            /* 32, 64, 128 or 256 */
-    int32_t max_T;               /* uniform rows per request (cu_seqlens NULL) or the ragged maximum, 0..GDN_ATTN_MAX_T */
+    int32_t max_T;               /* uniform rows per request (cu_seqlens NULL) or the ragged maximum, 0..GDN_ATTN_MAX_T;
+                                    the kernel is chosen by it, so keep it as small as the rows allow */
     int32_t dtype;               /* gdn_dtype of q, k, v, the pages and o */
     int32_t page_size;           /* 16, 32, 64, 128 or 256 */
     int32_t max_pages;           /* columns of page_table; max_pages * page_size <= 2^31 - 1 */
     int32_t window;              /* 0: every place up to the row's own; W > 0: the last W of them, itself among them */
     int32_t sinks;               /* first places that stay visible under a window (0 without one) */
-    float scale;                 /* factor on q.k, finite (1 / sqrt(head_dim) in most models) */
+    float scale;                 /* factor on q.k, finite and above 0 (1 / sqrt(head_dim) in most models) */
     int32_t reserved;            /* must be 0 */
     const int32_t *cu_seqlens;   /* device [batch+1] token-row offsets, or NULL (uniform) */
     int64_t n_tok;               /* rows of q/k/v/o: REQUIRED for ragged input, ignored for uniform */
@@ -391,12 +392,15 @@ GDN_API gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, cons
  *   o    device [N_tok][q_heads][head_dim], contiguous, dtype, 16-byte aligned
  *   lse  device float32 [N_tok][q_heads]: m + log(sum_j e_j), or NULL
  *   workspace  device, 16-byte aligned, at least gdn_paged_attn_workspace(p)
- *        bytes, zero when it is first used; one per stream.  Its first 16
- *        KB hold counters that every call leaves at zero (zero them again
- *        after a GDN_DEVERR_TIMEOUT); calls leave nothing else in it that a
- *        later call reads.
+ *        bytes; one per stream.  Its first 16 KB have to be zero when it is
+ *        first used, and again after a GDN_DEVERR_TIMEOUT: they hold counters,
+ *        which every call leaves at zero (and what a call writes for itself,
+ *        which no later call reads).
  * o, lse and the workspace overlap nothing else of the call.  Sums and the
- * softmax's statistics are 32-bit.  Keys and values at places that no row of a
+ * softmax's statistics are 32-bit.  The weights e_j are rounded to bf16 for the
+ * products with v where dtype is bf16, head_dim 64 or 128 and max_T * (q_heads /
+ * kv_heads) above 16, and carried to 2^-16 elsewhere: a token's output as a single
+ * row and within a draft may differ by a rounding of its weights.  Keys and values at places that no row of a
  * request sees are never used, whatever they hold.  An infinite value at a place
  * that a row sees makes that element of the row's output infinite; a NaN, or
  * infinities of both signs, make it NaN, and so may an infinite value whose

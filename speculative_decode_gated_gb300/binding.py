@@ -591,7 +591,8 @@ def gdn_paged_attn_workspace(attn: Attn) -> int:
 
 
 def paged_attn_workspace(attn: Attn) -> torch.Tensor:
-    """A workspace for gdn_paged_attn, zero-filled; one per stream, kept from call to call."""
+    """A workspace for gdn_paged_attn, zero-filled (on the current stream); one per stream, kept
+    from call to call."""
     return torch.zeros(gdn_paged_attn_workspace(attn), dtype=torch.uint8, device=attn.device)
 
 

@@ -8,9 +8,9 @@
 // (cp.async, 16-byte chunks XOR-swizzled by row, a ring of tiles ahead), and
 // keeps its own running maximum, total and output for all 16 rows, so that
 // nothing in the loop waits for another warp.  The warps' results are joined
-// through shared memory at the end of a segment; units that span blocks are
-// joined by combine_kernel.  Two blocks an SM: one streams while the other
-// joins.
+// through shared memory at the end of a segment; the partials of a unit that
+// spans blocks by the block that writes the last one, or by combine_kernel where
+// there may be many.  Two blocks an SM: one streams while the other joins.
 //
 // The products are mma.sync m16n8k16: 16 rows fill its M, where a 128-row
 // tcgen05 tile would be seven eighths padding, and the fragments of the scores

@@ -38,8 +38,6 @@ cudaError_t launch_rope(const AttnArgs &a, const gdn_rope &rope, bool bf16, cons
                         long long k_stride, const void *v, long long v_stride, void *k_pages,
                         void *v_pages, cudaStream_t stream);
 
-// Chunk attention over the cache.  a.desc and a.part point into the workspace:
-// attn_workspace() bytes: the descriptors, the counts, then the partials.
 // Shared memory above 48 KB is asked for once a device and kernel (KERNEL names the
 // instantiation, so each has its own record).
 template <auto KERNEL>
@@ -55,6 +53,8 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+// Chunk attention over the cache.  a.desc, a.count and a.part point into the workspace of
+// attn_workspace() bytes: the descriptors, the counts, then the partials.
 constexpr int kAttnWorkers = 304;    // blocks, two on each of 152 SMs
 constexpr int kAttnHeader = 16384;   // bytes of the workspace before the partials
 constexpr int kAttnLevels = 3;       // of counters
@@ -63,7 +63,8 @@ enum AttnKind { kAttnSimple, kAttnRows, kAttnDrafts, kAttnWide };
 AttnKind attn_kind(bool bf16, int hd, long long rows);  // rows: max_T times the group
 int64_t attn_workspace(bool bf16, int hd, long long rows);
 cudaError_t launch_attn(AttnArgs a, bool bf16, cudaStream_t stream);
-cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t stream);  // their first launches
+// Of launch_attn, the launch of one kernel, without that of combine_kernel.
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnArgs &a, bool wide, cudaStream_t stream);
 
 }  // namespace gdn
