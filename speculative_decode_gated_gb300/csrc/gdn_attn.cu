@@ -330,8 +330,8 @@ cudaError_t launch_attn(AttnArgs a, bool bf16, cudaStream_t stream) {
 }
 
 // Which kernel runs, by type and rows a key head: float32 on the CUDA cores; up to
-// 16 rows as one mma.sync tile; more on tcgen05, in units of 128 or 256 rows, for the
-// heads whose tiles fit there.  Prompt chunks in units of 128 rows would read the cache twice
+// 16 rows as one mma.sync tile; more on tcgen05, in units of 128 or 256 rows, for heads of
+// 64 and 128 (those of 32 and 256 have the 16-row kernel only).  Prompt chunks in units of 128 rows would read the cache twice
 // as often, and lose the second warpgroup that keeps the tensor cores busy: 4001 rows over
 // 6007 places 704 us in units of 256 and 880 of 128, 8000 rows behind a window of 512
 // 167 and 237.  Drafts in units of 256 rows, one block an SM: 64 requests' 16 drafts 137 us

@@ -22,8 +22,10 @@
 // that is not zero is kept above zero: both terms of an infinite value then have its sign.
 //
 // Measured: 64 requests' single tokens over contexts of up to 8191 places, 8 key heads
-// of 128: 1.33 GB in 207 us, 6.4 TB/s, 94% of a plain copy's rate, with the tensor pipe
-// 27% and the issue slots 30% busy.  A single request's token over 1000 places 11 us:
+// of 128: 1.33 GB in 203 to 207 us, 6.4 TB/s, 95% of a plain copy's rate, with the tensor pipe
+// 28% and the issue slots 31% busy.  2 key heads of 256: 0.66 GB in 120 us.  More rows than 16 read
+// the cache once for each 16 of them (heads of 32 and 256 have no other kernel): 16 drafts of
+// 8 heads each over up to 4000 places 433 us, where the bytes would take 50.  A single request's token over 1000 places 11 us:
 // latencies in a row (lengths, pages, keys, the join of the workers).
 #include <cstdint>
 

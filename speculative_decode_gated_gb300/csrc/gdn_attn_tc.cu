@@ -17,11 +17,12 @@
 //     rows that are not there cost tensor time that the stream leaves over.
 //
 // Measured (bf16): two requests' prompt chunks of 4001 rows over 6007 places, 32 heads
-// on 8 key heads of 128: 704 us, 1.49 PFLOP/s of visible products, tensor pipe 68% busy
+// on 8 key heads of 128: 665 to 740 us by the clocks that the power leaves, 1.42 to 1.58
+// PFLOP/s of visible products, tensor pipe 68% busy
 // (the tensor cores wait while a warpgroup hands its weights over).  8000 rows behind a
-// window of 512, heads of 64: 166 us; a unit has six tiles, so its start and end and the
-// masked tiles are most of it.  64 requests' 16 drafts over up to 4000 places: 0.67 GB in 124 us,
-// 5.5 TB/s.  128 requests' up to 16 drafts behind a window of 1024: 72 us, 290 MB; the
+// window of 512, heads of 64: 162 us; a unit has six tiles, so its start and end and the
+// masked tiles are most of it.  64 requests' 16 drafts over up to 4000 places: 0.67 GB in 125 us,
+// 5.4 TB/s.  128 requests' up to 16 drafts behind a window of 1024: 75 us, 290 MB; the
 // units are short.  16 drafts over 130001 places, heads of 64: 61 us, 4.4 TB/s; its 38
 // partials to each of eight units are joined by a second launch.
 //

@@ -18,8 +18,8 @@
 // neighbours.
 //
 // Measured: 64 requests of 16 rows (32 + 2 * 8 heads of 128, bf16, 25 MB that the L2 holds)
-// 4.9 us; a prompt of 5127 rows (16 + 2 * 4 heads of 256, bf16, 126 MB) 25.4 us, 5.0 TB/s,
-// half the issue slots busy; a single row 2.8 us, all of it latency.
+// 4.9 to 5.4 us; a prompt of 5127 rows (16 + 2 * 4 heads of 256, bf16, 126 MB) 26 us, 4.8 TB/s,
+// half the issue slots busy; a single row 3 us, all of it latency.
 #include <cstdint>
 
 #include "gdn_attn.cuh"
