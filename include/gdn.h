@@ -54,6 +54,15 @@
  *                            of it or a sliding window with first tokens that
  *                            stay visible.
  *   gdn_read_attn_error      the device error word of an attention layer's step.
+ *   gdn_linear_verify/commit/step  linear attention with a decay for each head over
+ *                            the same kind of state pool: drafts and their accepted
+ *                            prefix, single tokens and prompts.
+ *   gdn_accept_sample        accepted lengths and next tokens of drafts that were
+ *                            sampled, from both models' probabilities and given
+ *                            random numbers, on the device.
+ *   gdn_plan_pages           the next step's cache lengths, page table, row offsets,
+ *                            slots and positions, from lengths on the device.
+ *   gdn_read_error           any device error word.
  *   gdn_selftest_wait_timeout  runs the bounded wait to its expiry (diagnostic).
  *
  * Device-side argument errors (a slot id outside [0, pool_slots), a_r outside
@@ -89,7 +98,7 @@ typedef enum gdn_status {
                                  batch*max_T or n_tok, above 2^31 - 1), or unknown flags */
     GDN_ERR_BAD_DTYPE = 3,    /* qkv_dtype is not a gdn_dtype */
     GDN_ERR_UNSUPPORTED = 4,  /* dk/dv (or a forced algo) not supported */
-    GDN_ERR_DEVICE_ARG = 5,   /* reported by gdn_read_device_error and gdn_read_attn_error only */
+    GDN_ERR_DEVICE_ARG = 5,   /* reported by gdn_read_device_error, gdn_read_attn_error and gdn_read_error only */
     GDN_ERR_CUDA = 6,         /* a CUDA call failed; see gdn_last_error_string */
     GDN_ERR_ALIGN = 7,        /* a pointer is not aligned (16 bytes for q/k/v/pool/o) */
     GDN_ERR_ALIAS = 8,        /* o overlaps an input, or the pool overlaps q/k/v/o */
@@ -129,7 +138,10 @@ typedef enum gdn_algo {
                                    the CUDA context has been rebuilt. */
 #define GDN_DEVERR_REPLAY  16   /* replay buffer: len_in[slot] < 0, or buffered plus new rows > capacity */
 #define GDN_DEVERR_KV_LEN  32   /* cache: kv_len[r] < 0, or kv_len[r] + T_r > max_pages * page_size */
-#define GDN_DEVERR_PAGE    64   /* cache: a page id that the call needs is outside [0, n_pages) */
+#define GDN_DEVERR_PAGE    64   /* cache: a page id that the call needs is outside [0, n_pages);
+                                   gdn_plan_pages: the free list's count is */
+#define GDN_DEVERR_TOKEN  128   /* a draft id outside [0, vocab), or a row without any probability */
+#define GDN_DEVERR_NO_PAGES 256 /* the free list has too few pages for a request's next rows */
 
 /* Variant bits of gdn_problem.flags (the same in every problem of a layer batch). */
 #define GDN_FLAG_O_BF16    1    /* o is bfloat16 [N_tok][heads][dv], round to nearest even of the
@@ -416,6 +428,163 @@ GDN_API gdn_status gdn_paged_attn(const gdn_attn *p, const void *q, int64_t q_st
  * validation. */
 GDN_API int64_t gdn_paged_attn_workspace(const gdn_attn *p);
 
+/* Linear attention with a decay for each head: layers that keep, like GDN
+ * layers, a state per request and head, but only let it decay and add to it.  With S
+ * the dk x dv state of one unit (request r, head h; the tile layout of the pool above) and
+ * row t of the request,
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T        o_t = scale S_t^T q_t
+ *
+ * g is the logarithm of the decay, at most 0 in most models (0: none, -infinity: the state
+ * before is multiplied by 0): a constant of each head (decay_stride = 0), or given for each row.
+ * Requests, rows and slots are those of the GDN calls, with up to GDN_ATTN_MAX_T rows a request:
+ * single tokens, drafts and prompts.
+ *
+ * Products, sums and states are 32-bit.  With bfloat16 rows, dk 64 or 128, dv a multiple of
+ * 64 and max_T of 48 or more, states and weights are rounded for the tensor cores: to
+ * bfloat16 for o, which is bfloat16 itself, and to 16 bits' significands for what is
+ * added to a state, so a row's o and a state may differ by such roundings from those of calls
+ * with fewer rows.  There a value, key or query that is not finite makes outputs of its request
+ * and head not finite from the row's block of 128 rows on, the block's earlier rows among them;
+ * in shorter calls from its own row on. */
+typedef struct gdn_linear {
+    int32_t batch;               /* B >= 0 requests (B = 0: calls return GDN_OK, no launch) */
+    int32_t heads;               /* H >= 1: states, and heads of v and o */
+    int32_t k_heads;             /* heads of q and k, divides H: head h reads head h / (H / k_heads) */
+    int32_t dk;                  /* 32, 64, 128 or 256 */
+    int32_t dv;                  /* a multiple of 32, 32 .. 256 */
+    int32_t max_T;               /* uniform rows per request (cu_seqlens NULL) or the ragged maximum, 0..GDN_ATTN_MAX_T;
+                                    the kernel is chosen by it, so keep it as small as the rows allow */
+    int32_t dtype;               /* gdn_dtype of q, k, v and o */
+    float scale;                 /* factor on o, finite */
+    const int32_t *cu_seqlens;   /* device [batch+1] token-row offsets, or NULL (uniform) */
+    int64_t n_tok;               /* rows of the arrays: REQUIRED for ragged input, ignored for uniform */
+    const void *q;               /* device [N_tok][k_heads][dk], q_stride elements from a row to the next; may be
+                                    NULL for gdn_linear_commit */
+    const void *k;               /* device [N_tok][k_heads][dk], k_stride elements apart */
+    const void *v;               /* device [N_tok][heads][dv], v_stride elements apart */
+    int64_t q_stride;            /* each at least the row, a multiple of 16 bytes, at most 2^36, and */
+    int64_t k_stride;            /*   N_tok times a stride at most 2^56; pointers 16-byte aligned */
+    int64_t v_stride;
+    const float *log_decay;      /* device float32 [N_tok][heads], decay_stride elements apart, or [heads] */
+    int64_t decay_stride;        /* 0: one row for all; else at least heads, at most 2^36 */
+    float *pool;                 /* device float32 [pool_slots][heads][dk][dv], 16-byte aligned */
+    int64_t pool_slots;          /* >= batch */
+    const int32_t *slot_ids;     /* device [batch], distinct, in [0, pool_slots) */
+    int32_t *dev_err;            /* device int32 error word (GDN_DEVERR_* bits), or NULL */
+} gdn_linear;
+
+/* o for every row from the states in the pool, which stays as it is (drafts).
+ * o: device dtype [N_tok][heads][dv], contiguous, 16-byte aligned; it overlaps nothing else.
+ * A request with a bad slot or bad row offsets is skipped, here and below. */
+GDN_API gdn_status gdn_linear_verify(const gdn_linear *p, void *o, cudaStream_t stream);
+
+/* pool[slot_ids[r]] <- the states after the first accepted[r] rows, for every request with
+ * accepted[r] > 0 (device int32 [batch], in [0, T_r]); all other slots stay as they are. */
+GDN_API gdn_status gdn_linear_commit(const gdn_linear *p, const int32_t *accepted,
+                                     cudaStream_t stream);
+
+/* Both in one pass, of all rows: o for every row, and the states after the last one (single
+ * tokens, prompts).  A request without rows keeps its state. */
+GDN_API gdn_status gdn_linear_step(const gdn_linear *p, void *o, cudaStream_t stream);
+
+/* Accepted lengths and next tokens of sampled drafts, on the device (gdn_accept_prefix
+ * is the greedy form).  Rows are those of the step that verified the drafts: row 0 of a
+ * request is its last token, which is always kept, and row t >= 1 holds a draft, x = draft_ids[row].
+ * Row t of target_probs is the target model's distribution after row t, so a draft at row t
+ * is judged by row t - 1; row t - 1 of draft_probs is the distribution that it was drawn
+ * from, q (NULL: drafts that were looked up, each with q = 1).  In the order of the rows,
+ * draft x stays if
+ *     u_accept[row] q(x) < p(x)
+ * (compared without rounding), and the first that does not ends the request's rows:
+ *     accepted[r] = 1 + the drafts that stay       (0 for a request without rows)
+ * The next token follows the last row kept: drawn from max(p - q, 0) there if a
+ * draft did not stay, from p if all did (and if p <= q everywhere).  With weights w_i in whole
+ * units of 2^-44 (p and q rounded down to them first; NaN and what is below 0 counts as 0, above
+ * 1 as 1), W their sum and U = floor(2^31 u_sample[r]), it is the lowest id i with
+ *     w_0 + ... + w_i > floor(U W / 2^31).
+ * All sums are of integers: the result is the same on every run, whatever the order.
+ *
+ * A draft id outside [0, vocab) does not stay, sets GDN_DEVERR_TOKEN, and the next token is
+ * drawn as for any other; so does a row of p without any weight, whose next_ids is -1. */
+#define GDN_MAX_VOCAB 262144
+
+typedef struct gdn_sample {
+    int32_t batch;               /* B >= 0 */
+    int32_t max_T;               /* uniform rows per request (cu_seqlens NULL) or the ragged maximum, 0..GDN_MAX_T */
+    int32_t vocab;               /* 1 .. GDN_MAX_VOCAB */
+    int32_t reserved;            /* must be 0 */
+    const int32_t *cu_seqlens;   /* device [batch+1] row offsets, or NULL (uniform) */
+    int64_t n_tok;               /* rows: REQUIRED for ragged input, ignored for uniform */
+    const int32_t *draft_ids;    /* device [N_tok]; a request's first is not read */
+    const float *target_probs;   /* device [N_tok][vocab], target_stride elements from a row to the next */
+    int64_t target_stride;       /* >= vocab, at most 2^36 */
+    const float *draft_probs;    /* device [N_tok][vocab], draft_stride elements apart, or NULL */
+    int64_t draft_stride;
+    const float *u_accept;       /* device [N_tok], in [0, 1); a request's first is not read */
+    const float *u_sample;       /* device [batch], in [0, 1); other values are taken to 0 and to 1 - 2^-31 */
+    int32_t *dev_err;            /* device int32 error word, or NULL */
+} gdn_sample;
+
+/* accepted, next_ids: device int32 [batch], written; they overlap nothing else.  accepted is what the
+ * commit calls take, next_ids the tokens to feed next (-1 for a request without rows).  A
+ * request whose rows leave [0, n_tok) or [0, max_T] sets GDN_DEVERR_SEQLEN and gets neither. */
+GDN_API gdn_status gdn_accept_sample(const gdn_sample *p, int32_t *accepted, int32_t *next_ids,
+                                     cudaStream_t stream);
+
+/* The next step of the requests of a paged cache, from lengths that only the device knows (the
+ * rows that were accepted): the lengths move, pages that are no longer needed go back to a
+ * free list and new ones come from it, and the row offsets, slots and positions that the
+ * step's calls read are written.  For request r in order, with a = accepted[r]:
+ *   length   l = kv_len[r] + a, or 0 if done[r] (it has ended, all its pages go back)
+ *   rows     T = rows[r], or max_T when rows is NULL; 0 if done[r]
+ *   pages    n = ceil((l + T) / page_size).  Of its held[r] pages, those in columns n and
+ *            on of its row of the page table go back, behind the free list's last (in the
+ *            order of requests and columns).  If n > held[r], n - held[r] pages come from the
+ *            list's end, the last one first, into columns held[r] and on, after all pages
+ *            of the call have gone back.
+ * A request gets its pages if the list has enough for all that are wanted up to and with its
+ * own (one that wants none goes on in any case).  One that does not keeps the pages it holds,
+ * has no rows in this step and sets GDN_DEVERR_NO_PAGES; its length moves all the same, so plan
+ * again, with accepted NULL, when there are pages.
+ *   kv_len_out[r] = l      held_out[r] = n (or held[r])    free_count_out = pages left
+ *   cu_seqlens = the rows' offsets (what the GDN, linear and attention calls take, with
+ *            n_tok = an upper bound)
+ *   slots[row] = page * page_size + row in the page, and positions[row] = l + t, for every row
+ *            of the step; what lies behind the last row is left as it was
+ * Device errors, each with no rows for the request: rows outside [0, max_T]
+ * (GDN_DEVERR_SEQLEN), kv_len < 0 or held outside [0, max_pages] (GDN_DEVERR_KV_LEN), a < 0 or more
+ * places used than the held pages have (GDN_DEVERR_ACCEPTED): its length and pages
+ * stay (of one that has ended only held is looked at); l + T above max_pages * page_size (GDN_DEVERR_KV_LEN): its length moves, T counts
+ * as 0.  A free count outside [0, n_pages], or more pages going back than the list has room for, sets
+ * GDN_DEVERR_PAGE, and no length or page moves and no request has rows. */
+typedef struct gdn_pages {
+    int32_t batch;               /* B >= 0 (0: GDN_OK, no launch, nothing written) */
+    int32_t max_T;               /* 0..GDN_ATTN_MAX_T; batch * max_T at most 2^31 - 1 */
+    int32_t page_size;           /* 16, 32, 64, 128 or 256 */
+    int32_t max_pages;           /* columns of page_table, >= 1; max_pages * page_size <= 2^31 - 1, batch * max_pages too */
+    int64_t n_pages;             /* entries of free_pages, 1 .. 2^31 - 1 */
+    const int32_t *rows;         /* device [batch], or NULL */
+    const int32_t *accepted;     /* device [batch], or NULL (0 each) */
+    const int32_t *done;         /* device [batch], not 0: ended; or NULL */
+    const int32_t *kv_len;       /* device [batch] */
+    const int32_t *held;         /* device [batch]: pages of each request */
+    const int32_t *free_count;   /* device [1] */
+    int32_t *kv_len_out;         /* device [batch]; each of the three may be its input's array, */
+    int32_t *held_out;           /* device [batch];   or one that overlaps nothing else */
+    int32_t *free_count_out;     /* device [1] */
+    int32_t *free_pages;         /* device [n_pages]: the free list, its first free_count entries */
+    int32_t *page_table;         /* device [batch][max_pages] */
+    int32_t *cu_seqlens;         /* device [batch+1], written */
+    int64_t *slots;              /* device [max_rows], 8-byte aligned, written; or NULL */
+    int32_t *positions;          /* device [max_rows], written; or NULL */
+    int64_t max_rows;            /* entries of slots and positions, >= 0: rows from there on are not
+                                    written and set GDN_DEVERR_SEQLEN */
+    int32_t *dev_err;            /* device int32 error word, or NULL */
+} gdn_pages;
+
+GDN_API gdn_status gdn_plan_pages(const gdn_pages *p, cudaStream_t stream);
+
 /* Waits for `stream`, copies *p->dev_err to *host_code (0 when dev_err is NULL).
  * Returns GDN_ERR_DEVICE_ARG when the word is non-zero, GDN_OK when it is zero. */
 GDN_API gdn_status gdn_read_device_error(const gdn_problem *p, cudaStream_t stream,
@@ -423,6 +592,9 @@ GDN_API gdn_status gdn_read_device_error(const gdn_problem *p, cudaStream_t stre
 
 /* The same for the attention calls: of *p only dev_err is read. */
 GDN_API gdn_status gdn_read_attn_error(const gdn_attn *p, cudaStream_t stream, int32_t *host_code);
+
+/* The same for any error word (device int32, or NULL: no error). */
+GDN_API gdn_status gdn_read_error(const int32_t *dev_err, cudaStream_t stream, int32_t *host_code);
 
 /* Self-check of the bounded waits (diagnostic; not part of a decode step).
  * The chunked kernel waits on shared-memory barriers for its copies and

@@ -25,8 +25,10 @@ GDN_ALGO_AUTO, GDN_ALGO_RECURRENT, GDN_ALGO_CHUNK, GDN_ALGO_CHUNK_TC = 0, 1, 2, 
 GDN_DEVERR_SLOT, GDN_DEVERR_ACCEPTED, GDN_DEVERR_SEQLEN = 1, 2, 4
 GDN_DEVERR_TIMEOUT, GDN_DEVERR_REPLAY = 8, 16
 GDN_DEVERR_KV_LEN, GDN_DEVERR_PAGE = 32, 64
+GDN_DEVERR_TOKEN, GDN_DEVERR_NO_PAGES = 128, 256
 GDN_MAX_T = 1024
 GDN_ATTN_MAX_T = 65536
+GDN_MAX_VOCAB = 262144
 
 # Every symbol include/gdn.h declares.
 EXPORTED = (
@@ -36,6 +38,8 @@ EXPORTED = (
     "gdn_read_device_error", "gdn_selftest_wait_timeout",
     "gdn_select_algo", "gdn_status_string", "gdn_last_error_string", "gdn_version",
     "gdn_rope_append", "gdn_paged_attn", "gdn_paged_attn_workspace", "gdn_read_attn_error",
+    "gdn_linear_verify", "gdn_linear_commit", "gdn_linear_step", "gdn_accept_sample",
+    "gdn_plan_pages", "gdn_read_error",
 )
 
 
@@ -107,6 +111,49 @@ class gdn_rope(ctypes.Structure):
     ]
 
 
+class gdn_linear(ctypes.Structure):
+    """Mirror of the C struct gdn_linear (include/gdn.h), field for field."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+        ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("max_T", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p),
+        ("n_tok", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("log_decay", ctypes.c_void_p),
+        ("decay_stride", ctypes.c_int64), ("pool", ctypes.c_void_p), ("pool_slots", ctypes.c_int64),
+        ("slot_ids", ctypes.c_void_p), ("dev_err", ctypes.c_void_p),
+    ]
+
+
+class gdn_sample(ctypes.Structure):
+    """Mirror of the C struct gdn_sample (include/gdn.h), field for field."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("max_T", ctypes.c_int32), ("vocab", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("n_tok", ctypes.c_int64),
+        ("draft_ids", ctypes.c_void_p), ("target_probs", ctypes.c_void_p),
+        ("target_stride", ctypes.c_int64), ("draft_probs", ctypes.c_void_p),
+        ("draft_stride", ctypes.c_int64), ("u_accept", ctypes.c_void_p),
+        ("u_sample", ctypes.c_void_p), ("dev_err", ctypes.c_void_p),
+    ]
+
+
+class gdn_pages(ctypes.Structure):
+    """Mirror of the C struct gdn_pages (include/gdn.h), field for field."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("max_T", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("rows", ctypes.c_void_p),
+        ("accepted", ctypes.c_void_p), ("done", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("held", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("kv_len_out", ctypes.c_void_p),
+        ("held_out", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("max_rows", ctypes.c_int64), ("dev_err", ctypes.c_void_p),
+    ]
+
+
 _lib_handle: Optional[ctypes.CDLL] = None
 
 
@@ -137,6 +184,13 @@ def lib() -> ctypes.CDLL:
         h.gdn_paged_attn.argtypes = [A, S, I64, S, S, S, I64, S]
         h.gdn_paged_attn_workspace.argtypes = [A]
         h.gdn_paged_attn_workspace.restype = I64
+        L = ctypes.POINTER(gdn_linear)
+        h.gdn_linear_verify.argtypes = [L, S, S]
+        h.gdn_linear_commit.argtypes = [L, S, S]
+        h.gdn_linear_step.argtypes = [L, S, S]
+        h.gdn_accept_sample.argtypes = [ctypes.POINTER(gdn_sample), S, S, S]
+        h.gdn_plan_pages.argtypes = [ctypes.POINTER(gdn_pages), S]
+        h.gdn_read_error.argtypes = [S, S, ctypes.POINTER(ctypes.c_int32)]
         h.gdn_read_device_error.argtypes = [P, S, ctypes.POINTER(ctypes.c_int32)]
         h.gdn_read_attn_error.argtypes = [A, S, ctypes.POINTER(ctypes.c_int32)]
         h.gdn_selftest_wait_timeout.argtypes = [S, S]
@@ -147,7 +201,8 @@ def lib() -> ctypes.CDLL:
                      "gdn_accept_prefix", "gdn_replay_verify", "gdn_replay_commit",
                      "gdn_commit_verify", "gdn_read_device_error", "gdn_selftest_wait_timeout",
                      "gdn_select_algo", "gdn_rope_append", "gdn_paged_attn",
-                     "gdn_read_attn_error"):
+                     "gdn_read_attn_error", "gdn_linear_verify", "gdn_linear_commit",
+                     "gdn_linear_step", "gdn_accept_sample", "gdn_plan_pages", "gdn_read_error"):
             getattr(h, name).restype = ctypes.c_int
         for name in ("gdn_status_string", "gdn_last_error_string", "gdn_version"):
             getattr(h, name).restype = ctypes.c_char_p
@@ -629,4 +684,285 @@ def gdn_read_attn_error(attn: Attn, stream=None) -> int:
     st = lib().gdn_read_attn_error(attn.ref, _attn_stream(attn, stream), ctypes.byref(code))
     if st not in (GDN_OK, GDN_ERR_DEVICE_ARG):
         _raise(st, "gdn_read_attn_error")
+    return code.value
+
+
+# ------------------------------------------------------------------ linear attention
+
+class _Call:
+    """A C struct plus the tensors it points into and the device that the call runs on."""
+
+    def __init__(self, c, refs: tuple, device):
+        self.c = c
+        self.refs = refs
+        self.device = device
+        self.index = device.index if device.type == "cuda" else None
+        self.ref = ctypes.byref(c)
+
+
+class Linear(_Call):
+    """A gdn_linear (one linear attention layer's step)."""
+
+    def __init__(self, c: gdn_linear, refs: tuple, dtype, device):
+        super().__init__(c, refs, device)
+        self.dtype = dtype
+        self.o_shape = (c.n_tok, c.heads, c.dv)
+        self.batch = c.batch
+
+
+def _same_device(t: Optional[torch.Tensor], name: str, device) -> None:
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _heads_rows(t: torch.Tensor, name: str, n: int, heads: int, dim: int) -> int:
+    """Checks that t is [n, heads, dim] with the heads of a row contiguous; its row stride."""
+    if t.dim() != 3 or t.shape != (n, heads, dim):
+        raise ValueError(f"{name} must be {(n, heads, dim)}, is {tuple(t.shape)}")
+    if n == 0:
+        return heads * dim
+    s = t.stride()
+    if s[2] != 1 or (s[1] != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if n > 1 else heads * dim
+
+
+def make_linear(*, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                pool: torch.Tensor, slot_ids: torch.Tensor, max_T: int,
+                cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0,
+                dev_err: Optional[torch.Tensor] = None) -> Linear:
+    """Builds the C description of one linear attention layer's step (include/gdn.h).
+
+    q, k: [N_tok, k_heads, dk], v: [N_tok, heads, dv], all bf16 or all fp32, rows any equal distance
+    apart (slices of a projection's output); q may be None for gdn_linear_commit.  log_decay:
+    fp32, [heads] (constants) or [N_tok, heads]; pool: [slots, heads, dk, dv] fp32; slot_ids: [B]
+    int32; cu_seqlens: [B+1] int32 or None (uniform length max_T)."""
+    dev = pool.device
+    if pool.dim() != 4:
+        raise ValueError("pool must be [slots, heads, dk, dv]")
+    slots, H, dk, dv = pool.shape
+    if k.dtype not in (torch.bfloat16, torch.float32) or v.dtype != k.dtype or \
+            (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k, v must all be bf16 or all fp32")
+    _check(pool, "pool", (torch.float32,), dev)
+    _check(slot_ids, "slot_ids", (torch.int32,), dev)
+    _check(cu_seqlens, "cu_seqlens", (torch.int32,), dev)
+    _check(dev_err, "dev_err", (torch.int32,), dev)
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (log_decay, "log_decay")):
+        _same_device(t, n, dev)
+    batch = slot_ids.numel()
+    if cu_seqlens is not None and cu_seqlens.numel() != batch + 1:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    if k.dim() != 3:
+        raise ValueError("k must be [N_tok, k_heads, dk]")
+    n = k.shape[0]
+    if cu_seqlens is None and n != batch * int(max_T):
+        raise ValueError(f"a uniform step has batch * max_T = {batch * int(max_T)} rows, k has {n}")
+    Hk = k.shape[1]
+    c = gdn_linear()
+    c.batch, c.heads, c.k_heads, c.dk, c.dv, c.max_T = batch, H, Hk, dk, dv, int(max_T)
+    c.dtype = GDN_BF16 if k.dtype == torch.bfloat16 else GDN_FP32
+    c.scale = float(scale)
+    c.cu_seqlens, c.n_tok = _ptr(cu_seqlens), n
+    c.k_stride, c.v_stride = _heads_rows(k, "k", n, Hk, dk), _heads_rows(v, "v", n, H, dv)
+    c.q_stride = c.k_stride if q is None else _heads_rows(q, "q", n, Hk, dk)
+    c.q, c.k, c.v = _ptr(q), _ptr(k), _ptr(v)
+    if log_decay.dtype != torch.float32:
+        raise TypeError(f"log_decay: dtype {log_decay.dtype}, expected torch.float32")
+    if log_decay.shape == (H,):
+        if not log_decay.is_contiguous():
+            raise ValueError("log_decay must be contiguous")
+        c.decay_stride = 0
+    elif log_decay.shape == (n, H):
+        if log_decay.stride(1) != 1 and H > 1:
+            raise ValueError("log_decay: the heads of a row must be contiguous")
+        # (one row, or rows that an expand() made the same: constants)
+        c.decay_stride = log_decay.stride(0) if n > 1 else 0
+    else:
+        raise ValueError(f"log_decay must be {(H,)} or {(n, H)}, is {tuple(log_decay.shape)}")
+    c.log_decay = _ptr(log_decay)
+    c.pool, c.pool_slots, c.slot_ids, c.dev_err = _ptr(pool), slots, _ptr(slot_ids), _ptr(dev_err)
+    return Linear(c, (q, k, v, log_decay, pool, slot_ids, cu_seqlens, dev_err), k.dtype, dev)
+
+
+def _call(fn, name: str, call: _Call, stream, *args) -> None:
+    """fn(struct, *args, stream) on the call's own device."""
+    index = call.index
+    if index is None:
+        raise ValueError(f"the tensors are on {call.device}, expected a CUDA device")
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(fn, name, call, stream, *args)
+    st = fn(call.ref, *args, _attn_stream(call, stream))
+    if st:
+        _raise(st, name)
+
+
+def _check_o(lin: Linear, o: torch.Tensor) -> None:
+    if o.dtype is not lin.dtype:
+        raise TypeError(f"o: dtype {o.dtype}, expected {lin.dtype}")
+    if o.device != lin.device:
+        raise ValueError(f"o is on {o.device}, expected {lin.device}")
+    if o.shape != lin.o_shape or not o.is_contiguous():
+        raise ValueError(f"o must be contiguous and {lin.o_shape}, is {tuple(o.shape)}")
+
+
+def _check_requests(t: torch.Tensor, name: str, call: _Call, batch: int) -> None:
+    _check(t, name, (torch.int32,), call.device)
+    if t.numel() != batch:
+        raise ValueError(f"{name} must be [batch] = [{batch}]")
+
+
+def gdn_linear_verify(lin: Linear, o: torch.Tensor, stream=None) -> None:
+    """o [N_tok, heads, dv] (the type of q) for every row; the states stay."""
+    _check_o(lin, o)
+    _call(lib().gdn_linear_verify, "gdn_linear_verify", lin, stream, o.data_ptr())
+
+
+def gdn_linear_commit(lin: Linear, accepted: torch.Tensor, stream=None) -> None:
+    """The states after the first accepted[r] rows (int32 [batch]) into the pool."""
+    _check_requests(accepted, "accepted", lin, lin.batch)
+    _call(lib().gdn_linear_commit, "gdn_linear_commit", lin, stream, accepted.data_ptr())
+
+
+def gdn_linear_step(lin: Linear, o: torch.Tensor, stream=None) -> None:
+    """o for every row, and the states after the last one into the pool."""
+    _check_o(lin, o)
+    _call(lib().gdn_linear_step, "gdn_linear_step", lin, stream, o.data_ptr())
+
+
+# ------------------------------------------------------------------ sampled drafts
+
+class Sample(_Call):
+    """A gdn_sample (drafts, both models' probabilities and the random numbers of a step)."""
+
+    def __init__(self, c: gdn_sample, refs: tuple, device):
+        super().__init__(c, refs, device)
+        self.batch = c.batch
+
+
+def _probs(t: torch.Tensor, name: str, n: int, vocab: int, device) -> int:
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.float32")
+    _same_device(t, name, device)
+    if t.dim() != 2 or t.shape != (n, vocab):
+        raise ValueError(f"{name} must be {(n, vocab)}, is {tuple(t.shape)}")
+    if n and vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return t.stride(0) if n > 1 else vocab
+
+
+def make_sample(*, draft_ids: torch.Tensor, target_probs: torch.Tensor, u_accept: torch.Tensor,
+                u_sample: torch.Tensor, max_T: int, draft_probs: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None,
+                dev_err: Optional[torch.Tensor] = None) -> Sample:
+    """Builds the C description of one acceptance (include/gdn.h).
+
+    draft_ids: [N_tok] int32, the step's rows (each request's last token, then its drafts);
+    target_probs, draft_probs: [N_tok, vocab] fp32, rows any equal distance apart; draft_probs None:
+    drafts without a distribution; u_accept: [N_tok], u_sample: [B] fp32 in [0, 1); cu_seqlens:
+    [B+1] int32 or None (uniform length max_T)."""
+    dev = u_sample.device
+    for t, n in ((draft_ids, "draft_ids"), (cu_seqlens, "cu_seqlens"), (dev_err, "dev_err")):
+        _check(t, n, (torch.int32,), dev)
+    for t, n in ((u_accept, "u_accept"), (u_sample, "u_sample")):
+        _check(t, n, (torch.float32,), dev)
+    batch, n = u_sample.numel(), draft_ids.numel()
+    if cu_seqlens is not None and cu_seqlens.numel() != batch + 1:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    if cu_seqlens is None and n != batch * int(max_T):
+        raise ValueError(f"a uniform step has batch * max_T = {batch * int(max_T)} rows, draft_ids has {n}")
+    if u_accept.numel() != n:
+        raise ValueError("u_accept must be [N_tok]")
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [N_tok, vocab]")
+    c = gdn_sample()
+    c.batch, c.max_T, c.vocab, c.reserved = batch, int(max_T), target_probs.shape[1], 0
+    c.cu_seqlens, c.n_tok, c.draft_ids = _ptr(cu_seqlens), n, _ptr(draft_ids)
+    c.target_stride = _probs(target_probs, "target_probs", n, c.vocab, dev)
+    c.target_probs, c.draft_probs = _ptr(target_probs), _ptr(draft_probs)
+    c.draft_stride = c.vocab if draft_probs is None else _probs(draft_probs, "draft_probs", n, c.vocab, dev)
+    c.u_accept, c.u_sample, c.dev_err = _ptr(u_accept), _ptr(u_sample), _ptr(dev_err)
+    return Sample(c, (draft_ids, target_probs, draft_probs, u_accept, u_sample, cu_seqlens, dev_err), dev)
+
+
+def gdn_accept_sample(sample: Sample, accepted: torch.Tensor, next_ids: torch.Tensor,
+                      stream=None) -> None:
+    """accepted [B] <- rows kept of each request (what the commit calls take), next_ids [B] <- the
+    token that follows them (int32)."""
+    _check_requests(accepted, "accepted", sample, sample.batch)
+    _check_requests(next_ids, "next_ids", sample, sample.batch)
+    _call(lib().gdn_accept_sample, "gdn_accept_sample", sample, stream, accepted.data_ptr(),
+          next_ids.data_ptr())
+
+
+# ------------------------------------------------------------------ pages
+
+class Pages(_Call):
+    """A gdn_pages (the lengths, page table and free list of a paged cache)."""
+
+
+def make_pages(*, page_table: torch.Tensor, page_size: int, max_T: int, kv_len: torch.Tensor,
+               held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+               cu_seqlens: torch.Tensor, rows: Optional[torch.Tensor] = None,
+               accepted: Optional[torch.Tensor] = None, done: Optional[torch.Tensor] = None,
+               kv_len_out: Optional[torch.Tensor] = None, held_out: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None,
+               dev_err: Optional[torch.Tensor] = None) -> Pages:
+    """Builds the C description of a paged cache's next step (include/gdn.h).
+
+    int32 tensors: page_table [B, max_pages], kv_len and held [B], free_pages [n_pages], free_count
+    [1], cu_seqlens [B+1] (written), rows, accepted and done [B] or None; kv_len_out, held_out and
+    free_count_out: None for in place.  slots (int64) and positions (int32) [max_rows], written, or
+    None."""
+    dev = page_table.device
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    batch, max_pages = page_table.shape
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    for t, n, size in ((page_table, "page_table", None), (kv_len, "kv_len", batch), (held, "held", batch),
+                       (rows, "rows", batch), (accepted, "accepted", batch), (done, "done", batch),
+                       (kv_len_out, "kv_len_out", batch), (held_out, "held_out", batch),
+                       (free_count, "free_count", 1), (free_count_out, "free_count_out", 1),
+                       (cu_seqlens, "cu_seqlens", batch + 1), (free_pages, "free_pages", None),
+                       (positions, "positions", None), (dev_err, "dev_err", None)):
+        _check(t, n, (torch.int32,), dev)
+        if t is not None and size is not None and t.numel() != size:
+            raise ValueError(f"{n} must have {size} entries, has {t.numel()}")
+    _check(slots, "slots", (torch.int64,), dev)
+    sizes = {t.numel() for t in (slots, positions) if t is not None}
+    if len(sizes) > 1:
+        raise ValueError("slots and positions must have the same size")
+    c = gdn_pages()
+    c.batch, c.max_T, c.page_size, c.max_pages = batch, int(max_T), int(page_size), max_pages
+    c.n_pages = free_pages.numel()
+    c.rows, c.accepted, c.done = _ptr(rows), _ptr(accepted), _ptr(done)
+    c.kv_len, c.held, c.free_count = _ptr(kv_len), _ptr(held), _ptr(free_count)
+    c.kv_len_out, c.held_out, c.free_count_out = _ptr(kv_len_out), _ptr(held_out), _ptr(free_count_out)
+    c.free_pages, c.page_table, c.cu_seqlens = _ptr(free_pages), _ptr(page_table), _ptr(cu_seqlens)
+    c.slots, c.positions = _ptr(slots), _ptr(positions)
+    c.max_rows = sizes.pop() if sizes else 0
+    c.dev_err = _ptr(dev_err)
+    return Pages(c, (page_table, kv_len, held, free_pages, free_count, cu_seqlens, rows, accepted, done,
+                     kv_len_out, held_out, free_count_out, slots, positions, dev_err), dev)
+
+
+def gdn_plan_pages(pages: Pages, stream=None) -> None:
+    """The next step's lengths, pages, row offsets, slots and positions."""
+    _call(lib().gdn_plan_pages, "gdn_plan_pages", pages, stream)
+
+
+def gdn_read_error(dev_err: torch.Tensor, stream=None) -> int:
+    """Waits for the stream and returns an error word (GDN_DEVERR_* bits, 0: none)."""
+    _check(dev_err, "dev_err", (torch.int32,), None)
+    if dev_err.device.type != "cuda":
+        raise ValueError(f"dev_err is on {dev_err.device}, expected a CUDA device")
+    code = ctypes.c_int32(0)
+    with torch.cuda.device(dev_err.device):
+        st = lib().gdn_read_error(_ptr(dev_err), _stream(stream), ctypes.byref(code))
+    if st not in (GDN_OK, GDN_ERR_DEVICE_ARG):
+        _raise(st, "gdn_read_error")
     return code.value

@@ -496,9 +496,173 @@ gdn::AttnArgs attn_args(const gdn_attn *p, const void *q, int64_t q_stride, void
     return a;
 }
 
+// ------------------------------------------------------------ linear attention
+
+// Whether rows of `row` elements of esz bytes, n of them `stride` apart, are well formed.
+bool row_stride_ok(int64_t n, int64_t stride, int64_t row, int64_t esz) {
+    return stride >= row && stride <= (1ll << 36) && stride * esz % 16 == 0 && span_ok(n, stride);
+}
+// The bytes they span.
+Range strided(const void *ptr, int64_t n, int64_t stride, int64_t row, int64_t esz) {
+    return range(ptr, n > 0 ? ((n - 1) * stride + row) * esz : 0);
+}
+
+gdn_status run_linear(const gdn_linear *p, int mode, const int32_t *accepted, void *o,
+                      cudaStream_t stream) {
+    const bool commit = mode == gdn::kCommit;
+    if (!p) return GDN_ERR_NULL_PTR;
+    if (p->batch < 0 || p->heads < 1 || p->k_heads < 1 || p->heads % p->k_heads != 0 || p->max_T < 0 ||
+        p->max_T > GDN_ATTN_MAX_T || !std::isfinite(p->scale) ||
+        (int64_t)p->batch * p->heads > 0x7fffffffLL / 8)
+        return GDN_ERR_BAD_DIM;
+    if (p->dtype != GDN_FP32 && p->dtype != GDN_BF16) return GDN_ERR_BAD_DTYPE;
+    if ((p->dk != 32 && p->dk != 64 && p->dk != 128 && p->dk != 256) || p->dv < 32 || p->dv > 256 ||
+        p->dv % 32 != 0)
+        return GDN_ERR_UNSUPPORTED;
+    if (p->cu_seqlens && p->n_tok < 0) return GDN_ERR_BAD_DIM;
+    const int64_t n = p->cu_seqlens ? p->n_tok : (int64_t)p->batch * p->max_T;
+    if (n > 0x7fffffffLL) return GDN_ERR_BAD_DIM;
+    if (p->batch == 0 || n == 0) return GDN_OK;
+    if (p->pool_slots < p->batch || p->pool_slots > 0x7fffffffLL) return GDN_ERR_BAD_DIM;
+    const int64_t esz = p->dtype == GDN_BF16 ? 2 : 4;
+    const int64_t krow = (int64_t)p->k_heads * p->dk, vrow = (int64_t)p->heads * p->dv;
+    if ((!commit && !row_stride_ok(n, p->q_stride, krow, esz)) || !row_stride_ok(n, p->k_stride, krow, esz) ||
+        !row_stride_ok(n, p->v_stride, vrow, esz) || !span_ok(p->pool_slots, vrow * p->dk) ||
+        (p->decay_stride != 0 && (p->decay_stride < p->heads || p->decay_stride > (1ll << 36) ||
+                                  !span_ok(n, p->decay_stride))))
+        return GDN_ERR_BAD_DIM;
+    if ((!commit && (!p->q || !o)) || !p->k || !p->v || !p->log_decay || !p->pool || !p->slot_ids ||
+        (commit && !accepted))
+        return GDN_ERR_NULL_PTR;
+    if ((!commit && (!aligned16(p->q) || !aligned16(o))) || !aligned16(p->k) || !aligned16(p->v) ||
+        !aligned16(p->pool) || !aligned4(p->log_decay) || !aligned4(p->slot_ids) ||
+        !aligned4(p->cu_seqlens) || !aligned4(accepted) || !aligned4(p->dev_err))
+        return GDN_ERR_ALIGN;
+    const Range rp = range(p->pool, p->pool_slots * vrow * p->dk * 4);
+    const Range ro = range(commit ? nullptr : o, n * vrow * esz);
+    const Range ins[] = {strided(commit ? nullptr : p->q, n, p->q_stride, krow, esz),
+                         strided(p->k, n, p->k_stride, krow, esz),
+                         strided(p->v, n, p->v_stride, vrow, esz),
+                         strided(p->log_decay, p->decay_stride ? n : 1, p->decay_stride, p->heads, 4),
+                         range(p->slot_ids, (int64_t)p->batch * 4),
+                         range(p->cu_seqlens, p->cu_seqlens ? ((int64_t)p->batch + 1) * 4 : 0),
+                         range(accepted, commit ? (int64_t)p->batch * 4 : 0),
+                         range(p->dev_err, p->dev_err ? 4 : 0)};
+    for (const Range &x : ins)
+        if (overlap(ro, x) || (mode != gdn::kVerify && overlap(rp, x))) return GDN_ERR_ALIAS;
+    if (overlap(ro, rp)) return GDN_ERR_ALIAS;
+    gdn::LinearArgs a;
+    a.g = *p;
+    a.g.n_tok = n;
+    a.group = p->heads / p->k_heads;
+    a.accepted = commit ? accepted : nullptr;
+    a.o = commit ? nullptr : o;
+    const cudaError_t e = gdn::launch_linear(a, mode, stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, "kernel launch");
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+gdn_status gdn_linear_verify(const gdn_linear *p, void *o, cudaStream_t stream) {
+    return run_linear(p, gdn::kVerify, nullptr, o, stream);
+}
+
+gdn_status gdn_linear_commit(const gdn_linear *p, const int32_t *accepted, cudaStream_t stream) {
+    return run_linear(p, gdn::kCommit, accepted, nullptr, stream);
+}
+
+gdn_status gdn_linear_step(const gdn_linear *p, void *o, cudaStream_t stream) {
+    return run_linear(p, gdn::kFused, nullptr, o, stream);
+}
+
+gdn_status gdn_accept_sample(const gdn_sample *p, int32_t *accepted, int32_t *next_ids,
+                             cudaStream_t stream) {
+    if (!p) return GDN_ERR_NULL_PTR;
+    if (p->reserved != 0 || p->batch < 0 || p->max_T < 0 || p->max_T > GDN_MAX_T || p->vocab < 1 ||
+        p->vocab > GDN_MAX_VOCAB || p->batch > 0x7fffffff / 16)
+        return GDN_ERR_BAD_DIM;
+    if (p->batch == 0) return GDN_OK;
+    if (p->cu_seqlens && p->n_tok < 0) return GDN_ERR_BAD_DIM;
+    const int64_t n = p->cu_seqlens ? p->n_tok : (int64_t)p->batch * p->max_T;
+    if (n > 0x7fffffffLL) return GDN_ERR_BAD_DIM;
+    auto stride_bad = [&](int64_t s) { return s < p->vocab || s > (1ll << 36) || !span_ok(n, s); };
+    if (n > 0 && (stride_bad(p->target_stride) || (p->draft_probs && stride_bad(p->draft_stride))))
+        return GDN_ERR_BAD_DIM;
+    if (!accepted || !next_ids || !p->u_sample) return GDN_ERR_NULL_PTR;
+    if (n > 0 && (!p->draft_ids || !p->target_probs || !p->u_accept)) return GDN_ERR_NULL_PTR;
+    if (!aligned4(p->cu_seqlens) || !aligned4(p->draft_ids) || !aligned4(p->target_probs) ||
+        !aligned4(p->draft_probs) || !aligned4(p->u_accept) || !aligned4(p->u_sample) ||
+        !aligned4(p->dev_err) || !aligned4(accepted) || !aligned4(next_ids))
+        return GDN_ERR_ALIGN;
+    const Range ra = range(accepted, (int64_t)p->batch * 4), rn = range(next_ids, (int64_t)p->batch * 4);
+    const Range ins[] = {range(p->cu_seqlens, p->cu_seqlens ? ((int64_t)p->batch + 1) * 4 : 0),
+                         range(p->draft_ids, n * 4), range(p->u_accept, n * 4),
+                         strided(p->target_probs, n, p->target_stride, p->vocab, 4),
+                         strided(p->draft_probs, n, p->draft_stride, p->vocab, 4),
+                         range(p->u_sample, (int64_t)p->batch * 4), range(p->dev_err, p->dev_err ? 4 : 0)};
+    for (const Range &x : ins)
+        if (overlap(ra, x) || overlap(rn, x)) return GDN_ERR_ALIAS;
+    if (overlap(ra, rn)) return GDN_ERR_ALIAS;
+    const cudaError_t e = gdn::launch_sample(*p, n, accepted, next_ids, stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, "kernel launch");
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+gdn_status gdn_plan_pages(const gdn_pages *p, cudaStream_t stream) {
+    if (!p) return GDN_ERR_NULL_PTR;
+    if (p->batch < 0 || p->max_T < 0 || p->max_T > GDN_ATTN_MAX_T ||
+        (int64_t)p->batch * p->max_T > 0x7fffffffLL || p->max_pages < 1 || p->n_pages < 1 ||
+        p->n_pages > 0x7fffffffLL || p->max_rows < 0 || p->max_rows > 0x7fffffffLL)
+        return GDN_ERR_BAD_DIM;
+    if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128 &&
+        p->page_size != 256)
+        return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)p->max_pages * p->page_size > 0x7fffffffLL ||
+        (int64_t)p->batch * p->max_pages > 0x7fffffffLL)
+        return GDN_ERR_BAD_DIM;
+    if (p->batch == 0) return GDN_OK;
+    if (!p->kv_len || !p->held || !p->free_count || !p->kv_len_out || !p->held_out ||
+        !p->free_count_out || !p->free_pages || !p->page_table || !p->cu_seqlens)
+        return GDN_ERR_NULL_PTR;
+    const void *words[] = {p->rows, p->accepted, p->done, p->kv_len, p->held, p->free_count,
+                           p->kv_len_out, p->held_out, p->free_count_out, p->free_pages, p->page_table,
+                           p->cu_seqlens, p->positions, p->dev_err};
+    for (const void *w : words)
+        if (!aligned4(w)) return GDN_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(p->slots) & 7u) != 0) return GDN_ERR_ALIGN;
+    const int64_t B4 = (int64_t)p->batch * 4;
+    auto given = [](const void *ptr, int64_t bytes) { return range(ptr, ptr ? bytes : 0); };
+    // Every array that is written overlaps no other; three may be the input of the same name.
+    const Range out[] = {range(p->kv_len_out, B4), range(p->held_out, B4), range(p->free_count_out, 4),
+                         range(p->free_pages, p->n_pages * 4),
+                         range(p->page_table, B4 * p->max_pages), range(p->cu_seqlens, B4 + 4),
+                         given(p->slots, p->max_rows * 8), given(p->positions, p->max_rows * 4),
+                         given(p->dev_err, 4)};
+    const Range in[] = {range(p->kv_len, B4), range(p->held, B4), range(p->free_count, 4),
+                        given(p->rows, B4), given(p->accepted, B4), given(p->done, B4)};
+    constexpr int kOut = sizeof(out) / sizeof(out[0]), kIn = sizeof(in) / sizeof(in[0]);
+    for (int i = 0; i < kOut; ++i) {
+        for (int j = i + 1; j < kOut; ++j)
+            if (overlap(out[i], out[j])) return GDN_ERR_ALIAS;
+        for (int j = 0; j < kIn; ++j)
+            if (overlap(out[i], in[j]) && !(i == j && i < 3 && out[i].lo == in[j].lo)) return GDN_ERR_ALIAS;
+    }
+    const cudaError_t e = gdn::launch_pages(*p, stream);
+    if (e != cudaSuccess) {
+        set_cuda_error(e, "kernel launch");
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
 
 gdn_status gdn_rope_append(const gdn_attn *p, const gdn_rope *rope, const void *q,
                            int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -671,6 +835,11 @@ gdn_status gdn_read_device_error(const gdn_problem *p, cudaStream_t stream, int3
 gdn_status gdn_read_attn_error(const gdn_attn *p, cudaStream_t stream, int32_t *host_code) {
     if (!p || !host_code) return GDN_ERR_NULL_PTR;
     return read_error_word(p->dev_err, stream, host_code, "gdn_read_attn_error");
+}
+
+gdn_status gdn_read_error(const int32_t *dev_err, cudaStream_t stream, int32_t *host_code) {
+    if (!host_code) return GDN_ERR_NULL_PTR;
+    return read_error_word(dev_err, stream, host_code, "gdn_read_error");
 }
 
 int32_t gdn_select_algo(const gdn_problem *p) {

@@ -8,6 +8,7 @@
 
 #include "gdn_attn.cuh"
 #include "gdn_device.cuh"
+#include "gdn_linear.cuh"
 
 namespace gdn {
 
@@ -27,6 +28,16 @@ cudaError_t launch_chunk(const Args *layers, int n, int mode, cudaStream_t strea
 cudaError_t launch_accept(int B, int max_T, const int32_t *cu_seqlens, long long n_tok,
                           const int32_t *draft, const int32_t *target, int32_t *accepted,
                           int32_t *dev_err, cudaStream_t stream);
+
+// Accepted lengths and next tokens of sampled drafts, and the next step's pages (arguments already
+// validated on the host; n_tok: rows, for uniform input too).
+cudaError_t launch_sample(const gdn_sample &g, long long n_tok, int32_t *accepted, int32_t *next_ids,
+                          cudaStream_t stream);
+cudaError_t launch_pages(const gdn_pages &g, cudaStream_t stream);
+
+// Linear attention (arguments already validated on the host); mode: kVerify, kCommit, or kFused
+// for a step.
+cudaError_t launch_linear(const LinearArgs &a, int mode, cudaStream_t stream);
 
 // One block that waits on a barrier nothing completes, until the bounded wait
 // gives up; ORs GDN_DEVERR_TIMEOUT into *dev_err (not NULL).
