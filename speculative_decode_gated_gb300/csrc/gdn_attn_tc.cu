@@ -37,15 +37,11 @@
 // any row's mask hides something (the ends of a unit) a warp therefore clears them
 // from the value tile first; the rows that do see such a value get it
 // added at the end (add_unbounded).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstdint>
-#include <mutex>
 
 #include "gdn_attn.cuh"
 #include "gdn_launch.h"
-#include "gdn_wait.cuh"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace {
@@ -96,44 +92,6 @@ struct Shared {
     Segment seg[kSegs];  // r = -1: no more
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ uint32_t bar(const unsigned long long &b) { return smem_addr(&b); }
-
-__device__ __forceinline__ void arrive(uint32_t b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(b) : "memory");
-}
-// One arrival a warp, after all its threads' work.
-__device__ __forceinline__ void arrive_warp(uint32_t b) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) arrive(b);
-}
-__device__ __forceinline__ void arrive_expect(uint32_t b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(b), "r"(bytes)
-                 : "memory");
-}
-
-// Bounded wait of one thread; false once any role of the block has given up.
-__device__ __forceinline__ bool wait_one(uint32_t b, uint32_t parity, int *dead) {
-    if (mbar_try_wait(b, parity)) return true;
-    unsigned long long t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(b, parity)) return true;
-        if ((it & 63) == 0) {
-            if (*(volatile int *)dead) return false;
-            const unsigned long long now = globaltimer();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitNs) *(volatile int *)dead = 1;
-        }
-    }
-}
-// The same by all 32 threads of a warp, with one answer.
-__device__ __forceinline__ bool wait(uint32_t b, uint32_t parity, int *dead) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
-    return __all_sync(0xffffffffu, wait_one(b, parity, dead));
-}
-
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
                                        int c3, uint32_t b) {
     asm volatile(
@@ -141,122 +99,6 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int
         " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(b)
         : "memory");
-}
-
-// Shared-memory matrix descriptors, 128-byte swizzle: rows of 128 bytes in groups of
-// eight, 1024 bytes apart; the low word is the address and the distance of the column
-// boxes (both in 16 bytes; an offset within a tile is added to it), the high one the same
-// for all.
-constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
-    return (addr >> 4) | (lbo >> 4) << 16;
-}
-
-// kind::f16, bf16 operands, float32 accumulator, M = 128; A K-major, B K- or MN-major.
-__host__ __device__ constexpr uint32_t idesc(uint32_t n, bool b_mn_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) |
-           ((128u >> 4) << 24);
-}
-
-// The whole warp calls these with the same arguments, so that they stay in uniform
-// registers; the thread with `lead` set issues.
-__device__ __forceinline__ uint32_t elect() {
-    uint32_t lead;
-    asm volatile(
-        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(lead));
-    return lead;
-}
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id,
-                                       uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
-        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id,
-                                       uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
-        " mov.b64 db, {%2, %5};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t lead, uint32_t b) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(b),
-        "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-}
-__device__ __forceinline__ void fence_async() {
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-}
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
-#define GDN_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
-#define GDN_W4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
-// 32 columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-        "%30, %31}, [%32];\n"
-        : GDN_R4(r, 0), GDN_R4(r, 4), GDN_R4(r, 8), GDN_R4(r, 12), GDN_R4(r, 16), GDN_R4(r, 20),
-          GDN_R4(r, 24), GDN_R4(r, 28)
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-        "%30, %31, %32};\n" ::"r"(addr),
-        GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12), GDN_W4(r, 16), GDN_W4(r, 20),
-        GDN_W4(r, 24), GDN_W4(r, 28)
-        : "memory");
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Two float32 at a time.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Places of a TMA box: a page, or a tile's worth of one.
@@ -268,18 +110,6 @@ struct Launch {
     AttnArgs a;
     CUtensorMap k, v, q;
     int q_tma;  // the queries come by TMA too: a power of two of heads a group, up to 128
-};
-
-// A ring slot and the parity of its round; advances through the ring.
-template <int NS>
-struct Ring {
-    uint32_t slot = 0, parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == NS) {
-            slot = 0;
-            parity ^= 1;
-        }
-    }
 };
 
 // ---------------------------------------------------------------- the segment thread
@@ -1030,20 +860,6 @@ __global__ void __launch_bounds__(Cfg<HD, NWG>::kThreads, Cfg<HD, NWG>::kBlocks)
 }
 
 // ---------------------------------------------------------------- host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
 
 // Pages [n_pages][kv_heads][page][hd]; boxes of 64 columns by up to a tile's places of
 // one head of one page.  Pages past the end read as zeros.

@@ -6,8 +6,9 @@
 //     o_i = scale (d(i, -1) S^T q_i + sum_{j <= i} d(i, j) (q_i . k_j) v_j)
 //     S  <- d(n - 1, -1) S + sum_j d(n - 1, j) k_j v_j^T
 // which needs one multiply-add a state element and row for each of the two, where the recurrence
-// row by row needs two for the second.  Decays are products of single ones, so a decay of 0
-// (g = -infinity) is no special case and nothing cancels.
+// row by row needs two for the second.  Each decay is the exponential of a sum (products of
+// rounded decays would be off by as many roundings as rows), and each sum is its own, so nothing
+// cancels and a decay of 0 (g = -infinity) is no special case.
 //
 // A block holds dk x CV of a state in registers, a thread R rows of four columns, two rows to a
 // packed float32 operand.  Blocks of later rows follow with the state in place.
@@ -116,13 +117,17 @@ __global__ void __launch_bounds__(Shape<T, DK, CV, C>::NT) linear_kernel(const L
             const int i = e / (CV / VE), c = e % (CV / VE) * VE;
             stage(&sv[i][c], v + (row + i) * g.v_stride + c);
         }
-        // Column j + 1 of the decays, by products down the column.
+        // Column j + 1 of the decays: sums down the column.
         if (tid <= n) {
-            float d = 1.f;
+            float gs[C], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                gs[i] = i < n ? __ldg(g.log_decay + (row + i) * g.decay_stride + h) : 0.f;
             if (tid > 0) sd[tid - 1][tid] = 1.f;
-            for (int i = tid; i < n; ++i) {
-                d *= expf(g.log_decay[(row + i) * g.decay_stride + h]);
-                sd[i][tid] = d;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                sum += i >= tid ? gs[i] : 0.f;
+                if (i >= tid && i < n) sd[i][tid] = expf(sum);
             }
         }
         __syncthreads();
@@ -308,6 +313,7 @@ cudaError_t launch_type(const LinearArgs &a, int mode, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs &a, int mode, cudaStream_t stream) {
+    if (linear_tc_runs(a.g)) return launch_linear_tc(a, mode, stream);
     return a.g.dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(a, mode, stream)
                                  : launch_type<float>(a, mode, stream);
 }
