@@ -8,13 +8,13 @@
 //     U  = K^T W,  W_j = d(C - 1, j) v_j                     S <- e^{G_(C-1)} S + U
 // Only S goes from block to block: everything else runs ahead of it, in roles that
 // hand on through barriers:
-//   TMA warp     Q, K and V tiles, two blocks ahead (128-byte swizzle)
+//   TMA warp     K and V tiles, two blocks ahead (128-byte swizzle)
 //   MMA warp     the four products
-//   weights      (warpgroup, a thread a row) the decays, and W in three bf16 terms, which hold
-//                the float32 product v_j d whole: a state is as exact as its float32 sums
+//   weights      (warpgroup, a thread a row) the decays, and W in two bf16 terms: each product v_j d
+//                enters its state to 2^-17 of itself
 //   mask         (a thread a row) scores times decays to P, in tensor memory over the scores
 //   state        (a thread a row of dk) S in registers, its bf16 copy in shared memory for O2
-//   output       (a thread a row) o, through the block's Q tile, and by TMA to global memory
+//   output       (a thread a row) Q to tensor memory, from where both its products take it, and o
 //
 // Decays.  No exponent is positive and nothing cancels: within a warp's 32 rows, e^{...} of sums
 // taken from the row to the end of the 32 (cf) or from their start to the row (rowf); t, those
@@ -33,16 +33,19 @@ constexpr int C = 128;               // rows of a block
 constexpr int NV = 64;               // value columns
 constexpr int kBox = C * 128;        // bytes of 64 columns of a tile
 constexpr int kKeyTile = 2 * kBox;   // of queries, keys (dk = 64: the second half is not used)
+constexpr int kAhead = 4;            // blocks that come to L2 before
 constexpr int kThreads = 18 * 32;    // weights, mask, state, output; TMA, MMA
-constexpr int kTiles = 4 * kKeyTile + 2 * kBox + 3 * kBox + kBox;  // Q, K: 2; V: 2; W: 3 terms; S
+constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
+constexpr int kTiles = 2 * kKeyTile + 2 * kBox + 2 * kWTile + kBox;  // K, V and W twice; S
 
 // Columns of tensor memory.
-constexpr uint32_t kScores = 0, kO1 = 256, kO2 = 320, kU = 384;
+constexpr uint32_t kScores = 0, kQ = 128, kO1 = 256, kO2 = 320, kU = 384;  // (kU: two terms)
 
 struct Bars {
-    unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    unsigned long long dec_full[2], dec_empty[2], s_full[2], p_ready[2], u_full[2], u_free[2];
-    unsigned long long w_ready, w_free, st_ready, st_free, o_full, o_free, w_sync, o_sync, drain;
+    unsigned long long q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    unsigned long long dec_full[2], dec_empty[2];
+    unsigned long long w_ready[2][4], w_free[2][4];  // by 32 rows
+    unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, w_sync, drain;
 };
 
 struct Shared {
@@ -56,8 +59,9 @@ static_assert(kTiles + sizeof(Shared) <= 232448, "227 KB of shared memory");
 
 struct Launch {
     LinearArgs a;
-    CUtensorMap q, k, v, o;
+    CUtensorMap k, v;
     int slices;
+    bool q32, o32;  // rows are aligned to 32 bytes
     long long units;
 };
 
@@ -90,11 +94,37 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(b)
         : "memory");
 }
-__device__ __forceinline__ void tma_store(const CUtensorMap *map, int x, int y, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+// Into L2 only.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(src)
+                 "r"(x), "r"(y)
                  : "memory");
+}
+// 32 bytes of global memory: at once where they are aligned so (rows are to 16).
+__device__ __forceinline__ void ldg32(const void *at, bool whole, uint32_t *x) {
+    if (whole) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+                       "=r"(x[7])
+                     : "l"(at));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[e]), "=r"(x[e + 1]), "=r"(x[e + 2]), "=r"(x[e + 3])
+                         : "l"(static_cast<const char *>(at) + 4 * e));
+    }
+}
+__device__ __forceinline__ void stg32(void *at, bool whole, const uint32_t *x) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]),
+                     "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(at)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        static_cast<uint4 *>(at)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
 }
 __device__ __forceinline__ void lds128(uint32_t at, uint32_t *x) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -137,9 +167,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // Shared-memory tiles.
 struct Tiles {
-    uint32_t q, k, v, w, s;
+    uint32_t k, v, w, s;
     __device__ __forceinline__ explicit Tiles(uint32_t base)
-        : q(base), k(base + 2 * kKeyTile), v(base + 4 * kKeyTile), w(v + 2 * kBox), s(w + 3 * kBox) {}
+        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + 2 * kWTile) {}
 };
 
 // The logarithm of row i's decay (0 for rows past the block's end).
@@ -150,30 +180,29 @@ __device__ __forceinline__ float log_decay(const gdn_linear &g, const Unit &x, i
 
 // ---------------------------------------------------------------- the TMA warp (one thread)
 
-template <bool OUT>
-__device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tiles &t, uint32_t &issued) {
+__device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tiles &t, bool commit,
+                                          uint32_t &issued) {
     const gdn_linear &g = L.a.g;
     const int boxes = g.dk / 64;
     long long at = blockIdx.x;
     Unit x;
-    while (next_unit(L, !OUT, at, x)) {
+    while (next_unit(L, commit, at, x)) {
         const int kx = x.h / L.a.group * g.dk, vx = x.h * g.dv + x.c0;
         for (int c = 0; c < x.n; ++c, ++issued) {
             const uint32_t slot = issued & 1, free = ((issued >> 1) & 1) ^ 1;
             const int y = x.u.row0 + c * C;
-            auto keys = [&](const CUtensorMap *map, uint32_t dst, unsigned long long &full,
-                            unsigned long long &empty) {
-                if (!wait_one(bar(empty), free, &s.dead)) return false;
-                arrive_expect(bar(full), boxes * kBox);
-                for (int b = 0; b < boxes; ++b)
-                    tma_load(dst + slot * kKeyTile + b * kBox, map, kx + 64 * b, y, bar(full));
-                return true;
-            };
+            // L2 first, some blocks before: the ring holds two, and memory takes longer than one.
+            for (int a = c == 0 ? 1 : kAhead; a <= kAhead && c + a < x.n; ++a) {
+                tma_prefetch(&L.v, vx, y + a * C);
+                for (int b = 0; b < boxes; ++b) tma_prefetch(&L.k, kx + 64 * b, y + a * C);
+            }
+            if (!wait_one(bar(s.b.k_empty[slot]), free, &s.dead)) return;
+            arrive_expect(bar(s.b.k_full[slot]), boxes * kBox);
+            for (int b = 0; b < boxes; ++b)
+                tma_load(t.k + slot * kKeyTile + b * kBox, &L.k, kx + 64 * b, y, bar(s.b.k_full[slot]));
             if (!wait_one(bar(s.b.v_empty[slot]), free, &s.dead)) return;
             arrive_expect(bar(s.b.v_full[slot]), kBox);
             tma_load(t.v + slot * kBox, &L.v, vx, y, bar(s.b.v_full[slot]));
-            if (!keys(&L.k, t.k, s.b.k_full[slot], s.b.k_empty[slot])) return;
-            if (OUT && !keys(&L.q, t.q, s.b.q_full[slot], s.b.q_empty[slot])) return;
         }
     }
 }
@@ -184,8 +213,8 @@ template <bool OUT>
 __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm) {
     const uint32_t lead = elect();
     const int steps = __shfl_sync(0xffffffffu, L.a.g.dk / 16, 0);
-    const uint32_t q_lo = desc_lo(t.q, 16), k_lo = desc_lo(t.k, 16);  // rows of 64 columns
-    const uint32_t kt_lo = desc_lo(t.k, kBox);                        // K^T, 128 of its rows
+    const uint32_t k_lo = desc_lo(t.k, 16);     // rows of 64 columns
+    const uint32_t kt_lo = desc_lo(t.k, kBox);  // K^T, 128 of its rows
     const uint32_t v_lo = desc_lo(t.v, kBox), w_lo = desc_lo(t.w, kBox), s_lo = desc_lo(t.s, kBox);
     tm = __shfl_sync(0xffffffffu, tm, 0);
     long long at = blockIdx.x;
@@ -196,11 +225,10 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         if (!wait(bar(s.b.q_full[slot]), full, &s.dead)) return false;
         if (!wait(bar(s.b.k_full[slot]), full, &s.dead)) return false;
         fence_after();
-        for (int kk = 0; kk < steps; ++kk) {
-            const uint32_t off = (slot * kKeyTile + (kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            mma_ss(lead, tm + kScores + slot * 128, q_lo + off, k_lo + off, idesc(C, false), kk > 0);
-        }
-        commit(lead, bar(s.b.s_full[slot]));
+        for (int kk = 0; kk < steps; ++kk)
+            mma_ts(lead, tm + kScores, tm + kQ + slot * 64 + kk * 8,
+                   k_lo + ((slot * kKeyTile + (kk >> 2) * kBox + (kk & 3) * 32) >> 4), idesc(C, false), kk > 0);
+        commit(lead, bar(s.b.s_full));
         return true;
     };
     while (next_unit(L, !OUT, at, x)) {
@@ -208,42 +236,43 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         if (OUT && !scores(it)) return;
         for (int c = 0; c < n; ++c, ++it) {
             const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            // U = K^T W
+            // U = K^T W, both terms side by side
             if (!wait(bar(s.b.k_full[slot]), half, &s.dead)) return;
-            if (!wait(bar(s.b.w_ready), it & 1, &s.dead)) return;
-            if (!wait(bar(s.b.u_free[slot]), half ^ 1, &s.dead)) return;
-            fence_after();
+            if (!wait(bar(s.b.u_free), (it & 1) ^ 1, &s.dead)) return;
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+            for (int b = 0; b < 4; ++b) {  // 32 rows at a time, as their warp has them ready
+                if (!wait(bar(s.b.w_ready[slot][b]), half, &s.dead)) return;
+                fence_after();
 #pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    mma_ss(lead, tm + kU + slot * NV, kt_lo + ((slot * kKeyTile + kk * 2048) >> 4),
-                           w_lo + ((p * kBox + kk * 2048) >> 4), idesc(NV, true, true), p + kk > 0);
-            commit(lead, bar(s.b.u_full[slot]));
-            commit(lead, bar(s.b.w_free));
+                for (int kk = 2 * b; kk < 2 * b + 2; ++kk)
+                    mma_ss(lead, tm + kU, kt_lo + ((slot * kKeyTile + kk * 2048) >> 4),
+                           w_lo + ((slot * kWTile + kk * 2048) >> 4), idesc(2 * NV, true, true), kk > 0);
+                commit(lead, bar(s.b.w_free[slot][b]));
+            }
+            commit(lead, bar(s.b.u_full));
             commit(lead, bar(s.b.k_empty[slot]));
             if (!OUT) {
                 commit(lead, bar(s.b.v_empty[slot]));
                 continue;
             }
-            if (c + 1 < n && !scores(it + 1)) return;
             // O2 = Q S
             if (!wait(bar(s.b.st_ready), it & 1, &s.dead)) return;
             if (!wait(bar(s.b.o_free), (it & 1) ^ 1, &s.dead)) return;
             fence_after();
             for (int kk = 0; kk < steps; ++kk)
-                mma_ss(lead, tm + kO2, q_lo + ((slot * kKeyTile + (kk >> 2) * kBox + (kk & 3) * 32) >> 4),
-                       s_lo + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
+                mma_ts(lead, tm + kO2, tm + kQ + slot * 64 + kk * 8, s_lo + ((kk * 2048) >> 4), idesc(NV, true),
+                       kk > 0);
             commit(lead, bar(s.b.st_free));
             // O1 = P V
-            if (!wait(bar(s.b.p_ready[slot]), half, &s.dead)) return;
+            if (!wait(bar(s.b.p_ready), it & 1, &s.dead)) return;
             fence_after();
 #pragma unroll
             for (int kk = 0; kk < C / 16; ++kk)
-                mma_ts(lead, tm + kO1, tm + kScores + slot * 128 + kk * 8,
-                       v_lo + ((slot * kBox + kk * 2048) >> 4), idesc(NV, true), kk > 0);
+                mma_ts(lead, tm + kO1, tm + kScores + kk * 8, v_lo + ((slot * kBox + kk * 2048) >> 4),
+                       idesc(NV, true), kk > 0);
             commit(lead, bar(s.b.o_full));
             commit(lead, bar(s.b.v_empty[slot]));
+            if (c + 1 < n && !scores(it + 1)) return;
         }
     }
 }
@@ -286,7 +315,6 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
             for (int m = 1; m < 4; ++m)
                 if (m > b) w *= s.t[slot][m];
             if (!wait(bar(s.b.v_full[slot]), half, &s.dead)) return;
-            if (!wait(bar(s.b.w_free), (it & 1) ^ 1, &s.dead)) return;
             const uint32_t vt = t.v + slot * kBox;
             const uint32_t zero[4] = {0, 0, 0, 0};
             if (n < C) {  // rows of other requests, whatever they hold, count as 0
@@ -300,31 +328,28 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
                 }
             }
             const float2 w2 = make_float2(w, w);
+            uint32_t v8[8][4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lds128(chunk(vt, j, e), v8[e]);
+            if (!wait(bar(s.b.w_free[slot][b]), half ^ 1, &s.dead)) return;
+            const uint32_t wt = t.w + slot * kWTile;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                uint32_t v[4], hi[4], mid[4], lo[4];
-                lds128(chunk(vt, j, e), v);
+                uint32_t *v = v8[e], hi[4], lo[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float2 y = mul2(make_float2(__uint_as_float(v[m] << 16),
                                                       __uint_as_float(v[m] & 0xFFFF0000u)), w2);
-                    // the leading 8 bits of each, the next 8 and the last 8: exact
-                    const uint32_t yx = __float_as_uint(y.x), yy = __float_as_uint(y.y);
-                    hi[m] = __byte_perm(yx, yy, 0x7632);
-                    const float2 y1 = add2(y, make_float2(-__uint_as_float(yx & 0xFFFF0000u),
-                                                          -__uint_as_float(yy & 0xFFFF0000u)));
-                    const uint32_t zx = __float_as_uint(y1.x), zy = __float_as_uint(y1.y);
-                    mid[m] = __byte_perm(zx, zy, 0x7632);
-                    const float2 y2 = add2(y1, make_float2(-__uint_as_float(zx & 0xFFFF0000u),
-                                                           -__uint_as_float(zy & 0xFFFF0000u)));
-                    lo[m] = pack_bf16(y2.x, y2.y);
+                    hi[m] = pack_bf16(y.x, y.y);
+                    const float2 z = add2(y, make_float2(-__uint_as_float(hi[m] << 16),
+                                                         -__uint_as_float(hi[m] & 0xFFFF0000u)));
+                    lo[m] = pack_bf16(z.x, z.y);
                 }
-                sts128(chunk(t.w, j, e), hi);
-                sts128(chunk(t.w + kBox, j, e), mid);
-                sts128(chunk(t.w + 2 * kBox, j, e), lo);
+                sts128(chunk(wt, j, e), hi);
+                sts128(chunk(wt + kBox, j, e), lo);
             }
             fence_async();
-            arrive_warp(bar(s.b.w_ready));
+            arrive_warp(bar(s.b.w_ready[slot][b]));
         }
     }
 }
@@ -334,6 +359,7 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
 __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t tm, int i) {
     const gdn_linear &g = L.a.g;
     const int lane = i & 31, b = i >> 5;
+    const uint32_t ts = tm + kScores + ((uint32_t)b << 21);  // this warp's lanes
     long long at = blockIdx.x;
     Unit x;
     uint32_t it = 0;
@@ -341,11 +367,10 @@ __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t t
         float gi = log_decay(g, x, 0, i);
         for (int c = 0; c < x.n; ++c, ++it) {
             const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            const uint32_t ts = tm + kScores + slot * 128 + ((uint32_t)b << 21);  // this warp's lanes
             const float lam = expf(gi);
             if (c + 1 < x.n) gi = log_decay(g, x, c + 1, i);
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            if (!wait(bar(s.b.s_full[slot]), half, &s.dead)) return;
+            if (!wait(bar(s.b.s_full), it & 1, &s.dead)) return;
             fence_after();
             const float rowf = s.rowf[slot][i];
             // Earlier 32s: all of their rows are seen.
@@ -395,7 +420,7 @@ __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t t
             arrive_warp(bar(s.b.dec_empty[slot]));
             wait_st();
             fence_before();
-            arrive_warp(bar(s.b.p_ready[slot]));
+            arrive_warp(bar(s.b.p_ready));
         }
     }
 }
@@ -439,23 +464,25 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
             const float keep = s.t[slot][0] * s.t[slot][1] * (s.t[slot][2] * s.t[slot][3]);
             arrive_warp(bar(s.b.dec_empty[slot]));
-            if (!wait(bar(s.b.u_full[slot]), half, &s.dead)) return;
+            if (!wait(bar(s.b.u_full), it & 1, &s.dead)) return;
             fence_after();
 #pragma unroll
             for (int e = 0; e < NV; e += 16) {
-                uint32_t y[16];
-                tmem_ld16(tu + slot * NV + e, y);
+                uint32_t y[16], z[16];
+                tmem_ld16(tu + e, y);
+                tmem_ld16(tu + NV + e, z);
                 wait_ld();
 #pragma unroll
                 for (int m = 0; m < 16; m += 2) {
-                    const float2 z = fma2(make_float2(S[e + m], S[e + m + 1]), make_float2(keep, keep),
-                                          make_float2(__uint_as_float(y[m]), __uint_as_float(y[m + 1])));
-                    S[e + m] = z.x;
-                    S[e + m + 1] = z.y;
+                    const float2 u = add2(make_float2(__uint_as_float(y[m]), __uint_as_float(y[m + 1])),
+                                          make_float2(__uint_as_float(z[m]), __uint_as_float(z[m + 1])));
+                    const float2 w = fma2(make_float2(S[e + m], S[e + m + 1]), make_float2(keep, keep), u);
+                    S[e + m] = w.x;
+                    S[e + m + 1] = w.y;
                 }
             }
             fence_before();
-            arrive_warp(bar(s.b.u_free[slot]));
+            arrive_warp(bar(s.b.u_free));
         }
         if (STATE && d < g.dk) {
 #pragma unroll
@@ -465,72 +492,81 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
     }
 }
 
-// ---------------------------------------------------------------- the output's warpgroup
+// ---------------------------------------------------------------- the queries' and output's warpgroup
 
-__device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm, int i) {
+__device__ __forceinline__ void output_role(const Launch &L, Shared &s, uint32_t tm, int i) {
     const gdn_linear &g = L.a.g;
-    const int lane = i & 31, b = i >> 5;
+    const int b = i >> 5;
     const uint32_t lanes = (uint32_t)b << 21;
     long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0, stored = 0;
+    uint32_t it = 0;
     while (next_unit(L, false, at, x)) {
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + (long long)(x.h / L.a.group) * g.dk;
+        // Row i of block c to tensor memory, where block `to`'s are (its scores and O2 have been computed).
+        auto queries = [&](int c, uint32_t to) {
+            const int row = c * C + i;
+            const bool has = row < x.u.T;
+            const __nv_bfloat16 *src = q + (x.u.row0 + (long long)row) * g.q_stride;
+            uint32_t y[64];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) y[e] = 0u;
+            if (has) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
+                if (g.dk == 128) {
+#pragma unroll
+                    for (int e = 4; e < 8; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
+                }
+            }
+            const uint32_t tq = tm + kQ + (to & 1) * 64 + lanes;
+            tmem_st32(tq, y);
+            tmem_st32(tq + 32, y + 32);
+            wait_st();
+            fence_before();
+            arrive_warp(bar(s.b.q_full[to & 1]));
+        };
+        queries(0, it);
         for (int c = 0; c < x.n; ++c, ++it) {
             const uint32_t slot = it & 1, half = (it >> 1) & 1;
             const int n = min(C, x.u.T - c * C);
+            if (c + kAhead < x.n) {  // whole rows to come: into L2
+                const long long row = x.u.row0 + (long long)(c + kAhead) * C + i;
+                if ((c + kAhead) * C + i < x.u.T)
+                    for (int e = 0; e < g.dk; e += 64)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + row * g.q_stride + e));
+            }
+            if (c + 1 < x.n) queries(c + 1, it + 1);
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
             float f = s.rowf[slot][i] * g.scale;
             for (int m = 0; m < b; ++m) f *= s.t[slot][m];
             arrive_warp(bar(s.b.dec_empty[slot]));
             if (!wait(bar(s.b.o_full), it & 1, &s.dead)) return;
             fence_after();
-            // The block's queries have been read: its output goes through their place.
-            const uint32_t stage = t.q + slot * kKeyTile;
             const float2 f2 = make_float2(f, f), scale2 = make_float2(g.scale, g.scale);
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) +
+                               (x.u.row0 + (long long)c * C + i) * g.heads * g.dv + x.h * g.dv + x.c0;
 #pragma unroll
             for (int h = 0; h < NV; h += 32) {
                 uint32_t y[32], z[32];
                 tmem_ld32(tm + kO1 + lanes + h, y);
                 tmem_ld32(tm + kO2 + lanes + h, z);
                 wait_ld();
+                if (h + 32 == NV) {
+                    fence_before();
+                    arrive_warp(bar(s.b.o_free));
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float2 p = fma2(make_float2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), f2,
                                           mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale2));
                     y[e / 2] = pack_bf16(p.x, p.y);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sts128(chunk(stage, i, h / 8 + e), y + 4 * e);
-            }
-            fence_before();
-            arrive_warp(bar(s.b.o_free));
-            const int row = x.u.row0 + c * C, col = x.h * g.dv + x.c0;
-            if (n == C) {
-                fence_async();
-                arrive_warp(bar(s.b.o_sync));
-                if (b == 0) {
-                    if (!wait(bar(s.b.o_sync), stored & 1, &s.dead)) return;
-                    if (lane == 0) {
-                        tma_store(&L.o, col, row, stage);
-                        asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;\n" ::: "memory");
-                    }
+                if (i < n) {  // whole sectors: 32 bytes of a row at a time
+                    stg32(o + h, L.o32, y);
+                    stg32(o + h + 16, L.o32, y + 8);
                 }
-                ++stored;
-            } else {
-                __syncwarp();
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) + col + (lane & 7) * 8;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = 32 * b + 4 * e + (lane >> 3);
-                    uint32_t y[4];
-                    lds128(chunk(stage, r, lane & 7), y);
-                    if (r < n)
-                        *reinterpret_cast<uint4 *>(o + (long long)(row + r) * g.heads * g.dv) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
-                }
-                fence_async();  // before the copy that follows into the same place
             }
-            arrive_warp(bar(s.b.q_empty[slot]));
         }
     }
 }
@@ -547,27 +583,29 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(s.b.q_full[i]), 1);
+            mbar_init(bar(s.b.q_full[i]), 4);
             mbar_init(bar(s.b.k_full[i]), 1);
             mbar_init(bar(s.b.v_full[i]), 1);
-            mbar_init(bar(s.b.q_empty[i]), 4);
             mbar_init(bar(s.b.k_empty[i]), 1);
             mbar_init(bar(s.b.v_empty[i]), 1);
             mbar_init(bar(s.b.dec_full[i]), 4);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 12 : 4);
-            mbar_init(bar(s.b.s_full[i]), 1);
-            mbar_init(bar(s.b.p_ready[i]), 4);
-            mbar_init(bar(s.b.u_full[i]), 1);
-            mbar_init(bar(s.b.u_free[i]), 4);
         }
-        mbar_init(bar(s.b.w_ready), 4);
-        mbar_init(bar(s.b.w_free), 1);
+        for (int i = 0; i < 4; ++i) {
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(bar(s.b.w_ready[k][i]), 1);
+                mbar_init(bar(s.b.w_free[k][i]), 1);
+            }
+        }
+        mbar_init(bar(s.b.s_full), 1);
+        mbar_init(bar(s.b.p_ready), 4);
+        mbar_init(bar(s.b.u_full), 1);
+        mbar_init(bar(s.b.u_free), 4);
         mbar_init(bar(s.b.st_ready), 4);
         mbar_init(bar(s.b.st_free), 1);
         mbar_init(bar(s.b.o_full), 1);
         mbar_init(bar(s.b.o_free), 4);
         mbar_init(bar(s.b.w_sync), 4);
-        mbar_init(bar(s.b.o_sync), 4);
         mbar_init(bar(s.b.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s.dead = 0;
@@ -591,19 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     } else if (warp < 12) {
         state_role<OUT, STATE>(L, s, t, tm, tid - 256);
     } else if (warp < 16) {
-        if (OUT) {
-            output_role(L, s, t, tm, tid - 384);
-            if (tid == 384) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
-        }
+        if (OUT) output_role(L, s, tm, tid - 384);
     } else if (warp == 16) {
         if ((tid & 31) == 0) {
             uint32_t issued = 0;
-            load_role<OUT>(L, s, t, issued);
+            load_role(L, s, t, !OUT, issued);
             // Every copy has landed before the block ends (its roles waited for them unless one gave up).
             for (uint32_t p = issued > 2 ? issued - 2 : 0; s.dead && p <= issued; ++p) {
                 wait_parity(bar(s.b.v_full[p & 1]), (p >> 1) & 1);
                 wait_parity(bar(s.b.k_full[p & 1]), (p >> 1) & 1);
-                if (OUT) wait_parity(bar(s.b.q_full[p & 1]), (p >> 1) & 1);
             }
         }
     } else {
@@ -642,15 +676,12 @@ cudaError_t launch_tc(const LinearArgs &a, cudaStream_t stream) {
     Launch L;
     L.a = a;
     L.slices = g.dv / NV;
+    L.q32 = (reinterpret_cast<uintptr_t>(g.q) & 31) == 0 && g.q_stride % 16 == 0;
+    L.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
     L.units = (long long)g.batch * g.heads * L.slices;
     const long long krow = (long long)g.k_heads * g.dk, vrow = (long long)g.heads * g.dv;
     if (!encoder() || !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
         !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride))
-        return cudaErrorInvalidValue;
-    L.q = L.k;  // not used by a commit
-    L.o = L.v;
-    if (MODE != kCommit && (!encode_rows(&L.q, g.q, krow, g.n_tok, g.q_stride) ||
-                            !encode_rows(&L.o, a.o, vrow, g.n_tok, vrow)))
         return cudaErrorInvalidValue;
     constexpr int smem = kTiles + (int)sizeof(Shared);
     const cudaError_t e = allow_smem<linear_tc_kernel<MODE>>(smem);

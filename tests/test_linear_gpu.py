@@ -206,6 +206,24 @@ def test_grouped_heads_and_stride_of_the_decays():
 
 
 @pytest.mark.parametrize("T", [1, 12, 100])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_aligned_to_16_bytes_only(T, dtype):
+    c = Case(new=[T, T + 1], heads=2, seed=14, dtype=dtype)
+    step = 16 // (2 if dtype == "bf16" else 4)
+
+    def moved(x):  # a row 16 bytes longer than its heads, from 16 bytes behind an allocation's start
+        n, h, d = x.shape
+        flat = torch.full((n * (h * d + step) + step,), float("nan"), dtype=x.dtype, device="cuda")
+        y = flat[step:].view(n, h * d + step)[:, :h * d].view(n, h, d)
+        y.copy_(x)
+        return y
+
+    o = torch.full((c.rows * 2 * 128 + step,), 7.0, dtype=TYPES[dtype], device="cuda")[step:].view(c.rows, 2, 128)
+    binding.gdn_linear_step(c.make(q=moved(c.dq), k=moved(c.dk_), v=moved(c.dv_)), o)
+    c.check(o, c.new)
+
+
+@pytest.mark.parametrize("T", [1, 12, 100])
 def test_bad_requests_are_skipped(T):
     c = Case(new=[T] * 5, seed=8)
     bad = c.dcu.clone()
