@@ -19,7 +19,7 @@ LIB = os.path.join(LIB_DIR, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_recurrent.cu", "gdn_chunk.cu", "gdn_accept.cu", "gdn_selftest.cu",
            "gdn_rope.cu", "gdn_attn.cu", "gdn_attn_rows.cu",
            "gdn_attn_tc.cu", "gdn_sample.cu", "gdn_pages.cu", "gdn_linear.cu",
-           "gdn_linear_tc.cu"]
+           "gdn_linear_tc.cu", "gdn_linear_drafts.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -41,6 +41,8 @@ cudaError_t launch_linear(const LinearArgs &a, int mode, cudaStream_t stream);
 constexpr int kLinearTcRows = 48;  // rows a request from which the tensor-core kernel runs
 bool linear_tc_runs(const gdn_linear &g);
 cudaError_t launch_linear_tc(const LinearArgs &a, int mode, cudaStream_t stream);
+bool linear_drafts_runs(const gdn_linear &g);  // a verify
+cudaError_t launch_linear_drafts(const LinearArgs &a, cudaStream_t stream);
 
 // One block that waits on a barrier nothing completes, until the bounded wait
 // gives up; ORs GDN_DEVERR_TIMEOUT into *dev_err (not NULL).

@@ -314,6 +314,7 @@ cudaError_t launch_type(const LinearArgs &a, int mode, cudaStream_t stream) {
 
 cudaError_t launch_linear(const LinearArgs &a, int mode, cudaStream_t stream) {
     if (linear_tc_runs(a.g)) return launch_linear_tc(a, mode, stream);
+    if (mode == kVerify && linear_drafts_runs(a.g)) return launch_linear_drafts(a, stream);
     return a.g.dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(a, mode, stream)
                                  : launch_type<float>(a, mode, stream);
 }
