@@ -23,24 +23,15 @@ struct LinearUnit {
     float *tile;               // the state, dk x dv
 };
 
-// Every thread of the block finds the same answer; thread 0 reports.  False: skip the unit.
-__device__ __forceinline__ bool linear_unit(const LinearArgs &a, int r, int h, bool commit, LinearUnit &u) {
+// A unit from its request's words, for calls without accepted lengths.  Every thread of the block
+// finds the same answer; thread 0 reports.  False: skip the unit.
+__device__ __forceinline__ bool linear_words(const LinearArgs &a, long long c0, long long c1, int slot, int h,
+                                             LinearUnit &u) {
     const gdn_linear &g = a.g;
-    long long c0 = (long long)r * g.max_T, c1 = c0 + g.max_T;
-    if (g.cu_seqlens) {
-        c0 = g.cu_seqlens[r];
-        c1 = g.cu_seqlens[r + 1];
-    }
-    const int slot = g.slot_ids[r];
     int err = 0;
-    long long T = c1 - c0;
+    const long long T = c1 - c0;
     if (T < 0 || T > g.max_T || c0 < 0 || c1 > g.n_tok) err |= GDN_DEVERR_SEQLEN;
     if (slot < 0 || slot >= g.pool_slots) err |= GDN_DEVERR_SLOT;
-    if (commit) {
-        const int acc = a.accepted[r];
-        if (!err && (acc < 0 || acc > T)) err |= GDN_DEVERR_ACCEPTED;
-        T = acc;
-    }
     if (err) {
         if (threadIdx.x == 0 && g.dev_err) atomicOr(g.dev_err, err);
         return false;
@@ -49,6 +40,35 @@ __device__ __forceinline__ bool linear_unit(const LinearArgs &a, int r, int h, b
     u.T = (int)T;
     u.tile = g.pool + ((long long)slot * g.heads + h) * ((long long)g.dk * g.dv);
     return T > 0;
+}
+
+// Every thread of the block calls it, as above; commit: T is the accepted length.
+__device__ __forceinline__ bool linear_unit(const LinearArgs &a, int r, int h, bool commit, LinearUnit &u) {
+    const gdn_linear &g = a.g;
+    long long c0 = (long long)r * g.max_T, c1 = c0 + g.max_T;
+    if (g.cu_seqlens) {
+        c0 = g.cu_seqlens[r];
+        c1 = g.cu_seqlens[r + 1];
+    }
+    const int slot = g.slot_ids[r];
+    const int acc = commit ? a.accepted[r] : 0;
+    LinearUnit x;
+    x.T = 0;
+    const bool rows = linear_words(a, c0, c1, slot, h, x);
+    if (!commit) {
+        if (rows) u = x;
+        return rows;
+    }
+    if (acc < 0 || acc > (rows ? x.T : 0)) {
+        // (of a request that is skipped already, nothing more is reported)
+        const bool good = rows || (c1 == c0 && c0 >= 0 && c1 <= g.n_tok && slot >= 0 && slot < g.pool_slots);
+        if (good && threadIdx.x == 0 && g.dev_err) atomicOr(g.dev_err, GDN_DEVERR_ACCEPTED);
+        return false;
+    }
+    if (!rows) return false;
+    u = x;
+    u.T = acc;
+    return acc > 0;
 }
 
 }  // namespace gdn
