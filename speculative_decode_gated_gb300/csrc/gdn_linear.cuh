@@ -23,17 +23,17 @@ struct LinearUnit {
     float *tile;               // the state, dk x dv
 };
 
-// A unit from its request's words, for calls without accepted lengths.  Every thread of the block
-// finds the same answer; thread 0 reports.  False: skip the unit.
+// A unit from its request's words, for calls without accepted lengths; report: this thread reports what
+// is wrong with it.  False: skip the unit.
 __device__ __forceinline__ bool linear_words(const LinearArgs &a, long long c0, long long c1, int slot, int h,
-                                             LinearUnit &u) {
+                                             LinearUnit &u, bool report) {
     const gdn_linear &g = a.g;
     int err = 0;
     const long long T = c1 - c0;
     if (T < 0 || T > g.max_T || c0 < 0 || c1 > g.n_tok) err |= GDN_DEVERR_SEQLEN;
     if (slot < 0 || slot >= g.pool_slots) err |= GDN_DEVERR_SLOT;
     if (err) {
-        if (threadIdx.x == 0 && g.dev_err) atomicOr(g.dev_err, err);
+        if (report && g.dev_err) atomicOr(g.dev_err, err);
         return false;
     }
     u.row0 = (int)c0;
@@ -42,7 +42,7 @@ __device__ __forceinline__ bool linear_words(const LinearArgs &a, long long c0, 
     return T > 0;
 }
 
-// Every thread of the block calls it, as above; commit: T is the accepted length.
+// Every thread of the block calls it and finds the same answer; thread 0 reports.  commit: T is the accepted length.
 __device__ __forceinline__ bool linear_unit(const LinearArgs &a, int r, int h, bool commit, LinearUnit &u) {
     const gdn_linear &g = a.g;
     long long c0 = (long long)r * g.max_T, c1 = c0 + g.max_T;
@@ -54,7 +54,7 @@ __device__ __forceinline__ bool linear_unit(const LinearArgs &a, int r, int h, b
     const int acc = commit ? a.accepted[r] : 0;
     LinearUnit x;
     x.T = 0;
-    const bool rows = linear_words(a, c0, c1, slot, h, x);
+    const bool rows = linear_words(a, c0, c1, slot, h, x, threadIdx.x == 0);
     if (!commit) {
         if (rows) u = x;
         return rows;

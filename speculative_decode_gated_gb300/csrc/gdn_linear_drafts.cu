@@ -3,14 +3,13 @@
 //
 // The state before the drafts stays as it is, so all of a request's rows read the same one:
 //     o_i = scale (d(i, -1) S^T q_i + sum_{j <= i} d(i, j) (q_i . k_j) v_j)
-// Bound by the states' bytes (64 KB a head of 128 x 128).  A block holds dk x 64 of a state in
-// registers as B operands: thread (g, c) of a warp holds rows 2c, 2c + 1,
-// 2c + 8, 2c + 9 of a step's 16 and four columns from 4g, of which each belongs to another product
-// of 8 columns.  An element is the sum of two bf16 terms, 2^-17 of itself off, and products are
-// added up in float32; q and k are bf16 already.  A product has 16 rows of a draft, so few rows cost
-// as much as 16.  All that takes as long as the loads, one block at a time, so a block goes on to
-// further units: one thread asks the TMA engine for the next one's state and rows (128-byte swizzle)
-// as soon as its own state is in registers.  Three blocks an SM, 42 KB of loads each in flight.
+// Bound by the states' bytes (64 KB a head of 128 x 128).  A block goes through units (request,
+// head, 64 value columns): a warp of its own finds them, asks the TMA engine for their state and rows
+// (128-byte swizzle, two units' worth of shared memory) and works out their decays; eight warps each
+// take 8 columns of a unit from there to o, so none waits for another.  A product has 16 rows of a
+// draft, so few rows cost as much as 16.  The state enters as two bf16 terms, off by 2^-17 of itself,
+// and so do the weights d(i, j) (q_i . k_j), which are operands of the values' product just where their
+// own product left them; q, k and v are bf16 already, and sums are float32.
 #include <cstdint>
 
 #include "gdn_launch.h"
@@ -20,9 +19,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = 4;  // that share a state's rows; two of each, by columns
-constexpr int CV = 64;  // value columns of a block
+constexpr int kWarps = 8;  // that compute, 8 columns each; and one that loads
+constexpr int CV = 8 * kWarps;
 
 __device__ __forceinline__ uint32_t pack(float x, float y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -39,20 +37,28 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A unit: its rows (T < 0: no more units), head, first value column, and its state's first row in the pool.
+struct Work {
+    int T, row0, h, c0, row;
+};
+
 // NG groups of 16 rows.
 template <int DK, int NG>
 struct Tiles {
     static constexpr int T = 16 * NG;
-    static constexpr int BUFFERS = NG == 1 ? 2 : 1;  // of rows
-    struct Rows {
+    static constexpr int BUFFERS = 2;
+    struct Unit {
+        float state[2][DK][32];
         __nv_bfloat16 q[DK / 64][T][64], k[DK / 64][T][64], v[T][64];
-    };
-    float state[2][DK][32];
-    Rows rows[BUFFERS];
-    float red[kWarps][16][CV];  // (16 bytes c of a row lie at c ^ (row & 1): different banks)
-    float d[T][T + 2];  // d[i][j + 1] = d(i, j)
+    } unit[BUFFERS];
+    struct Decays {
+        alignas(8) float d[T][T + 2];  // d(i, j)
+        float from[T];                 // d(i, -1)
+    } decays[BUFFERS];
     float g[T];
-    unsigned long long full;  // barrier: a unit's state and rows are there
+    Work work[BUFFERS];
+    int dead;  // a wait gave up
+    unsigned long long full[BUFFERS], free[BUFFERS];
 };
 
 struct Launch {
@@ -69,33 +75,28 @@ __device__ __forceinline__ void tma(void *to, const CUtensorMap *map, int x, int
         : "memory");
 }
 
+__device__ __forceinline__ void ldmatrix4(uint32_t *x, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix2_trans(uint32_t *x, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];\n"
+                 : "=r"(x[0]), "=r"(x[1])
+                 : "r"(at)
+                 : "memory");
+}
+// 16 bytes c of row r of a tile whose rows have 128.
+__device__ __forceinline__ uint32_t chunk(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// The warp that finds the units and loads them.
 template <int DK, int NG>
-__global__ void __launch_bounds__(kThreads, 3) drafts_kernel(const __grid_constant__ Launch L) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int KS = DK / 64;  // steps of 16 rows of the state a warp
-    extern __shared__ __align__(1024) unsigned char raw[];
-    Tiles<DK, NG> &s = *reinterpret_cast<Tiles<DK, NG> *>(raw);
+__device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int lane) {
     const LinearArgs &a = L.a;
     const gdn_linear &g = a.g;
-    const unsigned units = L.units;
-    const int tid = threadIdx.x, lane = tid & 31, gr = lane >> 2, c = lane & 3;
-    const int warp = (tid >> 5) % kWarps, side = (tid >> 5) / kWarps;  // rows, and 32 columns
     const unsigned slices = g.dv / CV;
-    const int kb = warp * (DK / kWarps);
-    if (tid == 0) {
-        mbar_init(bar(s.full), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __syncthreads();
-
-    // A unit: rows (none: skip it), head, first value column, this thread's logarithm.
-    struct Work {
-        LinearUnit u;
-        int h, c0;
-        int row;  // the state's first row in the pool
-        float g;
-    };
+    constexpr int NB = Tiles<DK, NG>::BUFFERS;
     // Units in order, `step` at a time; a unit's words are loaded a round before they are looked at.
     struct Place {
         unsigned r, h, s;
@@ -122,37 +123,17 @@ __global__ void __launch_bounds__(kThreads, 3) drafts_kernel(const __grid_consta
         return x;
     };
     auto work_of = [&](const Words &x) {
-        Work w;
-        w.u.T = w.u.row0 = 0;
-        w.row = (x.slot * g.heads + (int)x.p.h) * DK;  // below 2^31: checked on the host
-        w.h = x.p.h;
-        w.c0 = x.p.s * CV;
-        w.g = 0.f;
-        if (x.p.r >= (unsigned)g.batch) return w;
-        if (linear_words(a, x.c0, x.c1, x.slot, w.h, w.u) && tid < w.u.T)
-            w.g = ld_early(g.log_decay + (long long)(w.u.row0 + tid) * g.decay_stride + w.h);
+        Work w = {0, 0, (int)x.p.h, (int)x.p.s * CV, 0};
+        LinearUnit u;
+        if (x.p.r < (unsigned)g.batch && linear_words(a, x.c0, x.c1, x.slot, w.h, u, lane == 0)) {
+            w.T = u.T;
+            w.row0 = u.row0;
+            w.row = (x.slot * g.heads + w.h) * DK;  // below 2^31: checked on the host
+        }
         return w;
     };
-    // One thread's: the state and the rows of a unit.
     constexpr uint32_t kStateBytes = DK * CV * 4, kRowBytes = Tiles<DK, NG>::T * (2 * DK + CV) * 2;
-    auto copy_state = [&](const Work &w) {
-        for (int x = 0; x < 2; ++x) tma(s.state[x], &L.pool, w.c0 + 32 * x, w.row, bar(s.full));
-    };
-    auto copy_rows = [&](const Work &w, typename Tiles<DK, NG>::Rows &to) {
-        const int col = w.h / a.group * DK;
-        for (int x = 0; x < DK / 64; ++x) {
-            tma(to.q[x], &L.q, col + 64 * x, w.u.row0, bar(s.full));
-            tma(to.k[x], &L.k, col + 64 * x, w.u.row0, bar(s.full));
-        }
-        tma(to.v, &L.v, w.h * g.dv + w.c0, w.u.row0, bar(s.full));
-    };
-    // Bytes of a row of 64 columns of bf16: 16 bytes c lie at c ^ (row & 7).
-    auto word = [](const __nv_bfloat16 (*tile)[64], int row, int col) {
-        return *reinterpret_cast<const uint32_t *>(&tile[row][(col & 7) + 8 * ((col >> 3) ^ (row & 7))]);
-    };
-
-    constexpr bool AHEAD = Tiles<DK, NG>::BUFFERS == 2;
-    const unsigned step = gridDim.x;  // (units and three steps fit 2^31)
+    const unsigned step = gridDim.x;  // (units and two steps fit 2^31)
     const Place by = place_of(step);
     auto advance = [&](Place &p) {
         p.s += by.s;
@@ -168,185 +149,186 @@ __global__ void __launch_bounds__(kThreads, 3) drafts_kernel(const __grid_consta
         }
     };
     Place ahead = place_of(blockIdx.x);
-    const Words first = words_of(ahead);
-    advance(ahead);
-    const Words second = words_of(ahead);
-    Work w = work_of(first), next = work_of(second);
-    int buffer = 0;
-    uint32_t round = 0;
-    auto ask = [&](const Work &x) {
-        if (x.u.T > 0) arrive_expect(bar(s.full), kStateBytes + kRowBytes);
-    };
-    if (tid == 0 && w.u.T > 0) {
-        ask(w);
-        copy_state(w);
-        copy_rows(w, s.rows[0]);
-    }
-    for (unsigned at = blockIdx.x; at < units; at += step) {
-        const int T = w.u.T;
-        typename Tiles<DK, NG>::Rows &rows_ = s.rows[buffer];
+    Words coming = words_of(ahead);
+    Ring<NB> ring;
+    for (unsigned at = blockIdx.x; at < L.units; at += step) {
+        const Work w = work_of(coming);
         advance(ahead);
-        const Words coming = words_of(ahead);
-        if (tid < T) s.g[tid] = w.g;
-        if (T > 0) {
-            const bool there = wait_parity(bar(s.full), round++ & 1);
-            if (!__syncthreads_and(there)) {  // the copies never came: nothing more can be right
-                if (tid == 0 && g.dev_err) atomicOr(g.dev_err, GDN_DEVERR_TIMEOUT);
-                return;
+        coming = words_of(ahead);
+        if (w.T <= 0) continue;
+        constexpr int T = Tiles<DK, NG>::T;
+        float log[(T + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (T + 31) / 32; ++i)
+            log[i] = 32 * i + lane < w.T ? ld_early(g.log_decay + (long long)(w.row0 + 32 * i + lane) * g.decay_stride + w.h)
+                                         : 0.f;
+        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) break;
+        const uint32_t full = bar(s.full[ring.slot]);
+        auto &to = s.unit[ring.slot];
+        if (lane == 0) {
+            arrive_expect(full, kStateBytes + kRowBytes);
+            const int col = w.h / a.group * DK;
+            for (int x = 0; x < DK / 64; ++x) {
+                tma(to.q[x], &L.q, col + 64 * x, w.row0, full);
+                tma(to.k[x], &L.k, col + 64 * x, w.row0, full);
             }
-        }
-        // The state as operands: rows 2c, 2c + 1 (and 8 further), four columns from 4 gr.
-        uint32_t hi[KS][4][2], lo[KS][4][2];
-        if (T > 0) {
-#pragma unroll
-            for (int st = 0; st < KS; ++st)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const int row = kb + 16 * st + 8 * p + 2 * c;  // 16 bytes gr of it, and of the next
-                    const float4 y = *reinterpret_cast<const float4 *>(&s.state[side][row][4 * (gr ^ (2 * c))]);
-                    const float4 z =
-                        *reinterpret_cast<const float4 *>(&s.state[side][row + 1][4 * (gr ^ (2 * c + 1))]);
-                    const float y4[4] = {y.x, y.y, y.z, y.w}, z4[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t b = pack(y4[t], z4[t]);
-                        hi[st][t][p] = b;
-                        lo[st][t][p] = pack(y4[t] - low(b), z4[t] - high(b));
-                    }
-                }
-        }
-        __syncthreads();
-        if (tid == 0 && next.u.T > 0) {
-            ask(next);
-            copy_state(next);
-            if (AHEAD) copy_rows(next, s.rows[buffer ^ 1]);
+            tma(to.v, &L.v, w.h * g.dv + w.c0, w.row0, full);
+            for (int x = 0; x < 2; ++x) tma(to.state[x], &L.pool, w.c0 + 32 * x, w.row, full);
         }
         __syncwarp();
-        // Row i's decays: sums from its end on, a lane a column (two where there are more rows).
-        for (int i = tid >> 5; i < T; i += kThreads / 32) {
 #pragma unroll
-            for (int y = 0; y < (NG > 1 ? 2 : 1); ++y) {
-                float sum = 0.f;  // of the logarithms of rows j + 1 to i
-                const int j = 32 * y + lane - 1;
-                if (NG == 1) {
-                    sum = lane <= i ? s.g[lane] : 0.f;
+        for (int i = 0; i < (T + 31) / 32; ++i)
+            if (32 * i + lane < T) s.g[32 * i + lane] = log[i];
+        __syncwarp();
+        // Row i's decays: sums from its end on.  Up to 16 rows: a lane a row (l), two sums at a time.
+        auto &to_d = s.decays[ring.slot];
+        if (NG == 1) {
+            const int l = lane & 15;
+#pragma unroll 2
+            for (int i = lane >> 4; i < 16; i += 2) {
+                float sum = l <= i ? s.g[l] : 0.f;
 #pragma unroll
-                    for (int d = 1; d < 16; d <<= 1) {
-                        const float z = __shfl_down_sync(0xffffffffu, sum, d);
-                        if (lane + d <= i) sum += z;
-                    }
-                } else if (j < i) {
-                    for (int l = j + 1; l <= i; ++l) sum += s.g[l];
+                for (int d = 1; d < 16; d <<= 1) {
+                    const float z = __shfl_down_sync(0xffffffffu, sum, d, 16);
+                    if (l + d <= i) sum += z;
                 }
-                if (j <= i) s.d[i][j + 1] = j == i ? 1.f : expf(sum);
+                const float d = expf(sum);  // of rows l to i: d(i, l - 1)
+                if (l == 0) {
+                    to_d.from[i] = d;
+                    to_d.d[i][i] = 1.f;
+                } else if (l <= i) {
+                    to_d.d[i][l - 1] = d;
+                }
+            }
+        } else {
+            for (int l = lane; l < w.T; l += 32) {  // down column l - 1
+                float sum = 0.f;
+                to_d.d[l][l] = 1.f;
+                for (int i = l; i < w.T; ++i) {
+                    sum += s.g[i];
+                    const float d = expf(sum);
+                    if (l == 0)
+                        to_d.from[i] = d;
+                    else
+                        to_d.d[i][l - 1] = d;
+                }
             }
         }
+        if (lane == 0) s.work[ring.slot] = w;
+        __syncwarp();
+        if (lane == 0) arrive(full);
+        ring.next();
+    }
+    if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) return;
+    if (lane == 0) {
+        s.work[ring.slot].T = -1;
+        arrive(bar(s.full[ring.slot]));
+        arrive(bar(s.full[ring.slot]));
+    }
+}
 
-        __syncthreads();
+template <int DK, int NG>
+__global__ void __launch_bounds__(32 * (kWarps + 1), 2) drafts_kernel(const __grid_constant__ Launch L) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(1024) unsigned char raw[];
+    constexpr int NB = Tiles<DK, NG>::BUFFERS;
+    Tiles<DK, NG> &s = *reinterpret_cast<Tiles<DK, NG> *>(raw);
+    const gdn_linear &g = L.a.g;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
+    if (tid == 0) {
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(bar(s.full[i]), 2);  // the copies, and the decays
+            mbar_init(bar(s.free[i]), kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        s.dead = 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    if (warp == kWarps) {
+        load_role<DK, NG>(L, s, lane);
+        return;
+    }
+
+    const int l7 = lane & 7, l8 = (lane >> 3) & 1, l16 = lane >> 4;
+    Ring<NB> ring;
+    for (;;) {
+        if (!wait(bar(s.full[ring.slot]), ring.parity, &s.dead)) {  // the copies never came
+            if (lane == 0 && g.dev_err) atomicOr(g.dev_err, GDN_DEVERR_TIMEOUT);
+            return;
+        }
+        const Work w = s.work[ring.slot];
+        const int T = w.T;
+        if (T < 0) return;
+        const auto &in = s.unit[ring.slot];
+        const auto &dec = s.decays[ring.slot];
+        const uint32_t qt = smem_addr(in.q), kt = smem_addr(in.k), vt = smem_addr(in.v);
+        // This lane's column of this warp's 8, in rows 16 st + 2c and so on of the state.
+        const float *col = &in.state[warp >> 2][0][0] + (gr & 3);
+        const int cc = 2 * (warp & 3) + (gr >> 2);
+        auto element = [&](int row) { return col[row * 32 + 4 * (cc ^ (row & 7))]; };
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) + ((long long)w.row0 * g.heads + w.h) * g.dv + w.c0 +
+                           8 * warp + 2 * c;
+
 #pragma unroll 1
         for (int m = 0; 16 * m < T; ++m) {
-            uint32_t A[KS][4];
-            float acc[4][4] = {};
+            uint32_t A[DK / 16][4];
+            float acc[2][4] = {};
 #pragma unroll
-            for (int st = 0; st < KS; ++st)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                        A[st][x] = word(rows_.q[(kb + 16 * st) / 64], 16 * m + gr + 8 * (x & 1),
-                                    (kb + 16 * st) % 64 + 8 * (x >> 1) + 2 * c);
-#pragma unroll
-            for (int st = 0; st < KS; ++st)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) mma(acc[t], A[st], lo[st][t][0], lo[st][t][1]);
-#pragma unroll
-            for (int st = 0; st < KS; ++st)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) mma(acc[t], A[st], hi[st][t][0], hi[st][t][1]);
-            // Rows gr and gr + 8 of the group.
-            const int i0 = 16 * m + gr, i1 = i0 + 8;
-            const float from0 = i0 < T ? s.d[i0][0] : 0.f, from1 = i1 < T ? s.d[i1][0] : 0.f;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                acc[t][0] *= from0;
-                acc[t][1] *= from0;
-                acc[t][2] *= from1;
-                acc[t][3] *= from1;
+            for (int st = 0; st < DK / 16; ++st) {
+                ldmatrix4(A[st], chunk(qt + (st >> 2) * Tiles<DK, NG>::T * 128, 16 * m + l7 + 8 * l8,
+                                       2 * (st & 3) + l16));
+                const int row = 16 * st + 2 * c;
+                const float x0 = element(row), x1 = element(row + 1), y0 = element(row + 8), y1 = element(row + 9);
+                const uint32_t b0 = pack(x0, x1), b1 = pack(y0, y1);
+                mma(acc[0], A[st], pack(x0 - low(b0), x1 - high(b0)), pack(y0 - low(b1), y1 - high(b1)));
+                mma(acc[1], A[st], b0, b1);
             }
-            // The rows' own products, this warp's share of dk: with their decays they are the weights of
-            // the values, as operands of the next product just where they are.
+            // Rows gr and gr + 8 of the group.  (Of rows that are not there everything may be anything: it
+            // stays in its row.)
+            const int i0 = 16 * m + gr, i1 = i0 + 8;
+            const float from0 = dec.from[i0], from1 = dec.from[i1];
+            float out[4] = {(acc[0][0] + acc[1][0]) * from0, (acc[0][1] + acc[1][1]) * from0,
+                            (acc[0][2] + acc[1][2]) * from1, (acc[0][3] + acc[1][3]) * from1};
             for (int l = 0; l <= m; ++l) {
-                uint32_t W[4], R[4];  // two terms
-                const auto weights = [&](int n) {
-                    float own[4] = {};
+                float own[2][4] = {};
 #pragma unroll
-                    for (int st = 0; st < KS; ++st) {
-                        const auto *key = rows_.k[(kb + 16 * st) / 64];
-                        const int j = 16 * l + 8 * n + gr, col = (kb + 16 * st) % 64 + 2 * c;
-                        mma(own, A[st], word(key, j, col), word(key, j, col + 8));
-                    }
+                for (int st = 0; st < DK / 16; ++st) {
+                    uint32_t b[4];
+                    ldmatrix4(b, chunk(kt + (st >> 2) * Tiles<DK, NG>::T * 128, 16 * l + l7 + 8 * l16,
+                                       2 * (st & 3) + l8));
+                    mma(own[0], A[st], b[0], b[1]);
+                    mma(own[1], A[st], b[2], b[3]);
+                }
+                uint32_t W[4], R[4];  // the weights' two terms
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
                     const int j = 16 * l + 8 * n + 2 * c;
-                    const float w0 = j <= i0 && i0 < T ? own[0] * s.d[i0][j + 1] : 0.f;
-                    const float w1 = j < i0 && i0 < T ? own[1] * s.d[i0][j + 2] : 0.f;
-                    const float w2 = j <= i1 && i1 < T ? own[2] * s.d[i1][j + 1] : 0.f;
-                    const float w3 = j < i1 && i1 < T ? own[3] * s.d[i1][j + 2] : 0.f;
+                    const float2 d0 = *reinterpret_cast<const float2 *>(&dec.d[i0][j]);
+                    const float2 d1 = *reinterpret_cast<const float2 *>(&dec.d[i1][j]);
+                    const float w0 = j <= i0 ? own[n][0] * d0.x : 0.f, w1 = j < i0 ? own[n][1] * d0.y : 0.f;
+                    const float w2 = j <= i1 ? own[n][2] * d1.x : 0.f, w3 = j < i1 ? own[n][3] * d1.y : 0.f;
                     W[2 * n] = pack(w0, w1);
                     W[2 * n + 1] = pack(w2, w3);
                     R[2 * n] = pack(w0 - low(W[2 * n]), w1 - high(W[2 * n]));
                     R[2 * n + 1] = pack(w2 - low(W[2 * n + 1]), w3 - high(W[2 * n + 1]));
-                };
-                weights(0);
-                weights(1);
-                // Four columns of values from 4 gr, of rows 2c, 2c + 1 and 8 further (0 where there are none:
-                // their weights are 0, and they hold whatever lay there).
-                uint2 v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int j = 16 * l + 2 * c + (x & 1) + 8 * (x >> 1), col = 32 * side + 4 * gr;
-                    v[x] = j < T ? *reinterpret_cast<const uint2 *>(
-                                       &rows_.v[j][(col & 7) + 8 * ((col >> 3) ^ (j & 7))])
-                                 : make_uint2(0u, 0u);
                 }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t take = t & 1 ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(t < 2 ? v[0].x : v[0].y, t < 2 ? v[1].x : v[1].y, take);
-                    const uint32_t b1 = __byte_perm(t < 2 ? v[2].x : v[2].y, t < 2 ? v[3].x : v[3].y, take);
-                    mma(acc[t], R, b0, b1);
-                    mma(acc[t], W, b0, b1);
+                uint32_t v[2];
+                ldmatrix2_trans(v, chunk(vt, 16 * l + (lane & 15), warp));
+                if (16 * l + 16 > T) {  // values that are not there: their weights are 0, they may be anything
+                    const int j = 16 * l + 2 * c;
+                    v[0] &= (j < T ? 0xFFFFu : 0u) | (j + 1 < T ? 0xFFFF0000u : 0u);
+                    v[1] &= (j + 8 < T ? 0xFFFFu : 0u) | (j + 9 < T ? 0xFFFF0000u : 0u);
                 }
+                mma(out, R, v[0], v[1]);
+                mma(out, W, v[0], v[1]);
             }
-            // Column 2c (2c + 1) of product t is column 8c (+ 4) + t of the warp's 32.
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    *reinterpret_cast<float4 *>(
-                        &s.red[warp][gr + 8 * i][4 * ((8 * side + 2 * c + n) ^ (gr & 1))]) =
-                        make_float4(acc[0][2 * i + n], acc[1][2 * i + n], acc[2][2 * i + n], acc[3][2 * i + n]);
-            __syncthreads();
-            const int rows = min(16, T - 16 * m);
-            for (int e = tid; e < rows * (CV / 4); e += kThreads) {
-                const int i = e / (CV / 4), col = e % (CV / 4) * 4, row = 16 * m + i;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float4 y = *reinterpret_cast<const float4 *>(&s.red[x][i][4 * ((col / 4) ^ (i & 1))]);
-                    o.x += y.x;
-                    o.y += y.y;
-                    o.z += y.z;
-                    o.w += y.w;
-                }
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) +
-                                           ((long long)(w.u.row0 + row) * g.heads + w.h) * g.dv + w.c0 + col) =
-                    make_uint2(pack(o.x * g.scale, o.y * g.scale), pack(o.z * g.scale, o.w * g.scale));
-            }
-            __syncthreads();
+            const long long step = (long long)g.heads * g.dv;
+            if (i0 < T) *reinterpret_cast<uint32_t *>(o + i0 * step) = pack(out[0] * g.scale, out[1] * g.scale);
+            if (i1 < T) *reinterpret_cast<uint32_t *>(o + i1 * step) = pack(out[2] * g.scale, out[3] * g.scale);
         }
-        if (AHEAD)
-            buffer ^= 1;
-        else
-            if (tid == 0 && next.u.T > 0) copy_rows(next, s.rows[0]);  // all have left this unit's
-        w = next;
-        next = work_of(coming);
+        arrive_warp(bar(s.free[ring.slot]));
+        ring.next();
     }
 }
 
@@ -378,11 +360,11 @@ cudaError_t launch_one(const LinearArgs &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<drafts_kernel<DK, NG>>(smem);
     if (e != cudaSuccess) return e;
-    constexpr int fit = 233472 / (smem + 1024), per_sm = fit < 3 ? fit : 3;
+    constexpr int fit = 233472 / (smem + 1024), per_sm = fit < 2 ? fit : 2;
     static_assert(per_sm >= 1, "");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.units < 152 * per_sm ? L.units : 152 * per_sm);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * (kWarps + 1));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
