@@ -4,9 +4,9 @@
 // The state before the drafts stays as it is, so all of a request's rows read the same one:
 //     o_i = scale (d(i, -1) S^T q_i + sum_{j <= i} d(i, j) (q_i . k_j) v_j)
 // Bound by the states' bytes (64 KB a head of 128 x 128).  A block goes through units (request,
-// head, 64 value columns): a warp of its own finds them, asks the TMA engine for their state and rows
-// (128-byte swizzle, two units' worth of shared memory) and works out their decays; eight warps each
-// take 8 columns of a unit from there to o, so none waits for another.  A product has 16 rows of a
+// head, 64 value columns): one warp asks the TMA engine for their states and rows (128-byte swizzle, two
+// units' worth of shared memory), one works out their decays, and eight each take 8 columns of a unit
+// from there to o, so none waits for another.  A product has 16 rows of a
 // draft, so few rows cost as much as 16.  The state enters as two bf16 terms, off by 2^-17 of itself,
 // and so do the weights d(i, j) (q_i . k_j), which are operands of the values' product just where their
 // own product left them; q, k and v are bf16 already, and sums are float32.
@@ -19,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;  // that compute, 8 columns each; and one that loads
+constexpr int kWarps = 8;  // that compute, 8 columns each; one that loads, and one for the decays
 constexpr int CV = 8 * kWarps;
 
 __device__ __forceinline__ uint32_t pack(float x, float y) {
@@ -90,26 +90,35 @@ __device__ __forceinline__ void ldmatrix2_trans(uint32_t *x, uint32_t at) {
 // 16 bytes c of row r of a tile whose rows have 128.
 __device__ __forceinline__ uint32_t chunk(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
 
-// The warp that finds the units and loads them.
-template <int DK, int NG>
-__device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int lane) {
-    const LinearArgs &a = L.a;
-    const gdn_linear &g = a.g;
-    const unsigned slices = g.dv / CV;
-    constexpr int NB = Tiles<DK, NG>::BUFFERS;
-    // Units in order, `step` at a time; a unit's words are loaded a round before they are looked at.
+// The units of a block in order, `step` at a time; a unit's words are loaded a round before they are
+// looked at.  One lane's answer is the warp's.
+template <int DK>
+struct Units {
     struct Place {
         unsigned r, h, s;
-    };
-    auto place_of = [&](unsigned at) {
-        const unsigned unit = at / slices;
-        return Place{unit / (unsigned)g.heads, unit % (unsigned)g.heads, at - unit * slices};
     };
     struct Words {
         int c0, c1, slot;
         Place p;
     };
-    auto words_of = [&](const Place &p) {
+    const LinearArgs &a;
+    const unsigned units, slices, step;
+    unsigned at;
+    Place by, ahead;
+    Words coming;
+
+    __device__ __forceinline__ Units(const Launch &L)
+        : a(L.a), units(L.units), slices(L.a.g.dv / CV), step(gridDim.x), at(blockIdx.x) {  // (at + step: below 2^31)
+        by = place_of(step);
+        ahead = place_of(at);
+        coming = words_of(ahead);
+    }
+    __device__ __forceinline__ Place place_of(unsigned i) const {
+        const unsigned unit = i / slices, H = a.g.heads;
+        return Place{unit / H, unit % H, i - unit * slices};
+    }
+    __device__ __forceinline__ Words words_of(const Place &p) const {
+        const gdn_linear &g = a.g;
         Words x = {0, 0, -1, p};
         if (p.r >= (unsigned)g.batch) return x;
         x.slot = ld_early(g.slot_ids + p.r);
@@ -121,71 +130,101 @@ __device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int
             x.c1 = x.c0 + g.max_T;
         }
         return x;
-    };
-    auto work_of = [&](const Words &x) {
-        Work w = {0, 0, (int)x.p.h, (int)x.p.s * CV, 0};
-        LinearUnit u;
-        if (x.p.r < (unsigned)g.batch && linear_words(a, x.c0, x.c1, x.slot, w.h, u, lane == 0)) {
-            w.T = u.T;
-            w.row0 = u.row0;
-            w.row = (x.slot * g.heads + w.h) * DK;  // below 2^31: checked on the host
+    }
+    // The next unit that has rows; T = -1 after the last.
+    __device__ __forceinline__ Work next(bool report) {
+        const gdn_linear &g = a.g;
+        while (at < units) {
+            const Words x = coming;
+            at += step;
+            ahead.s += by.s;
+            ahead.h += by.h;
+            ahead.r += by.r;
+            if (ahead.s >= slices) {
+                ahead.s -= slices;
+                ++ahead.h;
+            }
+            if (ahead.h >= (unsigned)g.heads) {
+                ahead.h -= g.heads;
+                ++ahead.r;
+            }
+            coming = words_of(ahead);
+            LinearUnit u;
+            if (linear_words(a, x.c0, x.c1, x.slot, (int)x.p.h, u, report))
+                return Work{u.T, u.row0, (int)x.p.h, (int)x.p.s * CV,
+                            (x.slot * g.heads + (int)x.p.h) * DK};  // (rows of the pool: below 2^31)
         }
-        return w;
-    };
-    constexpr uint32_t kStateBytes = DK * CV * 4, kRowBytes = Tiles<DK, NG>::T * (2 * DK + CV) * 2;
-    const unsigned step = gridDim.x;  // (units and two steps fit 2^31)
-    const Place by = place_of(step);
-    auto advance = [&](Place &p) {
-        p.s += by.s;
-        p.h += by.h;
-        p.r += by.r;
-        if (p.s >= slices) {
-            p.s -= slices;
-            ++p.h;
-        }
-        if (p.h >= (unsigned)g.heads) {
-            p.h -= g.heads;
-            ++p.r;
-        }
-    };
-    Place ahead = place_of(blockIdx.x);
-    Words coming = words_of(ahead);
-    Ring<NB> ring;
-    for (unsigned at = blockIdx.x; at < L.units; at += step) {
-        const Work w = work_of(coming);
-        advance(ahead);
-        coming = words_of(ahead);
-        if (w.T <= 0) continue;
-        constexpr int T = Tiles<DK, NG>::T;
-        float log[(T + 31) / 32];
-#pragma unroll
-        for (int i = 0; i < (T + 31) / 32; ++i)
-            log[i] = 32 * i + lane < w.T ? ld_early(g.log_decay + (long long)(w.row0 + 32 * i + lane) * g.decay_stride + w.h)
-                                         : 0.f;
-        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) break;
+        return Work{-1, 0, 0, 0, 0};
+    }
+};
+
+// The warp that loads the units' states and rows.
+template <int DK, int NG>
+__device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int lane) {
+    constexpr uint32_t kBytes = DK * CV * 4 + Tiles<DK, NG>::T * (2 * DK + CV) * 2;
+    const gdn_linear &g = L.a.g;
+    Units<DK> units(L);
+    Ring<Tiles<DK, NG>::BUFFERS> ring;
+    for (;; ring.next()) {
+        const Work w = units.next(lane == 0);
+        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) return;
         const uint32_t full = bar(s.full[ring.slot]);
         auto &to = s.unit[ring.slot];
         if (lane == 0) {
-            arrive_expect(full, kStateBytes + kRowBytes);
-            const int col = w.h / a.group * DK;
-            for (int x = 0; x < DK / 64; ++x) {
-                tma(to.q[x], &L.q, col + 64 * x, w.row0, full);
-                tma(to.k[x], &L.k, col + 64 * x, w.row0, full);
+            s.work[ring.slot] = w;
+            if (w.T < 0) {
+                arrive(full);
+            } else {
+                arrive_expect(full, kBytes);
+                for (int x = 0; x < 2; ++x) tma(to.state[x], &L.pool, w.c0 + 32 * x, w.row, full);
+                const int col = w.h / L.a.group * DK;
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma(to.q[x], &L.q, col + 64 * x, w.row0, full);
+                    tma(to.k[x], &L.k, col + 64 * x, w.row0, full);
+                }
+                tma(to.v, &L.v, w.h * g.dv + w.c0, w.row0, full);
             }
-            tma(to.v, &L.v, w.h * g.dv + w.c0, w.row0, full);
-            for (int x = 0; x < 2; ++x) tma(to.state[x], &L.pool, w.c0 + 32 * x, w.row, full);
         }
         __syncwarp();
+        if (w.T < 0) return;
+    }
+}
+
+// The warp that works out their decays.
+template <int DK, int NG>
+__device__ __forceinline__ void decay_role(const Launch &L, Tiles<DK, NG> &s, int lane) {
+    constexpr int T = Tiles<DK, NG>::T, N = (T + 31) / 32;
+    const gdn_linear &g = L.a.g;
+    Units<DK> units(L);
+    Ring<Tiles<DK, NG>::BUFFERS> ring;
+    float log[N];
+    auto load = [&](const Work &w) {
 #pragma unroll
-        for (int i = 0; i < (T + 31) / 32; ++i)
+        for (int i = 0; i < N; ++i)
+            log[i] = 32 * i + lane < w.T
+                         ? ld_early(g.log_decay + (long long)(w.row0 + 32 * i + lane) * g.decay_stride + w.h)
+                         : 0.f;
+    };
+    Work w = units.next(false);
+    load(w);
+    for (;; ring.next()) {
+        const int rows = w.T;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
             if (32 * i + lane < T) s.g[32 * i + lane] = log[i];
         __syncwarp();
-        // Row i's decays: sums from its end on.  Up to 16 rows: a lane a row (l), two sums at a time.
-        auto &to_d = s.decays[ring.slot];
-        if (NG == 1) {
+        if (rows >= 0) {
+            w = units.next(false);
+            load(w);
+        }
+        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) return;
+        auto &to = s.decays[ring.slot];
+        // Row i's: sums from its end on.  Up to 16 rows: a lane a row (l), two sums at a time.
+        if (NG == 1 && rows > 0) {
             const int l = lane & 15;
-#pragma unroll 2
-            for (int i = lane >> 4; i < 16; i += 2) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = 2 * k + (lane >> 4);
                 float sum = l <= i ? s.g[l] : 0.f;
 #pragma unroll
                 for (int d = 1; d < 16; d <<= 1) {
@@ -194,41 +233,33 @@ __device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int
                 }
                 const float d = expf(sum);  // of rows l to i: d(i, l - 1)
                 if (l == 0) {
-                    to_d.from[i] = d;
-                    to_d.d[i][i] = 1.f;
+                    to.from[i] = d;
+                    to.d[i][i] = 1.f;
                 } else if (l <= i) {
-                    to_d.d[i][l - 1] = d;
+                    to.d[i][l - 1] = d;
                 }
             }
         } else {
-            for (int l = lane; l < w.T; l += 32) {  // down column l - 1
+            for (int l = lane; l < rows; l += 32) {  // down column l - 1
                 float sum = 0.f;
-                to_d.d[l][l] = 1.f;
-                for (int i = l; i < w.T; ++i) {
+                to.d[l][l] = 1.f;
+                for (int i = l; i < rows; ++i) {
                     sum += s.g[i];
                     const float d = expf(sum);
                     if (l == 0)
-                        to_d.from[i] = d;
+                        to.from[i] = d;
                     else
-                        to_d.d[i][l - 1] = d;
+                        to.d[i][l - 1] = d;
                 }
             }
         }
-        if (lane == 0) s.work[ring.slot] = w;
-        __syncwarp();
-        if (lane == 0) arrive(full);
-        ring.next();
-    }
-    if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) return;
-    if (lane == 0) {
-        s.work[ring.slot].T = -1;
-        arrive(bar(s.full[ring.slot]));
-        arrive(bar(s.full[ring.slot]));
+        arrive_warp(bar(s.full[ring.slot]));
+        if (rows < 0) return;
     }
 }
 
 template <int DK, int NG>
-__global__ void __launch_bounds__(32 * (kWarps + 1), 2) drafts_kernel(const __grid_constant__ Launch L) {
+__global__ void __launch_bounds__(32 * (kWarps + 2), 2) drafts_kernel(const __grid_constant__ Launch L) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char raw[];
     constexpr int NB = Tiles<DK, NG>::BUFFERS;
@@ -245,8 +276,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) drafts_kernel(const __gr
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
-    if (warp == kWarps) {
-        load_role<DK, NG>(L, s, lane);
+    if (warp >= kWarps) {
+        if (warp == kWarps)
+            load_role<DK, NG>(L, s, lane);
+        else
+            decay_role<DK, NG>(L, s, lane);
         return;
     }
 
@@ -364,7 +398,7 @@ cudaError_t launch_one(const LinearArgs &a, cudaStream_t stream) {
     static_assert(per_sm >= 1, "");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.units < 152 * per_sm ? L.units : 152 * per_sm);
-    cfg.blockDim = dim3(32 * (kWarps + 1));
+    cfg.blockDim = dim3(32 * (kWarps + 2));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
