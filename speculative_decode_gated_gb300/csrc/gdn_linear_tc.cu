@@ -10,16 +10,19 @@
 // hand on through barriers:
 //   TMA warp     K and V tiles, two blocks ahead (128-byte swizzle)
 //   MMA warp     the four products
-//   weights      (warpgroup, a thread a row) the decays, and W in two bf16 terms: each product v_j d
-//                enters its state to 2^-17 of itself
+//   decays       (a warp, four rows a lane) see below
+//   weights      (warpgroup, a thread a row) W in two bf16 terms: each product v_j d enters its state
+//                to 2^-17 of itself
 //   mask         (a thread a row) scores times decays to P, in tensor memory over the scores
 //   state        (a thread a row of dk) S in registers, its bf16 copy in shared memory for O2
 //   output       (a thread a row) Q to tensor memory, from where both its products take it, and o
 //
-// Decays.  No exponent is positive and nothing cancels: within a warp's 32 rows, e^{...} of sums
-// taken from the row to the end of the 32 (cf) or from their start to the row (rowf); t, those
-// of whole 32s.  d(i, j) = cf_j (t of the 32s between) rowf_i; within the 32, products of
-// single decays.
+// Decays.  With b the 32 rows that row i is one of, and B_b the sum up to its start,
+//     d(i, j) = e^{G_i - B_b} e^{B_b - G_j}:
+// the first factor is left to o, so a score needs one product, with a column's factor that all of
+// the 32 rows share.  For an earlier 32's rows neither exponent is positive; for its own the second
+// one is, up to e^60: where the logarithms of 32 rows add up to more, their decays are products
+// of single ones, taken one by one.  All sums run from their own first row, so nothing cancels.
 #include <cstdint>
 
 #include "gdn_launch.h"
@@ -34,7 +37,9 @@ constexpr int NV = 64;               // value columns
 constexpr int kBox = C * 128;        // bytes of 64 columns of a tile
 constexpr int kKeyTile = 2 * kBox;   // of queries, keys (dk = 64: the second half is not used)
 constexpr int kAhead = 4;            // blocks that come to L2 before
-constexpr int kThreads = 18 * 32;    // weights, mask, state, output; TMA, MMA
+constexpr int kThreads = 19 * 32;    // weights, mask, state, output; TMA, MMA, decays
+constexpr float kSteep = 60.f;
+constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
 constexpr int kTiles = 2 * kKeyTile + 2 * kBox + 2 * kWTile + kBox;  // K, V and W twice; S
 
@@ -45,13 +50,21 @@ struct Bars {
     unsigned long long q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     unsigned long long dec_full[2], dec_empty[2];
     unsigned long long w_ready[2][4], w_free[2][4];  // by 32 rows
-    unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, w_sync, drain;
+    unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
 };
 
 struct Shared {
     Bars b;
-    alignas(16) float cf[2][C];  // read four at a time
-    float rowf[2][C], t[2][4];
+    struct Decays {
+        alignas(16) float column[4][C];  // of an earlier or the same 32: e^{B_b - G_j}
+        alignas(16) float log[C], row[C];   // (where steep) g_i, e^{G_i - B_b}
+        alignas(16) float o1[C], o2[C];     // factors of O1 and O2: scale e^{G_i - B_b} (or scale), scale e^{G_i}
+        alignas(16) float weight[C];        // e^{G_(C-1) - G_j}; 0 for rows past the end
+        float keep;                         // e^{G_(C-1)}
+        int steep;                          // a bit a 32
+    } dec[2];
+    unsigned short order[kSorted];          // requests, longest first
+    int length[kSorted];
     uint32_t tmem;
     int dead;  // a wait gave up: every role leaves
 };
@@ -61,6 +74,7 @@ struct Launch {
     LinearArgs a;
     CUtensorMap k, v;
     int slices;
+    bool sorted;     // ragged requests, longest first
     bool q32, o32;  // rows are aligned to 32 bytes
     long long units;
 };
@@ -71,13 +85,14 @@ struct Unit {
     LinearUnit u;
     int n;         // blocks of rows
 };
-__device__ __forceinline__ bool next_unit(const Launch &L, bool commit, long long &at, Unit &x) {
+__device__ __forceinline__ bool next_unit(const Launch &L, const Shared &s, bool commit, long long &at, Unit &x) {
     for (; at < L.units; at += gridDim.x) {
-        const int s = (int)(at % L.slices);
+        const int slice = (int)(at % L.slices);
         const long long rh = at / L.slices;
         x.r = (int)(rh / L.a.g.heads);
         x.h = (int)(rh - (long long)x.r * L.a.g.heads);
-        x.c0 = s * NV;
+        if (L.sorted) x.r = s.order[x.r];
+        x.c0 = slice * NV;
         if (linear_unit(L.a, x.r, x.h, commit, x.u)) {
             x.n = (x.u.T + C - 1) / C;
             at += gridDim.x;
@@ -172,12 +187,6 @@ struct Tiles {
         : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + 2 * kWTile) {}
 };
 
-// The logarithm of row i's decay (0 for rows past the block's end).
-__device__ __forceinline__ float log_decay(const gdn_linear &g, const Unit &x, int c, int i) {
-    const int row = c * C + i;
-    return row < x.u.T ? __ldg(g.log_decay + (x.u.row0 + (long long)row) * g.decay_stride + x.h) : 0.f;
-}
-
 // ---------------------------------------------------------------- the TMA warp (one thread)
 
 __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tiles &t, bool commit,
@@ -186,7 +195,7 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tile
     const int boxes = g.dk / 64;
     long long at = blockIdx.x;
     Unit x;
-    while (next_unit(L, commit, at, x)) {
+    while (next_unit(L, s, commit, at, x)) {
         const int kx = x.h / L.a.group * g.dk, vx = x.h * g.dv + x.c0;
         for (int c = 0; c < x.n; ++c, ++issued) {
             const uint32_t slot = issued & 1, free = ((issued >> 1) & 1) ^ 1;
@@ -231,7 +240,7 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         commit(lead, bar(s.b.s_full));
         return true;
     };
-    while (next_unit(L, !OUT, at, x)) {
+    while (next_unit(L, s, !OUT, at, x)) {
         const int n = __shfl_sync(0xffffffffu, x.n, 0);
         if (OUT && !scores(it)) return;
         for (int c = 0; c < n; ++c, ++it) {
@@ -277,43 +286,124 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
     }
 }
 
+// ---------------------------------------------------------------- the decays' warp
+
+template <bool OUT>
+__device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane) {
+    const gdn_linear &g = L.a.g;
+    const int b = lane >> 3, l = lane & 7;  // this lane's rows: 4 lane to 4 lane + 3, of the 32 that are b
+    long long at = blockIdx.x;
+    Unit x;
+    uint32_t it = 0;
+    float next[4];
+    while (next_unit(L, s, !OUT, at, x)) {
+        auto load = [&](int c) {  // 0 for rows past the end
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = c * C + 4 * lane + k;
+                next[k] = row < x.u.T ? __ldg(g.log_decay + (x.u.row0 + (long long)row) * g.decay_stride + x.h) : 0.f;
+            }
+        };
+        load(0);
+        for (int c = 0; c < x.n; ++c, ++it) {
+            const uint32_t slot = it & 1, half = (it >> 1) & 1;
+            const int n = min(C, x.u.T - c * C);
+            const float gl[4] = {next[0], next[1], next[2], next[3]};
+            if (c + 1 < x.n) load(c + 1);
+            // Sums within the 32: from its start up to each row, and from behind it to the end.
+            float upto[4] = {gl[0], gl[0] + gl[1], 0.f, 0.f}, after[4] = {0.f, 0.f, gl[3], 0.f};
+            upto[2] = upto[1] + gl[2];
+            upto[3] = upto[2] + gl[3];
+            after[1] = after[2] + gl[2];
+            after[0] = after[1] + gl[1];
+            float below = upto[3], above = upto[3];
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, below, d, 8);
+                const float z = __shfl_down_sync(0xffffffffu, above, d, 8);
+                if (l >= d) below += y;
+                if (l + d < 8) above += z;
+            }
+            const float total = __shfl_sync(0xffffffffu, below, lane | 7);
+            below = __shfl_up_sync(0xffffffffu, below, 1, 8);
+            above = __shfl_down_sync(0xffffffffu, above, 1, 8);
+            if (l == 0) below = 0.f;
+            if (l == 7) above = 0.f;
+            bool mild = true;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                upto[k] += below;
+                after[k] += above;
+                mild = mild && fabsf(upto[k]) < kSteep;  // (false for NaN)
+            }
+            const unsigned steep = ~__ballot_sync(0xffffffffu, mild);
+            const bool steep_here = (steep >> (8 * b) & 0xFFu) != 0;
+            const float whole = expf(total);
+            float t[4];  // of the four 32s
+#pragma unroll
+            for (int m = 0; m < 4; ++m) t[m] = __shfl_sync(0xffffffffu, whole, 8 * m);
+            if (!wait(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
+            Shared::Decays &d = s.dec[slot];
+            float row[4], col[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                row[k] = expf(upto[k]);
+                col[k] = expf(after[k]);
+            }
+            auto put = [&](float *to, float w, float x, float y, float z) {
+                *reinterpret_cast<float4 *>(to + 4 * lane) = make_float4(w, x, y, z);
+            };
+            float f = 1.f;
+#pragma unroll
+            for (int m = 1; m < 4; ++m) {
+                if (m <= b) continue;  // the rows of earlier 32s do not see this one
+                if (OUT) put(d.column[m], f * col[0], f * col[1], f * col[2], f * col[3]);
+                f *= t[m];
+            }
+            const int i = 4 * lane;
+            put(d.weight, i < n ? f * col[0] : 0.f, i + 1 < n ? f * col[1] : 0.f, i + 2 < n ? f * col[2] : 0.f,
+                i + 3 < n ? f * col[3] : 0.f);
+            if (OUT) {
+                put(d.column[b], expf(-upto[0]), expf(-upto[1]), expf(-upto[2]), expf(-upto[3]));
+                float e = g.scale;
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    if (m < b) e *= t[m];
+                put(d.o2, e * row[0], e * row[1], e * row[2], e * row[3]);
+                if (steep_here) {
+                    put(d.log, gl[0], gl[1], gl[2], gl[3]);
+                    put(d.row, row[0], row[1], row[2], row[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) row[k] = 1.f;
+                }
+                put(d.o1, g.scale * row[0], g.scale * row[1], g.scale * row[2], g.scale * row[3]);
+            }
+            if (lane == 0) {
+                d.keep = t[0] * t[1] * (t[2] * t[3]);
+                d.steep = ((steep & 0xFFu) != 0) | ((steep >> 8 & 0xFFu) != 0) << 1 |
+                          ((steep >> 16 & 0xFFu) != 0) << 2 | ((steep >> 24) != 0) << 3;
+            }
+            arrive_warp(bar(s.b.dec_full[slot]));
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the weights' warpgroup
 
 template <bool OUT>
 __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Tiles &t, int j) {
     const gdn_linear &g = L.a.g;
-    const int lane = j & 31, b = j >> 5;
+    const int b = j >> 5;
     long long at = blockIdx.x;
     Unit x;
     uint32_t it = 0;
-    while (next_unit(L, !OUT, at, x)) {
-        float gj = log_decay(g, x, 0, j);
+    while (next_unit(L, s, !OUT, at, x)) {
         for (int c = 0; c < x.n; ++c, ++it) {
             const uint32_t slot = it & 1, half = (it >> 1) & 1;
             const int n = min(C, x.u.T - c * C);
-            float upto = gj, after = __shfl_down_sync(0xffffffffu, gj, 1);
-            if (lane == 31) after = 0.f;
-            if (c + 1 < x.n) gj = log_decay(g, x, c + 1, j);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, upto, d);
-                const float z = __shfl_down_sync(0xffffffffu, after, d);
-                if (lane >= d) upto += y;
-                if (lane + d < 32) after += z;
-            }
-            const float cf = expf(after);
-            if (!wait(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
-            const float rowf = expf(upto);
-            s.rowf[slot][j] = rowf;
-            s.cf[slot][j] = cf;
-            if (lane == 31) s.t[slot][b] = rowf;
-            arrive_warp(bar(s.b.dec_full[slot]));
-            arrive_warp(bar(s.b.w_sync));
-            if (!wait(bar(s.b.w_sync), it & 1, &s.dead)) return;
-            float w = cf;
-#pragma unroll
-            for (int m = 1; m < 4; ++m)
-                if (m > b) w *= s.t[slot][m];
+            if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+            const float w = s.dec[slot].weight[j];
+            arrive_warp(bar(s.b.dec_empty[slot]));
             if (!wait(bar(s.b.v_full[slot]), half, &s.dead)) return;
             const uint32_t vt = t.v + slot * kBox;
             const uint32_t zero[4] = {0, 0, 0, 0};
@@ -356,67 +446,79 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
 
 // ---------------------------------------------------------------- the mask's warpgroup
 
+// A warp's rows whose 32 is steep: the factors of earlier 32s' columns times the row's, and its own
+// decays one by one.  (A function of its own, so that its registers are not the others'.)
+__device__ __noinline__ void mask_steep(const Shared::Decays &d, uint32_t ts, int lane, int b) {
+    const float f = d.row[32 * b + lane];
+#pragma unroll 1
+    for (int m = 0; m <= b; ++m) {
+        uint32_t y[32];
+        tmem_ld32(ts + 32 * m, y);
+        wait_ld();
+        if (m < b) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                y[e] = __float_as_uint(__uint_as_float(y[e]) * (d.column[b][32 * m + e] * f));
+        } else {
+            float p = 1.f;
+#pragma unroll
+            for (int e = 31; e >= 0; --e) {
+                if (e < lane) p *= expf(d.log[32 * b + e + 1]);
+                y[e] = e <= lane ? __float_as_uint(__uint_as_float(y[e]) * p) : 0u;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+            y[e / 2] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+        tmem_st16(ts + 16 * m, y);  // over scores that have been read
+    }
+}
+
 __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t tm, int i) {
-    const gdn_linear &g = L.a.g;
     const int lane = i & 31, b = i >> 5;
     const uint32_t ts = tm + kScores + ((uint32_t)b << 21);  // this warp's lanes
     long long at = blockIdx.x;
     Unit x;
     uint32_t it = 0;
-    while (next_unit(L, false, at, x)) {
-        float gi = log_decay(g, x, 0, i);
+    while (next_unit(L, s, false, at, x)) {
         for (int c = 0; c < x.n; ++c, ++it) {
             const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            const float lam = expf(gi);
-            if (c + 1 < x.n) gi = log_decay(g, x, c + 1, i);
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+            const Shared::Decays &d = s.dec[slot];
             if (!wait(bar(s.b.s_full), it & 1, &s.dead)) return;
             fence_after();
-            const float rowf = s.rowf[slot][i];
-            // Earlier 32s: all of their rows are seen.
+            if (d.steep >> b & 1) {
+                mask_steep(d, ts, lane, b);
+            } else {
 #pragma unroll 1
-            for (int m = 0; m < b; ++m) {
-                float f = rowf;
-                for (int k = m + 1; k < b; ++k) f *= s.t[slot][k];
-                const float2 f2 = make_float2(f, f);
-                uint32_t y[32];
-                tmem_ld32(ts + 32 * m, y);
-                wait_ld();
+                for (int m = 0; m <= b; ++m) {
+                    uint32_t y[32];
+                    tmem_ld32(ts + 32 * m, y);
+                    const float *column = d.column[b] + 32 * m;
+                    wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 cf = *reinterpret_cast<const float4 *>(&s.cf[slot][32 * m + e]);
-                    const float2 p0 = mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
-                                           mul2(make_float2(cf.x, cf.y), f2));
-                    const float2 p1 = mul2(make_float2(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])),
-                                           mul2(make_float2(cf.z, cf.w), f2));
-                    y[e / 2] = pack_bf16(p0.x, p0.y);
-                    y[e / 2 + 1] = pack_bf16(p1.x, p1.y);
-                }
-                tmem_st16(ts + 16 * m, y);  // over scores that have been read
-            }
-            // The row's own 32, up to itself.
-            {
-                uint32_t y[32];
-                tmem_ld32(ts + 32 * b, y);
-                wait_ld();
-                float d = 1.f;
-#pragma unroll
-                for (int e = 31; e >= 0; --e) {
-                    if (e < 31) {
-                        const float next = __shfl_sync(0xffffffffu, lam, e + 1);
-                        if (e + 1 <= lane) d *= next;
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(column + e);
+                        const float2 p0 = mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                                               make_float2(w.x, w.y));
+                        const float2 p1 = mul2(make_float2(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])),
+                                               make_float2(w.z, w.w));
+                        y[e / 2] = pack_bf16(p0.x, p0.y);
+                        y[e / 2 + 1] = pack_bf16(p1.x, p1.y);
                     }
-                    y[e] = e <= lane ? __float_as_uint(__uint_as_float(y[e]) * d) : 0u;
+                    if (m == b) {  // its own 32: up to itself
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            y[e] &= (2 * e <= lane ? 0xFFFFu : 0u) | (2 * e + 1 <= lane ? 0xFFFF0000u : 0u);
+                    }
+                    tmem_st16(ts + 16 * m, y);  // over scores that have been read
                 }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    y[e / 2] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                tmem_st16(ts + 16 * b, y);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = 0u;
-#pragma unroll 1
-                for (int m = b + 1; m < 4; ++m) tmem_st16(ts + 16 * m, y);
             }
+            uint32_t zero[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll 1
+            for (int m = b + 1; m < 4; ++m) tmem_st16(ts + 16 * m, zero);
             arrive_warp(bar(s.b.dec_empty[slot]));
             wait_st();
             fence_before();
@@ -434,7 +536,7 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
     long long at = blockIdx.x;
     Unit x;
     uint32_t it = 0;
-    while (next_unit(L, !OUT, at, x)) {
+    while (next_unit(L, s, !OUT, at, x)) {
         float *row = x.u.tile + (long long)d * g.dv + x.c0;
         float S[NV];
 #pragma unroll
@@ -462,7 +564,7 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
                 arrive_warp(bar(s.b.st_ready));
             }
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            const float keep = s.t[slot][0] * s.t[slot][1] * (s.t[slot][2] * s.t[slot][3]);
+            const float keep = s.dec[slot].keep;
             arrive_warp(bar(s.b.dec_empty[slot]));
             if (!wait(bar(s.b.u_full), it & 1, &s.dead)) return;
             fence_after();
@@ -501,7 +603,7 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, uint32_t
     long long at = blockIdx.x;
     Unit x;
     uint32_t it = 0;
-    while (next_unit(L, false, at, x)) {
+    while (next_unit(L, s, false, at, x)) {
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + (long long)(x.h / L.a.group) * g.dk;
         // Row i of block c to tensor memory, where block `to`'s are (its scores and O2 have been computed).
         auto queries = [&](int c, uint32_t to) {
@@ -538,12 +640,11 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, uint32_t
             }
             if (c + 1 < x.n) queries(c + 1, it + 1);
             if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            float f = s.rowf[slot][i] * g.scale;
-            for (int m = 0; m < b; ++m) f *= s.t[slot][m];
+            const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
             arrive_warp(bar(s.b.dec_empty[slot]));
             if (!wait(bar(s.b.o_full), it & 1, &s.dead)) return;
             fence_after();
-            const float2 f2 = make_float2(f, f), scale2 = make_float2(g.scale, g.scale);
+            const float2 f2 = make_float2(f, f), scale2 = make_float2(f1, f1);
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) +
                                (x.u.row0 + (long long)c * C + i) * g.heads * g.dv + x.h * g.dv + x.c0;
 #pragma unroll
@@ -588,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(bar(s.b.v_full[i]), 1);
             mbar_init(bar(s.b.k_empty[i]), 1);
             mbar_init(bar(s.b.v_empty[i]), 1);
-            mbar_init(bar(s.b.dec_full[i]), 4);
-            mbar_init(bar(s.b.dec_empty[i]), OUT ? 12 : 4);
+            mbar_init(bar(s.b.dec_full[i]), 1);
+            mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
         }
         for (int i = 0; i < 4; ++i) {
             for (int k = 0; k < 2; ++k) {
@@ -605,7 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(bar(s.b.st_free), 1);
         mbar_init(bar(s.b.o_full), 1);
         mbar_init(bar(s.b.o_free), 4);
-        mbar_init(bar(s.b.w_sync), 4);
         mbar_init(bar(s.b.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s.dead = 0;
@@ -618,6 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (L.sorted) {
+        const gdn_linear &g = L.a.g;
+        for (int i = tid; i < g.batch; i += kThreads) s.length[i] = g.cu_seqlens[i + 1] - g.cu_seqlens[i];
+        __syncthreads();
+        for (int i = tid; i < g.batch; i += kThreads) {
+            int before = 0;
+            for (int k = 0; k < g.batch; ++k)
+                before += s.length[k] > s.length[i] || (s.length[k] == s.length[i] && k < i);
+            s.order[before] = (unsigned short)i;
+        }
+    }
     __syncthreads();  // the barriers and the tensor memory's address
     fence_after();
     const uint32_t tm = *(volatile uint32_t *)&s.tmem;
@@ -630,6 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         state_role<OUT, STATE>(L, s, t, tm, tid - 256);
     } else if (warp < 16) {
         if (OUT) output_role(L, s, tm, tid - 384);
+    } else if (warp == 18) {
+        decay_role<OUT>(L, s, tid & 31);
     } else if (warp == 16) {
         if ((tid & 31) == 0) {
             uint32_t issued = 0;
@@ -679,6 +792,7 @@ cudaError_t launch_tc(const LinearArgs &a, cudaStream_t stream) {
     L.q32 = (reinterpret_cast<uintptr_t>(g.q) & 31) == 0 && g.q_stride % 16 == 0;
     L.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
     L.units = (long long)g.batch * g.heads * L.slices;
+    L.sorted = g.cu_seqlens && g.batch > 1 && g.batch <= kSorted && L.units > 152;
     const long long krow = (long long)g.k_heads * g.dk, vrow = (long long)g.heads * g.dv;
     if (!encoder() || !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
         !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride))
