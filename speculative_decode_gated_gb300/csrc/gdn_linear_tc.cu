@@ -9,7 +9,7 @@
 // Only S goes from block to block: everything else runs ahead of it, in roles that
 // hand on through barriers:
 //   TMA warp     K and V tiles, two blocks ahead (128-byte swizzle)
-//   MMA warp     the four products
+//   MMA warps    U; the other three products
 //   decays       (a warp, four rows a lane) see below
 //   weights      (warpgroup, a thread a row) W in two bf16 terms: each product v_j d enters its state
 //                to 2^-17 of itself
@@ -37,7 +37,7 @@ constexpr int NV = 64;               // value columns
 constexpr int kBox = C * 128;        // bytes of 64 columns of a tile
 constexpr int kKeyTile = 2 * kBox;   // of queries, keys (dk = 64: the second half is not used)
 constexpr int kAhead = 4;            // blocks that come to L2 before
-constexpr int kThreads = 19 * 32;    // weights, mask, state, output; TMA, MMA, decays
+constexpr int kThreads = 20 * 32;    // weights, mask, state, output; TMA, MMA, decays, U
 constexpr float kSteep = 60.f;
 constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
@@ -49,7 +49,7 @@ constexpr uint32_t kScores = 0, kQ = 128, kO1 = 256, kO2 = 320, kU = 384;  // (k
 struct Bars {
     unsigned long long q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     unsigned long long dec_full[2], dec_empty[2];
-    unsigned long long w_ready[2][4], w_free[2][4];  // by 32 rows
+    unsigned long long w_ready[2], w_free[2];
     unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
 };
 
@@ -79,27 +79,21 @@ struct Launch {
     long long units;
 };
 
-// The units of a block, in order.
+// The unit of a block (one each).
 struct Unit {
     int r, h, c0;  // request, head, first value column
     LinearUnit u;
     int n;         // blocks of rows
 };
-__device__ __forceinline__ bool next_unit(const Launch &L, const Shared &s, bool commit, long long &at, Unit &x) {
-    for (; at < L.units; at += gridDim.x) {
-        const int slice = (int)(at % L.slices);
-        const long long rh = at / L.slices;
-        x.r = (int)(rh / L.a.g.heads);
-        x.h = (int)(rh - (long long)x.r * L.a.g.heads);
-        if (L.sorted) x.r = s.order[x.r];
-        x.c0 = slice * NV;
-        if (linear_unit(L.a, x.r, x.h, commit, x.u)) {
-            x.n = (x.u.T + C - 1) / C;
-            at += gridDim.x;
-            return true;
-        }
-    }
-    return false;
+__device__ __forceinline__ bool find_unit(const Launch &L, const Shared &s, bool commit, Unit &x) {
+    const int slice = blockIdx.x % L.slices, rh = blockIdx.x / L.slices;
+    x.r = rh / L.a.g.heads;
+    x.h = rh - x.r * L.a.g.heads;
+    if (L.sorted) x.r = s.order[x.r];
+    x.c0 = slice * NV;
+    if (!linear_unit(L.a, x.r, x.h, commit, x.u)) return false;
+    x.n = (x.u.T + C - 1) / C;
+    return true;
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t b) {
@@ -180,6 +174,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
+// The waits' slow path out of line: twenty warps in eight roles share the instruction cache.
+__device__ __noinline__ bool wait_long(uint32_t b, uint32_t parity, int *dead) {
+    return wait_one(b, parity, dead);
+}
+__device__ __forceinline__ bool await(uint32_t b, uint32_t parity, int *dead) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    return __all_sync(0xffffffffu, wait_long(b, parity, dead));
+}
+
 // Shared-memory tiles.
 struct Tiles {
     uint32_t k, v, w, s;
@@ -193,96 +196,92 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tile
                                           uint32_t &issued) {
     const gdn_linear &g = L.a.g;
     const int boxes = g.dk / 64;
-    long long at = blockIdx.x;
     Unit x;
-    while (next_unit(L, s, commit, at, x)) {
-        const int kx = x.h / L.a.group * g.dk, vx = x.h * g.dv + x.c0;
-        for (int c = 0; c < x.n; ++c, ++issued) {
-            const uint32_t slot = issued & 1, free = ((issued >> 1) & 1) ^ 1;
-            const int y = x.u.row0 + c * C;
-            // L2 first, some blocks before: the ring holds two, and memory takes longer than one.
-            for (int a = c == 0 ? 1 : kAhead; a <= kAhead && c + a < x.n; ++a) {
-                tma_prefetch(&L.v, vx, y + a * C);
-                for (int b = 0; b < boxes; ++b) tma_prefetch(&L.k, kx + 64 * b, y + a * C);
-            }
-            if (!wait_one(bar(s.b.k_empty[slot]), free, &s.dead)) return;
-            arrive_expect(bar(s.b.k_full[slot]), boxes * kBox);
-            for (int b = 0; b < boxes; ++b)
-                tma_load(t.k + slot * kKeyTile + b * kBox, &L.k, kx + 64 * b, y, bar(s.b.k_full[slot]));
-            if (!wait_one(bar(s.b.v_empty[slot]), free, &s.dead)) return;
-            arrive_expect(bar(s.b.v_full[slot]), kBox);
-            tma_load(t.v + slot * kBox, &L.v, vx, y, bar(s.b.v_full[slot]));
+    if (!find_unit(L, s, commit, x)) return;
+    const int kx = x.h / L.a.group * g.dk, vx = x.h * g.dv + x.c0;
+    for (int c = 0; c < x.n; ++c, ++issued) {
+        const uint32_t slot = issued & 1, free = ((issued >> 1) & 1) ^ 1;
+        const int y = x.u.row0 + c * C;
+        // L2 first, some blocks before: the ring holds two, and memory takes longer than one.
+        for (int a = c == 0 ? 1 : kAhead; a <= kAhead && c + a < x.n; ++a) {
+            tma_prefetch(&L.v, vx, y + a * C);
+            for (int b = 0; b < boxes; ++b) tma_prefetch(&L.k, kx + 64 * b, y + a * C);
         }
+        if (!wait_one(bar(s.b.k_empty[slot]), free, &s.dead)) return;
+        arrive_expect(bar(s.b.k_full[slot]), boxes * kBox);
+        for (int b = 0; b < boxes; ++b)
+            tma_load(t.k + slot * kKeyTile + b * kBox, &L.k, kx + 64 * b, y, bar(s.b.k_full[slot]));
+        if (!wait_one(bar(s.b.v_empty[slot]), free, &s.dead)) return;
+        arrive_expect(bar(s.b.v_full[slot]), kBox);
+        tma_load(t.v + slot * kBox, &L.v, vx, y, bar(s.b.v_full[slot]));
     }
 }
 
-// ---------------------------------------------------------------- the MMA warp
+// ---------------------------------------------------------------- the MMA warps
 
-template <bool OUT>
+// Scores, Q S and P V.  Every wait and every instruction of these two warps is on the way from block
+// to block, so U, which waits on other roles, has a warp of its own, and both are short.
+template <int DK>
 __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm) {
-    const uint32_t lead = elect();
-    const int steps = __shfl_sync(0xffffffffu, L.a.g.dk / 16, 0);
-    const uint32_t k_lo = desc_lo(t.k, 16);     // rows of 64 columns
-    const uint32_t kt_lo = desc_lo(t.k, kBox);  // K^T, 128 of its rows
-    const uint32_t v_lo = desc_lo(t.v, kBox), w_lo = desc_lo(t.w, kBox), s_lo = desc_lo(t.s, kBox);
-    tm = __shfl_sync(0xffffffffu, tm, 0);
-    long long at = blockIdx.x;
+    const uint32_t lead = elect(), k_lo = desc_lo(t.k, 16), v_lo = desc_lo(t.v, kBox), s_lo = desc_lo(t.s, kBox);
     Unit x;
-    uint32_t it = 0;  // blocks so far
-    auto scores = [&](uint32_t i) -> bool {
-        const uint32_t slot = i & 1, full = (i >> 1) & 1;
-        if (!wait(bar(s.b.q_full[slot]), full, &s.dead)) return false;
-        if (!wait(bar(s.b.k_full[slot]), full, &s.dead)) return false;
+    if (!find_unit(L, s, false, x)) return;
+    const int n = __shfl_sync(0xffffffffu, x.n, 0);
+    for (int c = 0; c < n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1, tq = tm + kQ + slot * 64;
+        if (!await(bar(s.b.q_full[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
         fence_after();
-        for (int kk = 0; kk < steps; ++kk)
-            mma_ts(lead, tm + kScores, tm + kQ + slot * 64 + kk * 8,
-                   k_lo + ((slot * kKeyTile + (kk >> 2) * kBox + (kk & 3) * 32) >> 4), idesc(C, false), kk > 0);
+        const uint32_t k = k_lo + slot * (kKeyTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk)
+            mma_ts(lead, tm + kScores, tq + kk * 8, k + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                   idesc(C, false), kk > 0);
         commit(lead, bar(s.b.s_full));
-        return true;
-    };
-    while (next_unit(L, s, !OUT, at, x)) {
-        const int n = __shfl_sync(0xffffffffu, x.n, 0);
-        if (OUT && !scores(it)) return;
-        for (int c = 0; c < n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            // U = K^T W, both terms side by side
-            if (!wait(bar(s.b.k_full[slot]), half, &s.dead)) return;
-            if (!wait(bar(s.b.u_free), (it & 1) ^ 1, &s.dead)) return;
+        commit(lead, bar(s.b.k_empty[slot]));
+        // O2 = Q S
+        if (!await(bar(s.b.st_ready), c & 1, &s.dead)) return;
+        if (!await(bar(s.b.o_free), (c & 1) ^ 1, &s.dead)) return;
+        fence_after();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {  // 32 rows at a time, as their warp has them ready
-                if (!wait(bar(s.b.w_ready[slot][b]), half, &s.dead)) return;
-                fence_after();
+        for (int kk = 0; kk < DK / 16; ++kk)
+            mma_ts(lead, tm + kO2, tq + kk * 8, s_lo + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
+        commit(lead, bar(s.b.st_free));
+        // O1 = P V
+        if (!await(bar(s.b.p_ready), c & 1, &s.dead)) return;
+        // (rows past the end are 0 by now)
+        if (c + 1 == n && !await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
+        fence_after();
+        const uint32_t v = v_lo + slot * (kBox >> 4);
 #pragma unroll
-                for (int kk = 2 * b; kk < 2 * b + 2; ++kk)
-                    mma_ss(lead, tm + kU, kt_lo + ((slot * kKeyTile + kk * 2048) >> 4),
-                           w_lo + ((slot * kWTile + kk * 2048) >> 4), idesc(2 * NV, true, true), kk > 0);
-                commit(lead, bar(s.b.w_free[slot][b]));
-            }
-            commit(lead, bar(s.b.u_full));
-            commit(lead, bar(s.b.k_empty[slot]));
-            if (!OUT) {
-                commit(lead, bar(s.b.v_empty[slot]));
-                continue;
-            }
-            // O2 = Q S
-            if (!wait(bar(s.b.st_ready), it & 1, &s.dead)) return;
-            if (!wait(bar(s.b.o_free), (it & 1) ^ 1, &s.dead)) return;
-            fence_after();
-            for (int kk = 0; kk < steps; ++kk)
-                mma_ts(lead, tm + kO2, tm + kQ + slot * 64 + kk * 8, s_lo + ((kk * 2048) >> 4), idesc(NV, true),
-                       kk > 0);
-            commit(lead, bar(s.b.st_free));
-            // O1 = P V
-            if (!wait(bar(s.b.p_ready), it & 1, &s.dead)) return;
-            fence_after();
+        for (int kk = 0; kk < C / 16; ++kk)
+            mma_ts(lead, tm + kO1, tm + kScores + kk * 8, v + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
+        commit(lead, bar(s.b.o_full));
+        commit(lead, bar(s.b.v_empty[slot]));
+    }
+}
+
+// U = K^T W, both terms side by side.
+template <bool OUT>
+__device__ __forceinline__ void update_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm) {
+    const uint32_t lead = elect(), kt_lo = desc_lo(t.k, kBox), w_lo = desc_lo(t.w, kBox);
+    Unit x;
+    if (!find_unit(L, s, !OUT, x)) return;
+    const int n = __shfl_sync(0xffffffffu, x.n, 0);
+    for (int c = 0; c < n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.u_free), (c & 1) ^ 1, &s.dead)) return;
+        fence_after();
+        const uint32_t k = kt_lo + slot * (kKeyTile >> 4), w = w_lo + slot * (kWTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-                mma_ts(lead, tm + kO1, tm + kScores + kk * 8, v_lo + ((slot * kBox + kk * 2048) >> 4),
-                       idesc(NV, true), kk > 0);
-            commit(lead, bar(s.b.o_full));
-            commit(lead, bar(s.b.v_empty[slot]));
-            if (c + 1 < n && !scores(it + 1)) return;
-        }
+        for (int kk = 0; kk < C / 16; ++kk)
+            mma_ss(lead, tm + kU, k + ((kk * 2048) >> 4), w + ((kk * 2048) >> 4), idesc(2 * NV, true, true),
+                   kk > 0);
+        commit(lead, bar(s.b.u_full));
+        commit(lead, bar(s.b.w_free[slot]));
+        commit(lead, bar(s.b.k_empty[slot]));
     }
 }
 
@@ -292,99 +291,96 @@ template <bool OUT>
 __device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane) {
     const gdn_linear &g = L.a.g;
     const int b = lane >> 3, l = lane & 7;  // this lane's rows: 4 lane to 4 lane + 3, of the 32 that are b
-    long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0;
     float next[4];
-    while (next_unit(L, s, !OUT, at, x)) {
-        auto load = [&](int c) {  // 0 for rows past the end
+    if (!find_unit(L, s, !OUT, x)) return;
+    auto load = [&](int c) {  // 0 for rows past the end
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int row = c * C + 4 * lane + k;
-                next[k] = row < x.u.T ? __ldg(g.log_decay + (x.u.row0 + (long long)row) * g.decay_stride + x.h) : 0.f;
-            }
-        };
-        load(0);
-        for (int c = 0; c < x.n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            const int n = min(C, x.u.T - c * C);
-            const float gl[4] = {next[0], next[1], next[2], next[3]};
-            if (c + 1 < x.n) load(c + 1);
-            // Sums within the 32: from its start up to each row, and from behind it to the end.
-            float upto[4] = {gl[0], gl[0] + gl[1], 0.f, 0.f}, after[4] = {0.f, 0.f, gl[3], 0.f};
-            upto[2] = upto[1] + gl[2];
-            upto[3] = upto[2] + gl[3];
-            after[1] = after[2] + gl[2];
-            after[0] = after[1] + gl[1];
-            float below = upto[3], above = upto[3];
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, below, d, 8);
-                const float z = __shfl_down_sync(0xffffffffu, above, d, 8);
-                if (l >= d) below += y;
-                if (l + d < 8) above += z;
-            }
-            const float total = __shfl_sync(0xffffffffu, below, lane | 7);
-            below = __shfl_up_sync(0xffffffffu, below, 1, 8);
-            above = __shfl_down_sync(0xffffffffu, above, 1, 8);
-            if (l == 0) below = 0.f;
-            if (l == 7) above = 0.f;
-            bool mild = true;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                upto[k] += below;
-                after[k] += above;
-                mild = mild && fabsf(upto[k]) < kSteep;  // (false for NaN)
-            }
-            const unsigned steep = ~__ballot_sync(0xffffffffu, mild);
-            const bool steep_here = (steep >> (8 * b) & 0xFFu) != 0;
-            const float whole = expf(total);
-            float t[4];  // of the four 32s
-#pragma unroll
-            for (int m = 0; m < 4; ++m) t[m] = __shfl_sync(0xffffffffu, whole, 8 * m);
-            if (!wait(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
-            Shared::Decays &d = s.dec[slot];
-            float row[4], col[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                row[k] = expf(upto[k]);
-                col[k] = expf(after[k]);
-            }
-            auto put = [&](float *to, float w, float x, float y, float z) {
-                *reinterpret_cast<float4 *>(to + 4 * lane) = make_float4(w, x, y, z);
-            };
-            float f = 1.f;
-#pragma unroll
-            for (int m = 1; m < 4; ++m) {
-                if (m <= b) continue;  // the rows of earlier 32s do not see this one
-                if (OUT) put(d.column[m], f * col[0], f * col[1], f * col[2], f * col[3]);
-                f *= t[m];
-            }
-            const int i = 4 * lane;
-            put(d.weight, i < n ? f * col[0] : 0.f, i + 1 < n ? f * col[1] : 0.f, i + 2 < n ? f * col[2] : 0.f,
-                i + 3 < n ? f * col[3] : 0.f);
-            if (OUT) {
-                put(d.column[b], expf(-upto[0]), expf(-upto[1]), expf(-upto[2]), expf(-upto[3]));
-                float e = g.scale;
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    if (m < b) e *= t[m];
-                put(d.o2, e * row[0], e * row[1], e * row[2], e * row[3]);
-                if (steep_here) {
-                    put(d.log, gl[0], gl[1], gl[2], gl[3]);
-                    put(d.row, row[0], row[1], row[2], row[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) row[k] = 1.f;
-                }
-                put(d.o1, g.scale * row[0], g.scale * row[1], g.scale * row[2], g.scale * row[3]);
-            }
-            if (lane == 0) {
-                d.keep = t[0] * t[1] * (t[2] * t[3]);
-                d.steep = ((steep & 0xFFu) != 0) | ((steep >> 8 & 0xFFu) != 0) << 1 |
-                          ((steep >> 16 & 0xFFu) != 0) << 2 | ((steep >> 24) != 0) << 3;
-            }
-            arrive_warp(bar(s.b.dec_full[slot]));
+        for (int k = 0; k < 4; ++k) {
+            const int row = c * C + 4 * lane + k;
+            next[k] = row < x.u.T ? __ldg(g.log_decay + (x.u.row0 + (long long)row) * g.decay_stride + x.h) : 0.f;
         }
+    };
+    load(0);
+    for (int c = 0; c < x.n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        const int n = min(C, x.u.T - c * C);
+        const float gl[4] = {next[0], next[1], next[2], next[3]};
+        if (c + 1 < x.n) load(c + 1);
+        // Sums within the 32: from its start up to each row, and from behind it to the end.
+        float upto[4] = {gl[0], gl[0] + gl[1], 0.f, 0.f}, after[4] = {0.f, 0.f, gl[3], 0.f};
+        upto[2] = upto[1] + gl[2];
+        upto[3] = upto[2] + gl[3];
+        after[1] = after[2] + gl[2];
+        after[0] = after[1] + gl[1];
+        float below = upto[3], above = upto[3];
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, below, d, 8);
+            const float z = __shfl_down_sync(0xffffffffu, above, d, 8);
+            if (l >= d) below += y;
+            if (l + d < 8) above += z;
+        }
+        const float total = __shfl_sync(0xffffffffu, below, lane | 7);
+        below = __shfl_up_sync(0xffffffffu, below, 1, 8);
+        above = __shfl_down_sync(0xffffffffu, above, 1, 8);
+        if (l == 0) below = 0.f;
+        if (l == 7) above = 0.f;
+        bool mild = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            upto[k] += below;
+            after[k] += above;
+            mild = mild && fabsf(upto[k]) < kSteep;  // (false for NaN)
+        }
+        const unsigned steep = ~__ballot_sync(0xffffffffu, mild);
+        const bool steep_here = (steep >> (8 * b) & 0xFFu) != 0;
+        const float whole = expf(total);
+        float t[4];  // of the four 32s
+#pragma unroll
+        for (int m = 0; m < 4; ++m) t[m] = __shfl_sync(0xffffffffu, whole, 8 * m);
+        if (!await(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
+        Shared::Decays &d = s.dec[slot];
+        float row[4], col[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            row[k] = expf(upto[k]);
+            col[k] = expf(after[k]);
+        }
+        auto put = [&](float *to, float w, float x, float y, float z) {
+            *reinterpret_cast<float4 *>(to + 4 * lane) = make_float4(w, x, y, z);
+        };
+        float f = 1.f;
+#pragma unroll
+        for (int m = 1; m < 4; ++m) {
+            if (m <= b) continue;  // the rows of earlier 32s do not see this one
+            if (OUT) put(d.column[m], f * col[0], f * col[1], f * col[2], f * col[3]);
+            f *= t[m];
+        }
+        const int i = 4 * lane;
+        put(d.weight, i < n ? f * col[0] : 0.f, i + 1 < n ? f * col[1] : 0.f, i + 2 < n ? f * col[2] : 0.f,
+            i + 3 < n ? f * col[3] : 0.f);
+        if (OUT) {
+            put(d.column[b], expf(-upto[0]), expf(-upto[1]), expf(-upto[2]), expf(-upto[3]));
+            float e = g.scale;
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                if (m < b) e *= t[m];
+            put(d.o2, e * row[0], e * row[1], e * row[2], e * row[3]);
+            if (steep_here) {
+                put(d.log, gl[0], gl[1], gl[2], gl[3]);
+                put(d.row, row[0], row[1], row[2], row[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) row[k] = 1.f;
+            }
+            put(d.o1, g.scale * row[0], g.scale * row[1], g.scale * row[2], g.scale * row[3]);
+        }
+        if (lane == 0) {
+            d.keep = t[0] * t[1] * (t[2] * t[3]);
+            d.steep = ((steep & 0xFFu) != 0) | ((steep >> 8 & 0xFFu) != 0) << 1 |
+                      ((steep >> 16 & 0xFFu) != 0) << 2 | ((steep >> 24) != 0) << 3;
+        }
+        arrive_warp(bar(s.b.dec_full[slot]));
     }
 }
 
@@ -393,54 +389,51 @@ __device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane)
 template <bool OUT>
 __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Tiles &t, int j) {
     const gdn_linear &g = L.a.g;
-    const int b = j >> 5;
-    long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0;
-    while (next_unit(L, s, !OUT, at, x)) {
-        for (int c = 0; c < x.n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            const int n = min(C, x.u.T - c * C);
-            if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            const float w = s.dec[slot].weight[j];
-            arrive_warp(bar(s.b.dec_empty[slot]));
-            if (!wait(bar(s.b.v_full[slot]), half, &s.dead)) return;
-            const uint32_t vt = t.v + slot * kBox;
-            const uint32_t zero[4] = {0, 0, 0, 0};
-            if (n < C) {  // rows of other requests, whatever they hold, count as 0
-                if (!wait(bar(s.b.k_full[slot]), half, &s.dead)) return;
-                if (j >= n) {
-                    for (int e = 0; e < 8; ++e) {
-                        sts128(chunk(vt, j, e), zero);
-                        for (int box = 0; box < g.dk / 64; ++box)
-                            sts128(chunk(t.k + slot * kKeyTile + box * kBox, j, e), zero);
-                    }
+    if (!find_unit(L, s, !OUT, x)) return;
+    for (int c = 0; c < x.n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        const int n = min(C, x.u.T - c * C);
+        if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+        const float w = s.dec[slot].weight[j];
+        arrive_warp(bar(s.b.dec_empty[slot]));
+        if (!await(bar(s.b.v_full[slot]), half, &s.dead)) return;
+        const uint32_t vt = t.v + slot * kBox;
+        const uint32_t zero[4] = {0, 0, 0, 0};
+        if (n < C) {  // rows of other requests, whatever they hold, count as 0
+            if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
+            if (j >= n) {
+                for (int e = 0; e < 8; ++e) {
+                    sts128(chunk(vt, j, e), zero);
+                    for (int box = 0; box < g.dk / 64; ++box)
+                        sts128(chunk(t.k + slot * kKeyTile + box * kBox, j, e), zero);
                 }
             }
-            const float2 w2 = make_float2(w, w);
-            uint32_t v8[8][4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lds128(chunk(vt, j, e), v8[e]);
-            if (!wait(bar(s.b.w_free[slot][b]), half ^ 1, &s.dead)) return;
-            const uint32_t wt = t.w + slot * kWTile;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                uint32_t *v = v8[e], hi[4], lo[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float2 y = mul2(make_float2(__uint_as_float(v[m] << 16),
-                                                      __uint_as_float(v[m] & 0xFFFF0000u)), w2);
-                    hi[m] = pack_bf16(y.x, y.y);
-                    const float2 z = add2(y, make_float2(-__uint_as_float(hi[m] << 16),
-                                                         -__uint_as_float(hi[m] & 0xFFFF0000u)));
-                    lo[m] = pack_bf16(z.x, z.y);
-                }
-                sts128(chunk(wt, j, e), hi);
-                sts128(chunk(wt + kBox, j, e), lo);
-            }
-            fence_async();
-            arrive_warp(bar(s.b.w_ready[slot][b]));
         }
+        const float2 w2 = make_float2(w, w);
+        uint32_t v8[8][4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lds128(chunk(vt, j, e), v8[e]);
+        arrive_warp(bar(s.b.v_empty[slot]));
+        if (!await(bar(s.b.w_free[slot]), half ^ 1, &s.dead)) return;
+        const uint32_t wt = t.w + slot * kWTile;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t *v = v8[e], hi[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 y = mul2(make_float2(__uint_as_float(v[m] << 16),
+                                                  __uint_as_float(v[m] & 0xFFFF0000u)), w2);
+                hi[m] = pack_bf16(y.x, y.y);
+                const float2 z = add2(y, make_float2(-__uint_as_float(hi[m] << 16),
+                                                     -__uint_as_float(hi[m] & 0xFFFF0000u)));
+                lo[m] = pack_bf16(z.x, z.y);
+            }
+            sts128(chunk(wt, j, e), hi);
+            sts128(chunk(wt + kBox, j, e), lo);
+        }
+        fence_async();
+        arrive_warp(bar(s.b.w_ready[slot]));
     }
 }
 
@@ -477,53 +470,50 @@ __device__ __noinline__ void mask_steep(const Shared::Decays &d, uint32_t ts, in
 __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t tm, int i) {
     const int lane = i & 31, b = i >> 5;
     const uint32_t ts = tm + kScores + ((uint32_t)b << 21);  // this warp's lanes
-    long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0;
-    while (next_unit(L, s, false, at, x)) {
-        for (int c = 0; c < x.n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            const Shared::Decays &d = s.dec[slot];
-            if (!wait(bar(s.b.s_full), it & 1, &s.dead)) return;
-            fence_after();
-            if (d.steep >> b & 1) {
-                mask_steep(d, ts, lane, b);
-            } else {
+    if (!find_unit(L, s, false, x)) return;
+    for (int c = 0; c < x.n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+        const Shared::Decays &d = s.dec[slot];
+        if (!await(bar(s.b.s_full), c & 1, &s.dead)) return;
+        fence_after();
+        if (d.steep >> b & 1) {
+            mask_steep(d, ts, lane, b);
+        } else {
 #pragma unroll 1
-                for (int m = 0; m <= b; ++m) {
-                    uint32_t y[32];
-                    tmem_ld32(ts + 32 * m, y);
-                    const float *column = d.column[b] + 32 * m;
-                    wait_ld();
+            for (int m = 0; m <= b; ++m) {
+                uint32_t y[32];
+                tmem_ld32(ts + 32 * m, y);
+                const float *column = d.column[b] + 32 * m;
+                wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(column + e);
-                        const float2 p0 = mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
-                                               make_float2(w.x, w.y));
-                        const float2 p1 = mul2(make_float2(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])),
-                                               make_float2(w.z, w.w));
-                        y[e / 2] = pack_bf16(p0.x, p0.y);
-                        y[e / 2 + 1] = pack_bf16(p1.x, p1.y);
-                    }
-                    if (m == b) {  // its own 32: up to itself
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            y[e] &= (2 * e <= lane ? 0xFFFFu : 0u) | (2 * e + 1 <= lane ? 0xFFFF0000u : 0u);
-                    }
-                    tmem_st16(ts + 16 * m, y);  // over scores that have been read
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(column + e);
+                    const float2 p0 = mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                                           make_float2(w.x, w.y));
+                    const float2 p1 = mul2(make_float2(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])),
+                                           make_float2(w.z, w.w));
+                    y[e / 2] = pack_bf16(p0.x, p0.y);
+                    y[e / 2 + 1] = pack_bf16(p1.x, p1.y);
                 }
-            }
-            uint32_t zero[16];
+                if (m == b) {  // its own 32: up to itself
 #pragma unroll
-            for (int e = 0; e < 16; ++e) zero[e] = 0u;
-#pragma unroll 1
-            for (int m = b + 1; m < 4; ++m) tmem_st16(ts + 16 * m, zero);
-            arrive_warp(bar(s.b.dec_empty[slot]));
-            wait_st();
-            fence_before();
-            arrive_warp(bar(s.b.p_ready));
+                    for (int e = 0; e < 16; ++e)
+                        y[e] &= (2 * e <= lane ? 0xFFFFu : 0u) | (2 * e + 1 <= lane ? 0xFFFF0000u : 0u);
+                }
+                tmem_st16(ts + 16 * m, y);  // over scores that have been read
+            }
         }
+        uint32_t zero[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll 1
+        for (int m = b + 1; m < 4; ++m) tmem_st16(ts + 16 * m, zero);
+        arrive_warp(bar(s.b.dec_empty[slot]));
+        wait_st();
+        fence_before();
+        arrive_warp(bar(s.b.p_ready));
     }
 }
 
@@ -533,64 +523,61 @@ template <bool OUT, bool STATE>
 __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm, int d) {
     const gdn_linear &g = L.a.g;
     const uint32_t tu = tm + kU + ((uint32_t)(d >> 5) << 21);
-    long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0;
-    while (next_unit(L, s, !OUT, at, x)) {
-        float *row = x.u.tile + (long long)d * g.dv + x.c0;
-        float S[NV];
+    if (!find_unit(L, s, !OUT, x)) return;
+    float *row = x.u.tile + (long long)d * g.dv + x.c0;
+    float S[NV];
 #pragma unroll
-        for (int e = 0; e < NV; e += 4) {
-            const float4 y = d < g.dk ? __ldcs(reinterpret_cast<const float4 *>(row + e))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[e] = y.x;
-            S[e + 1] = y.y;
-            S[e + 2] = y.z;
-            S[e + 3] = y.w;
-        }
-        for (int c = 0; c < x.n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            if (OUT) {
-                if (!wait(bar(s.b.st_free), (it & 1) ^ 1, &s.dead)) return;
-                if (d < g.dk) {
+    for (int e = 0; e < NV; e += 4) {
+        const float4 y = d < g.dk ? __ldcs(reinterpret_cast<const float4 *>(row + e))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[e] = y.x;
+        S[e + 1] = y.y;
+        S[e + 2] = y.z;
+        S[e + 3] = y.w;
+    }
+    for (int c = 0; c < x.n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        if (OUT) {
+            if (!await(bar(s.b.st_free), (c & 1) ^ 1, &s.dead)) return;
+            if (d < g.dk) {
 #pragma unroll
-                    for (int e = 0; e < NV; e += 8) {
-                        const uint32_t y[4] = {pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]),
-                                               pack_bf16(S[e + 4], S[e + 5]), pack_bf16(S[e + 6], S[e + 7])};
-                        sts128(chunk(t.s, d, e / 8), y);
-                    }
-                }
-                fence_async();
-                arrive_warp(bar(s.b.st_ready));
-            }
-            if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            const float keep = s.dec[slot].keep;
-            arrive_warp(bar(s.b.dec_empty[slot]));
-            if (!wait(bar(s.b.u_full), it & 1, &s.dead)) return;
-            fence_after();
-#pragma unroll
-            for (int e = 0; e < NV; e += 16) {
-                uint32_t y[16], z[16];
-                tmem_ld16(tu + e, y);
-                tmem_ld16(tu + NV + e, z);
-                wait_ld();
-#pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    const float2 u = add2(make_float2(__uint_as_float(y[m]), __uint_as_float(y[m + 1])),
-                                          make_float2(__uint_as_float(z[m]), __uint_as_float(z[m + 1])));
-                    const float2 w = fma2(make_float2(S[e + m], S[e + m + 1]), make_float2(keep, keep), u);
-                    S[e + m] = w.x;
-                    S[e + m + 1] = w.y;
+                for (int e = 0; e < NV; e += 8) {
+                    const uint32_t y[4] = {pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]),
+                                           pack_bf16(S[e + 4], S[e + 5]), pack_bf16(S[e + 6], S[e + 7])};
+                    sts128(chunk(t.s, d, e / 8), y);
                 }
             }
-            fence_before();
-            arrive_warp(bar(s.b.u_free));
+            fence_async();
+            arrive_warp(bar(s.b.st_ready));
         }
-        if (STATE && d < g.dk) {
+        if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+        const float keep = s.dec[slot].keep;
+        arrive_warp(bar(s.b.dec_empty[slot]));
+        if (!await(bar(s.b.u_full), c & 1, &s.dead)) return;
+        fence_after();
 #pragma unroll
-            for (int e = 0; e < NV; e += 4)
-                __stcs(reinterpret_cast<float4 *>(row + e), make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
+        for (int e = 0; e < NV; e += 16) {
+            uint32_t y[16], z[16];
+            tmem_ld16(tu + e, y);
+            tmem_ld16(tu + NV + e, z);
+            wait_ld();
+#pragma unroll
+            for (int m = 0; m < 16; m += 2) {
+                const float2 u = add2(make_float2(__uint_as_float(y[m]), __uint_as_float(y[m + 1])),
+                                      make_float2(__uint_as_float(z[m]), __uint_as_float(z[m + 1])));
+                const float2 w = fma2(make_float2(S[e + m], S[e + m + 1]), make_float2(keep, keep), u);
+                S[e + m] = w.x;
+                S[e + m + 1] = w.y;
+            }
         }
+        fence_before();
+        arrive_warp(bar(s.b.u_free));
+    }
+    if (STATE && d < g.dk) {
+#pragma unroll
+        for (int e = 0; e < NV; e += 4)
+            __stcs(reinterpret_cast<float4 *>(row + e), make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
     }
 }
 
@@ -600,73 +587,70 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, uint32_t
     const gdn_linear &g = L.a.g;
     const int b = i >> 5;
     const uint32_t lanes = (uint32_t)b << 21;
-    long long at = blockIdx.x;
     Unit x;
-    uint32_t it = 0;
-    while (next_unit(L, s, false, at, x)) {
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + (long long)(x.h / L.a.group) * g.dk;
-        // Row i of block c to tensor memory, where block `to`'s are (its scores and O2 have been computed).
-        auto queries = [&](int c, uint32_t to) {
-            const int row = c * C + i;
-            const bool has = row < x.u.T;
-            const __nv_bfloat16 *src = q + (x.u.row0 + (long long)row) * g.q_stride;
-            uint32_t y[64];
+    if (!find_unit(L, s, false, x)) return;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + (long long)(x.h / L.a.group) * g.dk;
+    // Row i of block c to tensor memory, where block `to`'s are (its scores and O2 have been computed).
+    auto queries = [&](int c) {
+        const int row = c * C + i;
+        const bool has = row < x.u.T;
+        const __nv_bfloat16 *src = q + (x.u.row0 + (long long)row) * g.q_stride;
+        uint32_t y[64];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) y[e] = 0u;
-            if (has) {
+        for (int e = 0; e < 64; ++e) y[e] = 0u;
+        if (has) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
-                if (g.dk == 128) {
+            for (int e = 0; e < 4; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
+            if (g.dk == 128) {
 #pragma unroll
-                    for (int e = 4; e < 8; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
-                }
+                for (int e = 4; e < 8; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
             }
-            const uint32_t tq = tm + kQ + (to & 1) * 64 + lanes;
-            tmem_st32(tq, y);
-            tmem_st32(tq + 32, y + 32);
-            wait_st();
-            fence_before();
-            arrive_warp(bar(s.b.q_full[to & 1]));
-        };
-        queries(0, it);
-        for (int c = 0; c < x.n; ++c, ++it) {
-            const uint32_t slot = it & 1, half = (it >> 1) & 1;
-            const int n = min(C, x.u.T - c * C);
-            if (c + kAhead < x.n) {  // whole rows to come: into L2
-                const long long row = x.u.row0 + (long long)(c + kAhead) * C + i;
-                if ((c + kAhead) * C + i < x.u.T)
-                    for (int e = 0; e < g.dk; e += 64)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + row * g.q_stride + e));
+        }
+        const uint32_t tq = tm + kQ + (c & 1) * 64 + lanes;
+        tmem_st32(tq, y);
+        tmem_st32(tq + 32, y + 32);
+        wait_st();
+        fence_before();
+        arrive_warp(bar(s.b.q_full[c & 1]));
+    };
+    queries(0);
+    for (int c = 0; c < x.n; ++c) {
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
+        const int n = min(C, x.u.T - c * C);
+        if (c + kAhead < x.n) {  // whole rows to come: into L2
+            const long long row = x.u.row0 + (long long)(c + kAhead) * C + i;
+            if ((c + kAhead) * C + i < x.u.T)
+                for (int e = 0; e < g.dk; e += 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q + row * g.q_stride + e));
+        }
+        if (c + 1 < x.n) queries(c + 1);
+        if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
+        const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
+        arrive_warp(bar(s.b.dec_empty[slot]));
+        if (!await(bar(s.b.o_full), c & 1, &s.dead)) return;
+        fence_after();
+        const float2 f2 = make_float2(f, f), scale2 = make_float2(f1, f1);
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) +
+                           (x.u.row0 + (long long)c * C + i) * g.heads * g.dv + x.h * g.dv + x.c0;
+#pragma unroll
+        for (int h = 0; h < NV; h += 32) {
+            uint32_t y[32], z[32];
+            tmem_ld32(tm + kO1 + lanes + h, y);
+            tmem_ld32(tm + kO2 + lanes + h, z);
+            wait_ld();
+            if (h + 32 == NV) {
+                fence_before();
+                arrive_warp(bar(s.b.o_free));
             }
-            if (c + 1 < x.n) queries(c + 1, it + 1);
-            if (!wait(bar(s.b.dec_full[slot]), half, &s.dead)) return;
-            const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
-            arrive_warp(bar(s.b.dec_empty[slot]));
-            if (!wait(bar(s.b.o_full), it & 1, &s.dead)) return;
-            fence_after();
-            const float2 f2 = make_float2(f, f), scale2 = make_float2(f1, f1);
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(L.a.o) +
-                               (x.u.row0 + (long long)c * C + i) * g.heads * g.dv + x.h * g.dv + x.c0;
 #pragma unroll
-            for (int h = 0; h < NV; h += 32) {
-                uint32_t y[32], z[32];
-                tmem_ld32(tm + kO1 + lanes + h, y);
-                tmem_ld32(tm + kO2 + lanes + h, z);
-                wait_ld();
-                if (h + 32 == NV) {
-                    fence_before();
-                    arrive_warp(bar(s.b.o_free));
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 p = fma2(make_float2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), f2,
-                                          mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale2));
-                    y[e / 2] = pack_bf16(p.x, p.y);
-                }
-                if (i < n) {  // whole sectors: 32 bytes of a row at a time
-                    stg32(o + h, L.o32, y);
-                    stg32(o + h + 16, L.o32, y + 8);
-                }
+            for (int e = 0; e < 32; e += 2) {
+                const float2 p = fma2(make_float2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), f2,
+                                      mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale2));
+                y[e / 2] = pack_bf16(p.x, p.y);
+            }
+            if (i < n) {  // whole sectors: 32 bytes of a row at a time
+                stg32(o + h, L.o32, y);
+                stg32(o + h + 16, L.o32, y + 8);
             }
         }
     }
@@ -687,16 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(bar(s.b.q_full[i]), 4);
             mbar_init(bar(s.b.k_full[i]), 1);
             mbar_init(bar(s.b.v_full[i]), 1);
-            mbar_init(bar(s.b.k_empty[i]), 1);
-            mbar_init(bar(s.b.v_empty[i]), 1);
+            mbar_init(bar(s.b.k_empty[i]), OUT ? 2 : 1);
+            mbar_init(bar(s.b.w_ready[i]), 4);
+            mbar_init(bar(s.b.w_free[i]), 1);
+            mbar_init(bar(s.b.v_empty[i]), OUT ? 5 : 4);
             mbar_init(bar(s.b.dec_full[i]), 1);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
-        }
-        for (int i = 0; i < 4; ++i) {
-            for (int k = 0; k < 2; ++k) {
-                mbar_init(bar(s.b.w_ready[k][i]), 1);
-                mbar_init(bar(s.b.w_free[k][i]), 1);
-            }
         }
         mbar_init(bar(s.b.s_full), 1);
         mbar_init(bar(s.b.p_ready), 4);
@@ -706,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(bar(s.b.st_free), 1);
         mbar_init(bar(s.b.o_full), 1);
         mbar_init(bar(s.b.o_free), 4);
-        mbar_init(bar(s.b.drain), 1);
+        mbar_init(bar(s.b.drain), OUT ? 2 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s.dead = 0;
     }
@@ -754,8 +734,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             }
         }
     } else {
-        mma_role<OUT>(L, s, t, tm);
-        commit(elect(), bar(s.b.drain));
+        if (warp == 19) {
+            update_role<OUT>(L, s, t, tm);
+        } else if (OUT) {
+            if (L.a.g.dk == 128)
+                mma_role<128>(L, s, t, tm);
+            else
+                mma_role<64>(L, s, t, tm);
+        }
+        if (OUT || warp == 19) commit(elect(), bar(s.b.drain));
         wait_parity(bar(s.b.drain), 0);
     }
     __syncwarp();
