@@ -8,7 +8,7 @@
 //     U  = K^T W,  W_j = d(C - 1, j) v_j                     S <- e^{G_(C-1)} S + U
 // Only S goes from block to block: everything else runs ahead of it, in roles that
 // hand on through barriers:
-//   TMA warp     K and V tiles, two blocks ahead (128-byte swizzle)
+//   TMA warp     Q, K and V tiles, ahead of their use (128-byte swizzle)
 //   MMA warps    U; the other three products
 //   decays       (a warp, four rows a lane) see below
 //   weights      (warpgroup, a thread a row) W in two bf16 terms: each product v_j d enters its state
@@ -41,13 +41,13 @@ constexpr int kThreads = 20 * 32;    // weights, mask, state, output; TMA, MMA, 
 constexpr float kSteep = 60.f;
 constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
-constexpr int kTiles = 2 * kKeyTile + 2 * kBox + 2 * kWTile + kBox;  // K, V and W twice; S
+constexpr int kTiles = 3 * kKeyTile + 2 * kBox + 2 * kWTile + kBox;  // K, V and W twice; Q, S
 
 // Columns of tensor memory.
 constexpr uint32_t kScores = 0, kQ = 128, kO1 = 256, kO2 = 320, kU = 384;  // (kU: two terms)
 
 struct Bars {
-    unsigned long long q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    unsigned long long qs_full, qs_empty, q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     unsigned long long dec_full[2], dec_empty[2];
     unsigned long long w_ready[2], w_free[2];
     unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
@@ -72,10 +72,10 @@ static_assert(kTiles + sizeof(Shared) <= 232448, "227 KB of shared memory");
 
 struct Launch {
     LinearArgs a;
-    CUtensorMap k, v;
+    CUtensorMap q, k, v;
     int slices;
     bool sorted;     // ragged requests, longest first
-    bool q32, o32;  // rows are aligned to 32 bytes
+    bool o32;        // rows are aligned to 32 bytes
     long long units;
 };
 
@@ -110,21 +110,7 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int 
                  "r"(x), "r"(y)
                  : "memory");
 }
-// 32 bytes of global memory: at once where they are aligned so (rows are to 16).
-__device__ __forceinline__ void ldg32(const void *at, bool whole, uint32_t *x) {
-    if (whole) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
-                       "=r"(x[7])
-                     : "l"(at));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4)
-            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[e]), "=r"(x[e + 1]), "=r"(x[e + 2]), "=r"(x[e + 3])
-                         : "l"(static_cast<const char *>(at) + 4 * e));
-    }
-}
+// 32 bytes to global memory: at once where they are aligned so (rows are to 16).
 __device__ __forceinline__ void stg32(void *at, bool whole, const uint32_t *x) {
     if (whole) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]),
@@ -185,19 +171,19 @@ __device__ __forceinline__ bool await(uint32_t b, uint32_t parity, int *dead) {
 
 // Shared-memory tiles.
 struct Tiles {
-    uint32_t k, v, w, s;
+    uint32_t k, v, w, s, q;
     __device__ __forceinline__ explicit Tiles(uint32_t base)
-        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + 2 * kWTile) {}
+        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + 2 * kWTile), q(s + kBox) {}
 };
 
 // ---------------------------------------------------------------- the TMA warp (one thread)
 
-__device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tiles &t, bool commit,
-                                          uint32_t &issued) {
+template <bool OUT>
+__device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tiles &t, uint32_t &issued) {
     const gdn_linear &g = L.a.g;
     const int boxes = g.dk / 64;
     Unit x;
-    if (!find_unit(L, s, commit, x)) return;
+    if (!find_unit(L, s, !OUT, x)) return;
     const int kx = x.h / L.a.group * g.dk, vx = x.h * g.dv + x.c0;
     for (int c = 0; c < x.n; ++c, ++issued) {
         const uint32_t slot = issued & 1, free = ((issued >> 1) & 1) ^ 1;
@@ -205,7 +191,15 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tile
         // L2 first, some blocks before: the ring holds two, and memory takes longer than one.
         for (int a = c == 0 ? 1 : kAhead; a <= kAhead && c + a < x.n; ++a) {
             tma_prefetch(&L.v, vx, y + a * C);
-            for (int b = 0; b < boxes; ++b) tma_prefetch(&L.k, kx + 64 * b, y + a * C);
+            for (int b = 0; b < boxes; ++b) {
+                tma_prefetch(&L.k, kx + 64 * b, y + a * C);
+                if (OUT) tma_prefetch(&L.q, kx + 64 * b, y + a * C);
+            }
+        }
+        if (OUT) {
+            if (!wait_one(bar(s.b.qs_empty), (c & 1) ^ 1, &s.dead)) return;
+            arrive_expect(bar(s.b.qs_full), boxes * kBox);
+            for (int b = 0; b < boxes; ++b) tma_load(t.q + b * kBox, &L.q, kx + 64 * b, y, bar(s.b.qs_full));
         }
         if (!wait_one(bar(s.b.k_empty[slot]), free, &s.dead)) return;
         arrive_expect(bar(s.b.k_full[slot]), boxes * kBox);
@@ -583,47 +577,36 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
 
 // ---------------------------------------------------------------- the queries' and output's warpgroup
 
-__device__ __forceinline__ void output_role(const Launch &L, Shared &s, uint32_t tm, int i) {
+__device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm, int i) {
     const gdn_linear &g = L.a.g;
     const int b = i >> 5;
     const uint32_t lanes = (uint32_t)b << 21;
     Unit x;
     if (!find_unit(L, s, false, x)) return;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + (long long)(x.h / L.a.group) * g.dk;
-    // Row i of block c to tensor memory, where block `to`'s are (its scores and O2 have been computed).
-    auto queries = [&](int c) {
-        const int row = c * C + i;
-        const bool has = row < x.u.T;
-        const __nv_bfloat16 *src = q + (x.u.row0 + (long long)row) * g.q_stride;
+    // Row i of block c to tensor memory (where block c - 2's were: its scores and O2 have been computed).
+    auto queries = [&](int c) -> bool {
+        if (!await(bar(s.b.qs_full), c & 1, &s.dead)) return false;
         uint32_t y[64];
-#pragma unroll
-        for (int e = 0; e < 64; ++e) y[e] = 0u;
-        if (has) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
-            if (g.dk == 128) {
-#pragma unroll
-                for (int e = 4; e < 8; ++e) ldg32(src + 16 * e, L.q32, y + 8 * e);
-            }
-        }
         const uint32_t tq = tm + kQ + (c & 1) * 64 + lanes;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lds128(chunk(t.q, i, e), y + 4 * e);
+        if (g.dk == 128) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lds128(chunk(t.q + kBox, i, e), y + 32 + 4 * e);
+            tmem_st32(tq + 32, y + 32);
+        }
         tmem_st32(tq, y);
-        tmem_st32(tq + 32, y + 32);
+        arrive_warp(bar(s.b.qs_empty));
         wait_st();
         fence_before();
         arrive_warp(bar(s.b.q_full[c & 1]));
+        return true;
     };
-    queries(0);
+    if (!queries(0)) return;
     for (int c = 0; c < x.n; ++c) {
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         const int n = min(C, x.u.T - c * C);
-        if (c + kAhead < x.n) {  // whole rows to come: into L2
-            const long long row = x.u.row0 + (long long)(c + kAhead) * C + i;
-            if ((c + kAhead) * C + i < x.u.T)
-                for (int e = 0; e < g.dk; e += 64)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q + row * g.q_stride + e));
-        }
-        if (c + 1 < x.n) queries(c + 1);
+        if (c + 1 < x.n && !queries(c + 1)) return;
         if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
         const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
         arrive_warp(bar(s.b.dec_empty[slot]));
@@ -678,6 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(bar(s.b.dec_full[i]), 1);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
         }
+        mbar_init(bar(s.b.qs_full), 1);
+        mbar_init(bar(s.b.qs_empty), 4);
         mbar_init(bar(s.b.s_full), 1);
         mbar_init(bar(s.b.p_ready), 4);
         mbar_init(bar(s.b.u_full), 1);
@@ -720,17 +705,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     } else if (warp < 12) {
         state_role<OUT, STATE>(L, s, t, tm, tid - 256);
     } else if (warp < 16) {
-        if (OUT) output_role(L, s, tm, tid - 384);
+        if (OUT) output_role(L, s, t, tm, tid - 384);
     } else if (warp == 18) {
         decay_role<OUT>(L, s, tid & 31);
     } else if (warp == 16) {
         if ((tid & 31) == 0) {
             uint32_t issued = 0;
-            load_role(L, s, t, !OUT, issued);
+            load_role<OUT>(L, s, t, issued);
             // Every copy has landed before the block ends (its roles waited for them unless one gave up).
             for (uint32_t p = issued > 2 ? issued - 2 : 0; s.dead && p <= issued; ++p) {
                 wait_parity(bar(s.b.v_full[p & 1]), (p >> 1) & 1);
                 wait_parity(bar(s.b.k_full[p & 1]), (p >> 1) & 1);
+                if (OUT) wait_parity(bar(s.b.qs_full), p & 1);
             }
         }
     } else {
@@ -776,12 +762,12 @@ cudaError_t launch_tc(const LinearArgs &a, cudaStream_t stream) {
     Launch L;
     L.a = a;
     L.slices = g.dv / NV;
-    L.q32 = (reinterpret_cast<uintptr_t>(g.q) & 31) == 0 && g.q_stride % 16 == 0;
     L.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
     L.units = (long long)g.batch * g.heads * L.slices;
     L.sorted = g.cu_seqlens && g.batch > 1 && g.batch <= kSorted && L.units > 152;
     const long long krow = (long long)g.k_heads * g.dk, vrow = (long long)g.heads * g.dv;
-    if (!encoder() || !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
+    if (!encoder() || (MODE != kCommit && !encode_rows(&L.q, g.q, krow, g.n_tok, g.q_stride)) ||
+        !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
         !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride))
         return cudaErrorInvalidValue;
     constexpr int smem = kTiles + (int)sizeof(Shared);
