@@ -72,7 +72,7 @@ static_assert(kTiles + sizeof(Shared) <= 232448, "227 KB of shared memory");
 
 struct Launch {
     LinearArgs a;
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
     int slices;
     bool sorted;     // ragged requests, longest first
     bool o32;        // rows are aligned to 32 bytes
@@ -103,6 +103,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(b)
         : "memory");
 }
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
+                 "cp.async.bulk.commit_group;\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 // Into L2 only.
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
@@ -243,15 +250,14 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         commit(lead, bar(s.b.st_free));
         // O1 = P V
         if (!await(bar(s.b.p_ready), c & 1, &s.dead)) return;
-        // (rows past the end are 0 by now)
-        if (c + 1 == n && !await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
+        // (its values have been read: the output takes their place; past the end they are 0)
+        if (!await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
         fence_after();
         const uint32_t v = v_lo + slot * (kBox >> 4);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
             mma_ts(lead, tm + kO1, tm + kScores + kk * 8, v + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
         commit(lead, bar(s.b.o_full));
-        commit(lead, bar(s.b.v_empty[slot]));
     }
 }
 
@@ -607,6 +613,10 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Ti
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         const int n = min(C, x.u.T - c * C);
         if (c + 1 < x.n && !queries(c + 1)) return;
+        if (c > 0) {  // the last block's output has left
+            if ((i & 31) == 0) tma_stores_read();
+            arrive_warp(bar(s.b.v_empty[slot ^ 1]));
+        }
         if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
         const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
         arrive_warp(bar(s.b.dec_empty[slot]));
@@ -631,10 +641,19 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Ti
                                       mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale2));
                 y[e / 2] = pack_bf16(p.x, p.y);
             }
-            if (i < n) {  // whole sectors: 32 bytes of a row at a time
+            if (n == C) {  // over the values: 32 rows a warp leave by TMA
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sts128(chunk(t.v + slot * kBox, i, h / 8 + e), y + 4 * e);
+            } else if (i < n) {  // whole sectors: 32 bytes of a row at a time
                 stg32(o + h, L.o32, y);
                 stg32(o + h + 16, L.o32, y + 8);
             }
+        }
+        if (n == C) {
+            fence_async();
+            __syncwarp();
+            if ((i & 31) == 0)
+                tma_store(&L.o, x.h * g.dv + x.c0, x.u.row0 + c * C + i, t.v + slot * kBox + b * 32 * 128);
         }
     }
 }
@@ -657,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(bar(s.b.k_empty[i]), OUT ? 2 : 1);
             mbar_init(bar(s.b.w_ready[i]), 4);
             mbar_init(bar(s.b.w_free[i]), 1);
-            mbar_init(bar(s.b.v_empty[i]), OUT ? 5 : 4);
+            mbar_init(bar(s.b.v_empty[i]), OUT ? 8 : 4);
             mbar_init(bar(s.b.dec_full[i]), 1);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
         }
@@ -705,7 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     } else if (warp < 12) {
         state_role<OUT, STATE>(L, s, t, tm, tid - 256);
     } else if (warp < 16) {
-        if (OUT) output_role(L, s, t, tm, tid - 384);
+        if (OUT) {
+            output_role(L, s, t, tm, tid - 384);
+            if ((tid & 31) == 0) tma_stores_read();
+        }
     } else if (warp == 18) {
         decay_role<OUT>(L, s, tid & 31);
     } else if (warp == 16) {
@@ -743,12 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 
 // ---------------------------------------------------------------- host side
 
-// Rows of `cols` elements, `stride` apart; boxes of 64 columns by a block's rows.  Rows past the end
-// read as zeros.
-bool encode_rows(CUtensorMap *map, const void *base, long long cols, long long rows, long long stride) {
+// Rows of `cols` elements, `stride` apart; boxes of 64 columns.  Rows past the end read as zeros.
+bool encode_rows(CUtensorMap *map, const void *base, long long cols, long long rows, long long stride,
+                 unsigned box_rows = C) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, C};
+    const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t elem[2] = {1, 1};
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
                      elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -768,7 +790,8 @@ cudaError_t launch_tc(const LinearArgs &a, cudaStream_t stream) {
     const long long krow = (long long)g.k_heads * g.dk, vrow = (long long)g.heads * g.dv;
     if (!encoder() || (MODE != kCommit && !encode_rows(&L.q, g.q, krow, g.n_tok, g.q_stride)) ||
         !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
-        !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride))
+        !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride) ||
+        (MODE != kCommit && !encode_rows(&L.o, a.o, vrow, g.n_tok, vrow, 32)))
         return cudaErrorInvalidValue;
     constexpr int smem = kTiles + (int)sizeof(Shared);
     const cudaError_t e = allow_smem<linear_tc_kernel<MODE>>(smem);
