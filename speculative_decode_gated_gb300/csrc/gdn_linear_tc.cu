@@ -15,7 +15,7 @@
 //                to 2^-17 of itself
 //   mask         (a thread a row) scores times decays to P, in tensor memory over the scores
 //   state        (a thread a row of dk) S in registers, its bf16 copy in shared memory for O2
-//   output       (a thread a row) Q to tensor memory, from where both its products take it, and o
+//   output       (a thread a row) o, over the values' tile, from where it leaves by TMA
 //
 // Decays.  With b the 32 rows that row i is one of, and B_b the sum up to its start,
 //     d(i, j) = e^{G_i - B_b} e^{B_b - G_j}:
@@ -41,16 +41,15 @@ constexpr int kThreads = 20 * 32;    // weights, mask, state, output; TMA, MMA, 
 constexpr float kSteep = 60.f;
 constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
-constexpr int kTiles = 3 * kKeyTile + 2 * kBox + 2 * kWTile + kBox;  // K, V and W twice; Q, S
+constexpr int kTiles = 4 * kKeyTile + 2 * kBox + kWTile + kBox;  // Q, K, V twice; W, S
 
 // Columns of tensor memory.
-constexpr uint32_t kScores = 0, kQ = 128, kO1 = 256, kO2 = 320, kU = 384;  // (kU: two terms)
+constexpr uint32_t kScores = 0, kO1 = 256, kO2 = 320, kU = 384;  // (two blocks' scores; U: two terms)
 
 struct Bars {
-    unsigned long long qs_full, qs_empty, q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    unsigned long long dec_full[2], dec_empty[2];
-    unsigned long long w_ready[2], w_free[2];
-    unsigned long long s_full, p_ready, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
+    unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_read[2], v_empty[2];
+    unsigned long long dec_full[2], dec_empty[2], s_full[2], p_ready[2];
+    unsigned long long w_ready, w_free, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
 };
 
 struct Shared {
@@ -180,7 +179,7 @@ __device__ __forceinline__ bool await(uint32_t b, uint32_t parity, int *dead) {
 struct Tiles {
     uint32_t k, v, w, s, q;
     __device__ __forceinline__ explicit Tiles(uint32_t base)
-        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + 2 * kWTile), q(s + kBox) {}
+        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + kWTile), q(s + kBox) {}
 };
 
 // ---------------------------------------------------------------- the TMA warp (one thread)
@@ -204,9 +203,10 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tile
             }
         }
         if (OUT) {
-            if (!wait_one(bar(s.b.qs_empty), (c & 1) ^ 1, &s.dead)) return;
-            arrive_expect(bar(s.b.qs_full), boxes * kBox);
-            for (int b = 0; b < boxes; ++b) tma_load(t.q + b * kBox, &L.q, kx + 64 * b, y, bar(s.b.qs_full));
+            if (!wait_one(bar(s.b.q_empty[slot]), free, &s.dead)) return;
+            arrive_expect(bar(s.b.q_full[slot]), boxes * kBox);
+            for (int b = 0; b < boxes; ++b)
+                tma_load(t.q + slot * kKeyTile + b * kBox, &L.q, kx + 64 * b, y, bar(s.b.q_full[slot]));
         }
         if (!wait_one(bar(s.b.k_empty[slot]), free, &s.dead)) return;
         arrive_expect(bar(s.b.k_full[slot]), boxes * kBox);
@@ -220,43 +220,52 @@ __device__ __forceinline__ void load_role(const Launch &L, Shared &s, const Tile
 
 // ---------------------------------------------------------------- the MMA warps
 
-// Scores, Q S and P V.  Every wait and every instruction of these two warps is on the way from block
-// to block, so U, which waits on other roles, has a warp of its own, and both are short.
+// Scores, Q S and P V.  The scores run a block ahead, so that the mask's way from scores to P is on no
+// chain from block to block; U, which waits on other roles, is issued by a warp of its own.
 template <int DK>
 __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm) {
-    const uint32_t lead = elect(), k_lo = desc_lo(t.k, 16), v_lo = desc_lo(t.v, kBox), s_lo = desc_lo(t.s, kBox);
+    const uint32_t lead = elect(), q_lo = desc_lo(t.q, 16), k_lo = desc_lo(t.k, 16), v_lo = desc_lo(t.v, kBox),
+                   s_lo = desc_lo(t.s, kBox);
     Unit x;
     if (!find_unit(L, s, false, x)) return;
     const int n = __shfl_sync(0xffffffffu, x.n, 0);
-    for (int c = 0; c < n; ++c) {
-        const uint32_t slot = c & 1, half = (c >> 1) & 1, tq = tm + kQ + slot * 64;
-        if (!await(bar(s.b.q_full[slot]), half, &s.dead)) return;
-        if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
-        fence_after();
-        const uint32_t k = k_lo + slot * (kKeyTile >> 4);
+    for (int c = -1; c < n; ++c) {
+        if (c + 1 < n) {  // (P of block c - 1 was there: its product was issued before)
+            const uint32_t slot = (c + 1) & 1, half = ((c + 1) >> 1) & 1;
+            if (!await(bar(s.b.q_full[slot]), half, &s.dead)) return;
+            if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
+            fence_after();
+            const uint32_t at = slot * (kKeyTile >> 4), to = tm + kScores + slot * C;
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
-            mma_ts(lead, tm + kScores, tq + kk * 8, k + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
-                   idesc(C, false), kk > 0);
-        commit(lead, bar(s.b.s_full));
-        commit(lead, bar(s.b.k_empty[slot]));
+            for (int kk = 0; kk < DK / 16; ++kk) {
+                const uint32_t step = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+                mma_ss(lead, to, q_lo + at + step, k_lo + at + step, idesc(C, false), kk > 0);
+            }
+            commit(lead, bar(s.b.s_full[slot]));
+            commit(lead, bar(s.b.k_empty[slot]));
+        }
+        if (c < 0) continue;
+        const uint32_t slot = c & 1, half = (c >> 1) & 1;
         // O2 = Q S
         if (!await(bar(s.b.st_ready), c & 1, &s.dead)) return;
         if (!await(bar(s.b.o_free), (c & 1) ^ 1, &s.dead)) return;
         fence_after();
+        const uint32_t q = q_lo + slot * (kKeyTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk)
-            mma_ts(lead, tm + kO2, tq + kk * 8, s_lo + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
+            mma_ss(lead, tm + kO2, q + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), s_lo + ((kk * 2048) >> 4),
+                   idesc(NV, true), kk > 0);
         commit(lead, bar(s.b.st_free));
+        commit(lead, bar(s.b.q_empty[slot]));
         // O1 = P V
-        if (!await(bar(s.b.p_ready), c & 1, &s.dead)) return;
+        if (!await(bar(s.b.p_ready[slot]), half, &s.dead)) return;
         // (its values have been read: the output takes their place; past the end they are 0)
-        if (!await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.v_read[slot]), half, &s.dead)) return;
         fence_after();
         const uint32_t v = v_lo + slot * (kBox >> 4);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-            mma_ts(lead, tm + kO1, tm + kScores + kk * 8, v + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
+            mma_ts(lead, tm + kO1, tm + kScores + slot * C + kk * 8, v + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
         commit(lead, bar(s.b.o_full));
     }
 }
@@ -271,16 +280,16 @@ __device__ __forceinline__ void update_role(const Launch &L, Shared &s, const Ti
     for (int c = 0; c < n; ++c) {
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         if (!await(bar(s.b.k_full[slot]), half, &s.dead)) return;
-        if (!await(bar(s.b.w_ready[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.w_ready), c & 1, &s.dead)) return;
         if (!await(bar(s.b.u_free), (c & 1) ^ 1, &s.dead)) return;
         fence_after();
-        const uint32_t k = kt_lo + slot * (kKeyTile >> 4), w = w_lo + slot * (kWTile >> 4);
+        const uint32_t k = kt_lo + slot * (kKeyTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-            mma_ss(lead, tm + kU, k + ((kk * 2048) >> 4), w + ((kk * 2048) >> 4), idesc(2 * NV, true, true),
+            mma_ss(lead, tm + kU, k + ((kk * 2048) >> 4), w_lo + ((kk * 2048) >> 4), idesc(2 * NV, true, true),
                    kk > 0);
         commit(lead, bar(s.b.u_full));
-        commit(lead, bar(s.b.w_free[slot]));
+        commit(lead, bar(s.b.w_free));
         commit(lead, bar(s.b.k_empty[slot]));
     }
 }
@@ -414,9 +423,9 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
         uint32_t v8[8][4];
 #pragma unroll
         for (int e = 0; e < 8; ++e) lds128(chunk(vt, j, e), v8[e]);
-        arrive_warp(bar(s.b.v_empty[slot]));
-        if (!await(bar(s.b.w_free[slot]), half ^ 1, &s.dead)) return;
-        const uint32_t wt = t.w + slot * kWTile;
+        if (OUT && n < C) fence_async();
+        arrive_warp(bar(OUT ? s.b.v_read[slot] : s.b.v_empty[slot]));
+        if (!await(bar(s.b.w_free), (c & 1) ^ 1, &s.dead)) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             uint32_t *v = v8[e], hi[4], lo[4];
@@ -429,11 +438,11 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
                                                      -__uint_as_float(hi[m] & 0xFFFF0000u)));
                 lo[m] = pack_bf16(z.x, z.y);
             }
-            sts128(chunk(wt, j, e), hi);
-            sts128(chunk(wt + kBox, j, e), lo);
+            sts128(chunk(t.w, j, e), hi);
+            sts128(chunk(t.w + kBox, j, e), lo);
         }
         fence_async();
-        arrive_warp(bar(s.b.w_ready[slot]));
+        arrive_warp(bar(s.b.w_ready));
     }
 }
 
@@ -469,14 +478,14 @@ __device__ __noinline__ void mask_steep(const Shared::Decays &d, uint32_t ts, in
 
 __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t tm, int i) {
     const int lane = i & 31, b = i >> 5;
-    const uint32_t ts = tm + kScores + ((uint32_t)b << 21);  // this warp's lanes
     Unit x;
     if (!find_unit(L, s, false, x)) return;
     for (int c = 0; c < x.n; ++c) {
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
         const Shared::Decays &d = s.dec[slot];
-        if (!await(bar(s.b.s_full), c & 1, &s.dead)) return;
+        if (!await(bar(s.b.s_full[slot]), half, &s.dead)) return;
+        const uint32_t ts = tm + kScores + slot * C + ((uint32_t)b << 21);  // this warp's lanes
         fence_after();
         if (d.steep >> b & 1) {
             mask_steep(d, ts, lane, b);
@@ -513,7 +522,7 @@ __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t t
         arrive_warp(bar(s.b.dec_empty[slot]));
         wait_st();
         fence_before();
-        arrive_warp(bar(s.b.p_ready));
+        arrive_warp(bar(s.b.p_ready[slot]));
     }
 }
 
@@ -589,30 +598,9 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Ti
     const uint32_t lanes = (uint32_t)b << 21;
     Unit x;
     if (!find_unit(L, s, false, x)) return;
-    // Row i of block c to tensor memory (where block c - 2's were: its scores and O2 have been computed).
-    auto queries = [&](int c) -> bool {
-        if (!await(bar(s.b.qs_full), c & 1, &s.dead)) return false;
-        uint32_t y[64];
-        const uint32_t tq = tm + kQ + (c & 1) * 64 + lanes;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) lds128(chunk(t.q, i, e), y + 4 * e);
-        if (g.dk == 128) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lds128(chunk(t.q + kBox, i, e), y + 32 + 4 * e);
-            tmem_st32(tq + 32, y + 32);
-        }
-        tmem_st32(tq, y);
-        arrive_warp(bar(s.b.qs_empty));
-        wait_st();
-        fence_before();
-        arrive_warp(bar(s.b.q_full[c & 1]));
-        return true;
-    };
-    if (!queries(0)) return;
     for (int c = 0; c < x.n; ++c) {
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         const int n = min(C, x.u.T - c * C);
-        if (c + 1 < x.n && !queries(c + 1)) return;
         if (c > 0) {  // the last block's output has left
             if ((i & 31) == 0) tma_stores_read();
             arrive_warp(bar(s.b.v_empty[slot ^ 1]));
@@ -670,20 +658,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(s.b.q_full[i]), 4);
+            mbar_init(bar(s.b.q_full[i]), 1);
+            mbar_init(bar(s.b.q_empty[i]), 1);
             mbar_init(bar(s.b.k_full[i]), 1);
-            mbar_init(bar(s.b.v_full[i]), 1);
             mbar_init(bar(s.b.k_empty[i]), OUT ? 2 : 1);
-            mbar_init(bar(s.b.w_ready[i]), 4);
-            mbar_init(bar(s.b.w_free[i]), 1);
-            mbar_init(bar(s.b.v_empty[i]), OUT ? 8 : 4);
+            mbar_init(bar(s.b.v_full[i]), 1);
+            mbar_init(bar(s.b.v_read[i]), 4);
+            mbar_init(bar(s.b.v_empty[i]), 4);
             mbar_init(bar(s.b.dec_full[i]), 1);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
+            mbar_init(bar(s.b.s_full[i]), 1);
+            mbar_init(bar(s.b.p_ready[i]), 4);
         }
-        mbar_init(bar(s.b.qs_full), 1);
-        mbar_init(bar(s.b.qs_empty), 4);
-        mbar_init(bar(s.b.s_full), 1);
-        mbar_init(bar(s.b.p_ready), 4);
+        mbar_init(bar(s.b.w_ready), 4);
+        mbar_init(bar(s.b.w_free), 1);
         mbar_init(bar(s.b.u_full), 1);
         mbar_init(bar(s.b.u_free), 4);
         mbar_init(bar(s.b.st_ready), 4);
@@ -738,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             for (uint32_t p = issued > 2 ? issued - 2 : 0; s.dead && p <= issued; ++p) {
                 wait_parity(bar(s.b.v_full[p & 1]), (p >> 1) & 1);
                 wait_parity(bar(s.b.k_full[p & 1]), (p >> 1) & 1);
-                if (OUT) wait_parity(bar(s.b.qs_full), p & 1);
+                if (OUT) wait_parity(bar(s.b.q_full[p & 1]), (p >> 1) & 1);
             }
         }
     } else {
