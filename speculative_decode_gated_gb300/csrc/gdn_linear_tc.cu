@@ -15,7 +15,7 @@
 //                to 2^-17 of itself
 //   mask         (a thread a row) scores times decays to P, in tensor memory over the scores
 //   state        (a thread a row of dk) S in registers, its bf16 copy in shared memory for O2
-//   output       (a thread a row) o, over the values' tile, from where it leaves by TMA
+//   output       (a thread a row) o, which leaves by TMA
 //
 // Decays.  With b the 32 rows that row i is one of, and B_b the sum up to its start,
 //     d(i, j) = e^{G_i - B_b} e^{B_b - G_j}:
@@ -36,18 +36,19 @@ constexpr int C = 128;               // rows of a block
 constexpr int NV = 64;               // value columns
 constexpr int kBox = C * 128;        // bytes of 64 columns of a tile
 constexpr int kKeyTile = 2 * kBox;   // of queries, keys (dk = 64: the second half is not used)
-constexpr int kAhead = 4;            // blocks that come to L2 before
+constexpr int kAhead = 2;            // blocks that come to L2 before
 constexpr int kThreads = 20 * 32;    // weights, mask, state, output; TMA, MMA, decays, U
 constexpr float kSteep = 60.f;
 constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
-constexpr int kTiles = 4 * kKeyTile + 2 * kBox + kWTile + kBox;  // Q, K, V twice; W, S
+constexpr int kOut = 32 * 64;        // a warp's output on its way: 32 columns
+constexpr int kTiles = 4 * kKeyTile + 2 * kBox + kWTile + kBox + 4 * kOut;  // Q, K, V twice; W, S
 
 // Columns of tensor memory.
 constexpr uint32_t kScores = 0, kO1 = 256, kO2 = 320, kU = 384;  // (two blocks' scores; U: two terms)
 
 struct Bars {
-    unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_read[2], v_empty[2];
+    unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     unsigned long long dec_full[2], dec_empty[2], s_full[2], p_ready[2];
     unsigned long long w_ready, w_free, u_full, u_free, st_ready, st_free, o_full, o_free, drain;
 };
@@ -62,8 +63,7 @@ struct Shared {
         float keep;                         // e^{G_(C-1)}
         int steep;                          // a bit a 32
     } dec[2];
-    unsigned short order[kSorted];          // requests, longest first
-    int length[kSorted];
+    int request;
     uint32_t tmem;
     int dead;  // a wait gave up: every role leaves
 };
@@ -85,10 +85,9 @@ struct Unit {
     int n;         // blocks of rows
 };
 __device__ __forceinline__ bool find_unit(const Launch &L, const Shared &s, bool commit, Unit &x) {
-    const int slice = blockIdx.x % L.slices, rh = blockIdx.x / L.slices;
-    x.r = rh / L.a.g.heads;
-    x.h = rh - x.r * L.a.g.heads;
-    if (L.sorted) x.r = s.order[x.r];
+    const int slice = blockIdx.x % L.slices;
+    x.r = s.request;
+    x.h = blockIdx.x / L.slices % L.a.g.heads;
     x.c0 = slice * NV;
     if (!linear_unit(L.a, x.r, x.h, commit, x.u)) return false;
     x.n = (x.u.T + C - 1) / C;
@@ -177,9 +176,9 @@ __device__ __forceinline__ bool await(uint32_t b, uint32_t parity, int *dead) {
 
 // Shared-memory tiles.
 struct Tiles {
-    uint32_t k, v, w, s, q;
+    uint32_t k, v, w, s, q, o;
     __device__ __forceinline__ explicit Tiles(uint32_t base)
-        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + kWTile), q(s + kBox) {}
+        : k(base), v(base + 2 * kKeyTile), w(v + 2 * kBox), s(w + kWTile), q(s + kBox), o(q + 2 * kKeyTile) {}
 };
 
 // ---------------------------------------------------------------- the TMA warp (one thread)
@@ -259,14 +258,15 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         commit(lead, bar(s.b.q_empty[slot]));
         // O1 = P V
         if (!await(bar(s.b.p_ready[slot]), half, &s.dead)) return;
-        // (its values have been read: the output takes their place; past the end they are 0)
-        if (!await(bar(s.b.v_read[slot]), half, &s.dead)) return;
+        // (values past the end are 0 by now)
+        if (c + 1 == n && !await(bar(s.b.w_ready), c & 1, &s.dead)) return;
         fence_after();
         const uint32_t v = v_lo + slot * (kBox >> 4);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
             mma_ts(lead, tm + kO1, tm + kScores + slot * C + kk * 8, v + ((kk * 2048) >> 4), idesc(NV, true), kk > 0);
         commit(lead, bar(s.b.o_full));
+        commit(lead, bar(s.b.v_empty[slot]));
     }
 }
 
@@ -423,8 +423,7 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
         uint32_t v8[8][4];
 #pragma unroll
         for (int e = 0; e < 8; ++e) lds128(chunk(vt, j, e), v8[e]);
-        if (OUT && n < C) fence_async();
-        arrive_warp(bar(OUT ? s.b.v_read[slot] : s.b.v_empty[slot]));
+        arrive_warp(bar(s.b.v_empty[slot]));
         if (!await(bar(s.b.w_free), (c & 1) ^ 1, &s.dead)) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -595,16 +594,12 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
 __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm, int i) {
     const gdn_linear &g = L.a.g;
     const int b = i >> 5;
-    const uint32_t lanes = (uint32_t)b << 21;
+    const uint32_t lanes = (uint32_t)b << 21, out = t.o + b * kOut;
     Unit x;
     if (!find_unit(L, s, false, x)) return;
     for (int c = 0; c < x.n; ++c) {
         const uint32_t slot = c & 1, half = (c >> 1) & 1;
         const int n = min(C, x.u.T - c * C);
-        if (c > 0) {  // the last block's output has left
-            if ((i & 31) == 0) tma_stores_read();
-            arrive_warp(bar(s.b.v_empty[slot ^ 1]));
-        }
         if (!await(bar(s.b.dec_full[slot]), half, &s.dead)) return;
         const float f = s.dec[slot].o2[i], f1 = s.dec[slot].o1[i];
         arrive_warp(bar(s.b.dec_empty[slot]));
@@ -629,19 +624,19 @@ __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Ti
                                       mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale2));
                 y[e / 2] = pack_bf16(p.x, p.y);
             }
-            if (n == C) {  // over the values: 32 rows a warp leave by TMA
+            if (n == C) {  // 32 rows and columns a warp leave by TMA
+                const int lane = i & 31;
+                if (lane == 0) tma_stores_read();  // the last ones have
+                __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sts128(chunk(t.v + slot * kBox, i, h / 8 + e), y + 4 * e);
+                for (int e = 0; e < 4; ++e) sts128(out + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4), y + 4 * e);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) tma_store(&L.o, x.h * g.dv + x.c0 + h, x.u.row0 + c * C + i, out);
             } else if (i < n) {  // whole sectors: 32 bytes of a row at a time
                 stg32(o + h, L.o32, y);
                 stg32(o + h + 16, L.o32, y + 8);
             }
-        }
-        if (n == C) {
-            fence_async();
-            __syncwarp();
-            if ((i & 31) == 0)
-                tma_store(&L.o, x.h * g.dv + x.c0, x.u.row0 + c * C + i, t.v + slot * kBox + b * 32 * 128);
         }
     }
 }
@@ -663,8 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             mbar_init(bar(s.b.k_full[i]), 1);
             mbar_init(bar(s.b.k_empty[i]), OUT ? 2 : 1);
             mbar_init(bar(s.b.v_full[i]), 1);
-            mbar_init(bar(s.b.v_read[i]), 4);
-            mbar_init(bar(s.b.v_empty[i]), 4);
+            mbar_init(bar(s.b.v_empty[i]), OUT ? 5 : 4);
             mbar_init(bar(s.b.dec_full[i]), 1);
             mbar_init(bar(s.b.dec_empty[i]), OUT ? 16 : 8);
             mbar_init(bar(s.b.s_full[i]), 1);
@@ -690,16 +684,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     }
     fence_before();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (L.sorted) {
-        const gdn_linear &g = L.a.g;
-        for (int i = tid; i < g.batch; i += kThreads) s.length[i] = g.cu_seqlens[i + 1] - g.cu_seqlens[i];
+    const gdn_linear &g = L.a.g;
+    const int rank = blockIdx.x / L.slices / g.heads;
+    if (L.sorted) {  // (lengths where tiles will be)
+        int *length = reinterpret_cast<int *>(raw);
+        for (int i = tid; i < g.batch; i += kThreads) length[i] = g.cu_seqlens[i + 1] - g.cu_seqlens[i];
         __syncthreads();
         for (int i = tid; i < g.batch; i += kThreads) {
             int before = 0;
-            for (int k = 0; k < g.batch; ++k)
-                before += s.length[k] > s.length[i] || (s.length[k] == s.length[i] && k < i);
-            s.order[before] = (unsigned short)i;
+            for (int k = 0; k < g.batch; ++k) before += length[k] > length[i] || (length[k] == length[i] && k < i);
+            if (before == rank) s.request = i;
         }
+        fence_async();
+    } else if (tid == 0) {
+        s.request = rank;
     }
     __syncthreads();  // the barriers and the tensor memory's address
     fence_after();
@@ -753,15 +751,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 
 // ---------------------------------------------------------------- host side
 
-// Rows of `cols` elements, `stride` apart; boxes of 64 columns.  Rows past the end read as zeros.
+// Rows of `cols` elements, `stride` apart; boxes of 64 columns (or 32).  Rows past the end read as zeros.
 bool encode_rows(CUtensorMap *map, const void *base, long long cols, long long rows, long long stride,
-                 unsigned box_rows = C) {
+                 unsigned box_rows = C, unsigned box_cols = 64) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t elem[2] = {1, 1};
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-                     elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -779,7 +778,7 @@ cudaError_t launch_tc(const LinearArgs &a, cudaStream_t stream) {
     if (!encoder() || (MODE != kCommit && !encode_rows(&L.q, g.q, krow, g.n_tok, g.q_stride)) ||
         !encode_rows(&L.k, g.k, krow, g.n_tok, g.k_stride) ||
         !encode_rows(&L.v, g.v, vrow, g.n_tok, g.v_stride) ||
-        (MODE != kCommit && !encode_rows(&L.o, a.o, vrow, g.n_tok, vrow, 32)))
+        (MODE != kCommit && !encode_rows(&L.o, a.o, vrow, g.n_tok, vrow, 32, 32)))
         return cudaErrorInvalidValue;
     constexpr int smem = kTiles + (int)sizeof(Shared);
     const cudaError_t e = allow_smem<linear_tc_kernel<MODE>>(smem);
