@@ -258,6 +258,7 @@ __device__ __forceinline__ void mma_role(const Launch &L, Shared &s, const Tiles
         commit(lead, bar(s.b.q_empty[slot]));
         // O1 = P V
         if (!await(bar(s.b.p_ready[slot]), half, &s.dead)) return;
+        if (!await(bar(s.b.v_full[slot]), half, &s.dead)) return;
         // (values past the end are 0 by now)
         if (c + 1 == n && !await(bar(s.b.w_ready), c & 1, &s.dead)) return;
         fence_after();
