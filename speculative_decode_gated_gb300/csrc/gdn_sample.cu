@@ -10,7 +10,8 @@
 // Bound by the bytes of one row of p, and one of q where a draft did not stay, a request.
 // A cluster of CS blocks takes a request, each warp of it a stretch of the row in kSubs parts:
 // first the sums of all parts, then, by these, the one warp whose part holds the token reads
-// that part again (from L2) for the place.
+// that part again (from L2) for the place.  64 requests of 128000 ids take 18 us (48% of the copy's
+// rate: the drafts' own loads, the sums' exchange and the second look are latencies), one of 32000 5.4 us.
 //
 // A float x in [0, 1] in units, without a conversion to 64 bits (whose instruction took most
 // of the time: 56 us for 64 requests and 128000 ids, 34 us with shifts of the significand):
