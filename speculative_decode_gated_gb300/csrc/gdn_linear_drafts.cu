@@ -10,7 +10,7 @@
 // draft, so few rows cost as much as 16.  The state enters as two bf16 terms, off by 2^-17 of itself,
 // and so do the weights d(i, j) (q_i . k_j), which are operands of the values' product just where their
 // own product left them; q, k and v are bf16 already, and sums are float32.  16 rows of 64 requests and
-// 32 heads of 128 take 34 us, 70% of the copy's rate (78 on CUDA cores): the warps' own work on a unit, 40%
+// 32 heads of 128 take 34 us, 69% of the copy's rate (78 on CUDA cores): the warps' own work on a unit, 40%
 // of the issue slots, is what the next unit's copies do not hide.
 #include <cstdint>
 
@@ -91,6 +91,42 @@ __device__ __forceinline__ void ldmatrix2_trans(uint32_t *x, uint32_t at) {
 }
 // 16 bytes c of row r of a tile whose rows have 128.
 __device__ __forceinline__ uint32_t chunk(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// Two bf16 values: whether one is not finite; the same with 0 for such.
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t finite_part(uint32_t x) {
+    return ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+}
+// Adds the values that are not finite in rows j0 to j0 + 15 of a tile (those below T), columns 8 warp on, to the
+// warp's 16 rows of outputs from each one's own row on, by the weights' two terms.  (Rare, but not out of
+// line: the weights would then go through memory in every product, 38 us where it is 34.2 so.)
+__device__ __forceinline__ void add_not_finite(float *out, const uint32_t *W, const uint32_t *R, uint32_t vt, int j0,
+                                               int T, int warp, int lane) {
+    const int gr = lane >> 2, c = lane & 3;
+#pragma unroll 1
+    for (int j = 0; j < 16 && j0 + j < T; ++j) {
+        const int from = 4 * gr + (j >> 1 & 3), n = j >> 3;  // the lane that has this row's weights
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // of output rows gr and gr + 8
+            const uint32_t hi = __shfl_sync(0xffffffffu, n ? W[2 + i] : W[i], from);
+            const uint32_t lo = __shfl_sync(0xffffffffu, n ? R[2 + i] : R[i], from);
+            w[i] = j & 1 ? high(hi) + high(lo) : low(hi) + low(lo);
+        }
+        uint32_t v;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(chunk(vt, j0 + j, warp) + 4 * c) : "memory");
+        const float x = low(v), y = high(v);
+        const bool bad_x = (v & 0x7F80u) == 0x7F80u, bad_y = (v & 0x7F800000u) == 0x7F800000u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (gr + 8 * i < j) continue;
+            if (bad_x) out[2 * i] = fmaf(w[i], x, out[2 * i]);
+            if (bad_y) out[2 * i + 1] = fmaf(w[i], y, out[2 * i + 1]);
+        }
+    }
+}
 
 // The units of a block in order, `step` at a time; a unit's words are loaded a round before they are
 // looked at.  One lane's answer is the warp's.
@@ -356,8 +392,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2) drafts_kernel(const __gr
                     v[0] &= (j < T ? 0xFFFFu : 0u) | (j + 1 < T ? 0xFFFF0000u : 0u);
                     v[1] &= (j + 8 < T ? 0xFFFFu : 0u) | (j + 9 < T ? 0xFFFF0000u : 0u);
                 }
+                // A value that is not finite would reach rows before its own by their weight of 0, so it
+                // leaves the product, and rows from its own on add it for themselves.
+                const bool odd = l == m && __any_sync(0xffffffffu, not_finite(v[0]) || not_finite(v[1]));
+                if (odd) {
+                    v[0] = finite_part(v[0]);
+                    v[1] = finite_part(v[1]);
+                }
                 mma(out, R, v[0], v[1]);
                 mma(out, W, v[0], v[1]);
+                if (odd) add_not_finite(out, W, R, vt, 16 * l, T, warp, lane);
             }
             const long long step = (long long)g.heads * g.dv;
             if (i0 < T) *reinterpret_cast<uint32_t *>(o + i0 * step) = pack(out[0] * g.scale, out[1] * g.scale);
