@@ -22,7 +22,13 @@
 // the first factor is left to o, so a score needs one product, with a column's factor that all of
 // the 32 rows share.  For an earlier 32's rows neither exponent is positive; for its own the second
 // one is, up to e^60: where the logarithms of 32 rows add up to more, their decays are products
-// of single ones, taken one by one.  All sums run from their own first row, so nothing cancels.
+// of single ones, taken one by one.  All sums run from their own first row; what the two exponents have in
+// common cancels in the product but for its rounding, 2^-24 of up to 60: far below bf16 weights'.
+// Factors of several 32s are products.  With positive logarithms these may leave float32 where the decay
+// itself does not.  A block that has some is as any other while all sums within its 32s are at most 4 (what
+// products of up to four then lose to underflow is below e^(16 - 87)) or within 20 of 0; else it takes each
+// decay as the exponential of its own sum, out of line (709 us where it is 132; with the exponentials
+// of the decays' warp alone taken so in every block it was 181).
 //
 // Bound by latencies from block to block, not by memory or products: 8001 rows of 32 heads take 132 us
 // (64 blocks, an SM each; 39 us would be the bytes, and the tensor pipe is busy half the time there), six
@@ -45,7 +51,8 @@ constexpr int kBox = C * 128;        // bytes of 64 columns of a tile
 constexpr int kKeyTile = 2 * kBox;   // of queries, keys (dk = 64: the second half is not used)
 constexpr int kAhead = 2;            // blocks that come to L2 before
 constexpr int kThreads = 20 * 32;    // weights, mask, state, output; TMA, MMA, decays, U
-constexpr float kSteep = 60.f;
+constexpr float kSteep = 60.f, kRise = 4.f, kGentle = 20.f;
+constexpr int kRising = 16;          // decays by their sums
 constexpr int kSorted = 512;         // requests that are taken longest first
 constexpr int kWTile = 2 * kBox;     // of weighted values, two terms
 constexpr int kOut = 32 * 64;        // a warp's output on its way: 32 columns
@@ -63,12 +70,12 @@ struct Bars {
 struct Shared {
     Bars b;
     struct Decays {
-        alignas(16) float column[4][C];  // of an earlier or the same 32: e^{B_b - G_j}
-        alignas(16) float log[C], row[C];   // (where steep) g_i, e^{G_i - B_b}
+        alignas(16) float column[4][C];  // of an earlier or the same 32: e^{B_b - G_j} (rising: B_b - G_j)
+        alignas(16) float log[C], row[C];   // (where steep) g_i, e^{G_i - B_b} (rising: G_i - B_b)
         alignas(16) float o1[C], o2[C];     // factors of O1 and O2: scale e^{G_i - B_b} (or scale), scale e^{G_i}
         alignas(16) float weight[C];        // e^{G_(C-1) - G_j}; 0 for rows past the end
         float keep;                         // e^{G_(C-1)}
-        int steep;                          // a bit a 32
+        int steep;                          // a bit a 32, and kRising
     } dec[2];
     int request;
     uint32_t tmem;
@@ -304,6 +311,52 @@ __device__ __forceinline__ void update_role(const Launch &L, Shared &s, const Ti
 
 // ---------------------------------------------------------------- the decays' warp
 
+// Whether a block with positive logarithms needs its decays by their sums.
+__device__ __forceinline__ bool rises_far(float4 x, float4 y) {
+    const float high = fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
+    const float low = fminf(fminf(fminf(x.x, x.y), fminf(x.z, x.w)), fminf(fminf(y.x, y.y), fminf(y.z, y.w)));
+    const bool number = !isnan(x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w);
+    return !__all_sync(0xffffffffu, number && high <= kRise) &&
+           !__all_sync(0xffffffffu, number && high <= kGentle && low >= -kGentle);
+}
+
+// A block's decays where its logarithms rise: sums, or exponentials of whole sums.  This lane's rows as below.
+template <bool OUT>
+__device__ __noinline__ bool rising_decays(Shared::Decays &d, float scale, int lane, int n, float4 gl, float4 upto,
+                                           float4 after, float total) {
+    if (!rises_far(upto, after)) return false;
+    const int b = lane >> 3, i = 4 * lane;
+    float before = 0.f, behind = 0.f, all = 0.f;
+    auto put = [&](float *to, float w, float x, float y, float z) {
+        *reinterpret_cast<float4 *>(to + i) = make_float4(w, x, y, z);
+    };
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float sum = __shfl_sync(0xffffffffu, total, 8 * m);
+        all += sum;
+        if (m < b) before += sum;
+        if (m > b) {
+            if (OUT)
+                put(d.column[m], after.x + behind, after.y + behind, after.z + behind, after.w + behind);
+            behind += sum;
+        }
+    }
+    put(d.weight, i < n ? expf(after.x + behind) : 0.f, i + 1 < n ? expf(after.y + behind) : 0.f,
+        i + 2 < n ? expf(after.z + behind) : 0.f, i + 3 < n ? expf(after.w + behind) : 0.f);
+    if (OUT) {
+        put(d.log, gl.x, gl.y, gl.z, gl.w);
+        put(d.row, upto.x, upto.y, upto.z, upto.w);
+        put(d.o1, scale, scale, scale, scale);
+        put(d.o2, scale * expf(before + upto.x), scale * expf(before + upto.y), scale * expf(before + upto.z),
+            scale * expf(before + upto.w));
+    }
+    if (lane == 0) {
+        d.keep = expf(all);
+        d.steep = kRising;
+    }
+    return true;
+}
+
 template <bool OUT>
 __device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane) {
     const gdn_linear &g = L.a.g;
@@ -344,6 +397,8 @@ __device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane)
         if (l == 0) below = 0.f;
         if (l == 7) above = 0.f;
         bool mild = true;
+        const bool falls =  // (false for NaN)
+            gl[0] <= 0.f && gl[1] <= 0.f && gl[2] <= 0.f && gl[3] <= 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             upto[k] += below;
@@ -356,13 +411,20 @@ __device__ __forceinline__ void decay_role(const Launch &L, Shared &s, int lane)
         float t[4];  // of the four 32s
 #pragma unroll
         for (int m = 0; m < 4; ++m) t[m] = __shfl_sync(0xffffffffu, whole, 8 * m);
-        if (!await(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
-        Shared::Decays &d = s.dec[slot];
         float row[4], col[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             row[k] = expf(upto[k]);
             col[k] = expf(after[k]);
+        }
+        const bool falls_all = __all_sync(0xffffffffu, falls);
+        if (!await(bar(s.b.dec_empty[slot]), half ^ 1, &s.dead)) return;
+        Shared::Decays &d = s.dec[slot];
+        if (!falls_all && rising_decays<OUT>(d, g.scale, lane, n, make_float4(gl[0], gl[1], gl[2], gl[3]),
+                                             make_float4(upto[0], upto[1], upto[2], upto[3]),
+                                             make_float4(after[0], after[1], after[2], after[3]), total)) {
+            arrive_warp(bar(s.b.dec_full[slot]));
+            continue;
         }
         auto put = [&](float *to, float w, float x, float y, float z) {
             *reinterpret_cast<float4 *>(to + 4 * lane) = make_float4(w, x, y, z);
@@ -455,6 +517,30 @@ __device__ __forceinline__ void weight_role(const Launch &L, Shared &s, const Ti
 
 // ---------------------------------------------------------------- the mask's warpgroup
 
+// A warp's rows in a block whose logarithms rise: each decay the exponential of its sum.
+__device__ __noinline__ void mask_rising(const Shared::Decays &d, uint32_t ts, int lane, int b) {
+    const float f = d.row[32 * b + lane];
+#pragma unroll 1
+    for (int m = 0; m <= b; ++m) {
+        uint32_t y[32];
+        tmem_ld32(ts + 32 * m, y);
+        wait_ld();
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 31; e >= 0; --e) {
+            if (m < b)
+                sum = d.column[b][32 * m + e] + f;
+            else if (e < lane)
+                sum += d.log[32 * b + e + 1];
+            y[e] = m < b || e <= lane ? __float_as_uint(__uint_as_float(y[e]) * expf(sum)) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+            y[e / 2] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+        tmem_st16(ts + 16 * m, y);  // over scores that have been read
+    }
+}
+
 // A warp's rows whose 32 is steep: the factors of earlier 32s' columns times the row's, and its own
 // decays one by one.  (A function of its own, so that its registers are not the others'.)
 __device__ __noinline__ void mask_steep(const Shared::Decays &d, uint32_t ts, int lane, int b) {
@@ -494,7 +580,9 @@ __device__ __forceinline__ void mask_role(const Launch &L, Shared &s, uint32_t t
         if (!await(bar(s.b.s_full[slot]), half, &s.dead)) return;
         const uint32_t ts = tm + kScores + slot * C + ((uint32_t)b << 21);  // this warp's lanes
         fence_after();
-        if (d.steep >> b & 1) {
+        if (d.steep & kRising) {
+            mask_rising(d, ts, lane, b);
+        } else if (d.steep >> b & 1) {
             mask_steep(d, ts, lane, b);
         } else {
 #pragma unroll 1
