@@ -60,7 +60,7 @@ struct Tiles {
     float g[T];
     Work work[BUFFERS];
     int dead;  // a wait gave up
-    unsigned long long full[BUFFERS], free[BUFFERS];
+    unsigned long long full[BUFFERS], decayed[BUFFERS], free[BUFFERS];  // copies there; decays there; both done with
 };
 
 struct Launch {
@@ -203,9 +203,11 @@ __device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int
     const gdn_linear &g = L.a.g;
     Units<DK> units(L);
     Ring<Tiles<DK, NG>::BUFFERS> ring;
+    uint32_t issued = 0;
     for (;; ring.next()) {
         const Work w = units.next(lane == 0);
-        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) return;
+        if (!wait(bar(s.free[ring.slot]), ring.parity ^ 1, &s.dead)) break;
+        ++issued;
         const uint32_t full = bar(s.full[ring.slot]);
         auto &to = s.unit[ring.slot];
         if (lane == 0) {
@@ -224,8 +226,10 @@ __device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int
             }
         }
         __syncwarp();
-        if (w.T < 0) return;
+        if (w.T < 0) break;
     }
+    if (lane == 0)
+        wait_copies<Tiles<DK, NG>::BUFFERS>(issued, [&](uint32_t slot, uint32_t p) { wait_parity(bar(s.full[slot]), p); });
 }
 
 // The warp that works out their decays.
@@ -291,7 +295,7 @@ __device__ __forceinline__ void decay_role(const Launch &L, Tiles<DK, NG> &s, in
                 }
             }
         }
-        arrive_warp(bar(s.full[ring.slot]));
+        arrive_warp(bar(s.decayed[ring.slot]));
         if (rows < 0) return;
     }
 }
@@ -306,7 +310,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2) drafts_kernel(const __gr
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
     if (tid == 0) {
         for (int i = 0; i < NB; ++i) {
-            mbar_init(bar(s.full[i]), 2);  // the copies, and the decays
+            mbar_init(bar(s.full[i]), 1);
+            mbar_init(bar(s.decayed[i]), 1);
             mbar_init(bar(s.free[i]), kWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -325,7 +330,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2) drafts_kernel(const __gr
     const int l7 = lane & 7, l8 = (lane >> 3) & 1, l16 = lane >> 4;
     Ring<NB> ring;
     for (;;) {
-        if (!wait(bar(s.full[ring.slot]), ring.parity, &s.dead)) {  // the copies never came
+        if (!wait(bar(s.full[ring.slot]), ring.parity, &s.dead) ||
+            !wait(bar(s.decayed[ring.slot]), ring.parity, &s.dead)) {  // they never came
             if (lane == 0 && g.dev_err) atomicOr(g.dev_err, GDN_DEVERR_TIMEOUT);
             return;
         }

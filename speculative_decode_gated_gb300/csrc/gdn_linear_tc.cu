@@ -816,8 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if ((tid & 31) == 0) {
             uint32_t issued = 0;
             load_role<OUT>(L, s, t, issued);
-            // Every copy has landed before the block ends (its roles waited for them unless one gave up).
-            for (uint32_t p = issued > 2 ? issued - 2 : 0; s.dead && p <= issued; ++p) {
+            // Every copy has landed before the block ends (its roles waited for them unless one gave up; then those of
+            // a block of rows that was asked for in part may be on their way too, and its other waits run out).
+            for (uint32_t p = issued > 2 ? issued - 2 : 0; p < issued + (s.dead ? 1 : 0); ++p) {
                 wait_parity(bar(s.b.v_full[p & 1]), (p >> 1) & 1);
                 wait_parity(bar(s.b.k_full[p & 1]), (p >> 1) & 1);
                 if (OUT) wait_parity(bar(s.b.q_full[p & 1]), (p >> 1) & 1);

@@ -179,6 +179,14 @@ struct Ring {
     }
 };
 
+// The phases that copies into a ring of NS slots may still complete after `issued` uses of it: wait(slot, parity)
+// for the last NS of them.  The thread that asked for the copies calls it before it leaves, whatever ended its
+// work, so that none lands in shared memory that is another block's by then.
+template <int NS, typename Wait>
+__host__ __device__ __forceinline__ void wait_copies(uint32_t issued, Wait wait) {
+    for (uint32_t p = issued > NS ? issued - NS : 0; p < issued; ++p) wait(p % NS, (p / NS) & 1);
+}
+
 // The driver's encoder of tensor maps; NULL if it has none.
 inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
