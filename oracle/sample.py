@@ -22,6 +22,13 @@ def units(x: float) -> int:
     return UNIT if x > 1.0 else int(Fraction(x) * UNIT)
 
 
+def below(u: float, q: float, p: float) -> bool:
+    """u q < p, exactly; with NaN, or 0 times infinity, it is not."""
+    if all(np.isfinite([u, q, p])):
+        return Fraction(u) * Fraction(q) < Fraction(p)
+    return u * q < p
+
+
 def draw(weights, u: float) -> int:
     """The lowest i with w_0 + ... + w_i > floor(U W / 2^31), U = floor(2^31 u); -1 without weight."""
     total = sum(weights)
@@ -55,7 +62,7 @@ def accept_sample(draft_ids, target, draft, u_accept, u_sample, cu):
                 break
             p, u = float(target[c + a - 1][x]), float(u_accept[c + a])
             q = 1.0 if draft is None else float(draft[c + a - 1][x])
-            if not all(np.isfinite([p, q, u])) or not Fraction(u) * Fraction(q) < Fraction(p):
+            if not below(u, q, p):
                 break
             a += 1
         row = c + a - 1
