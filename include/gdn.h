@@ -440,13 +440,20 @@ GDN_API int64_t gdn_paged_attn_workspace(const gdn_attn *p);
  * Requests, rows and slots are those of the GDN calls, with up to GDN_ATTN_MAX_T rows a request:
  * single tokens, drafts and prompts.
  *
- * Products, sums and states are 32-bit.  With bfloat16 rows, dk 64 or 128, dv a multiple of
- * 64 and max_T of 48 or more, states and weights are rounded for the tensor cores: to
- * bfloat16 for o, which is bfloat16 itself, and to 16 bits' significands for what is
- * added to a state, so a row's o and a state may differ by such roundings from those of calls
- * with fewer rows.  There a value, key or query that is not finite makes outputs of its request
- * and head not finite from the row's block of 128 rows on, the block's earlier rows among them;
- * in shorter calls from its own row on. */
+ * Products, sums and states are 32-bit, but for calls with bfloat16 rows, dk 64 or 128 and dv a
+ * multiple of 64, which round states and weights for the tensor cores:
+ *   gdn_linear_verify with max_T of 2 to 47: for o to two bfloat16 terms each, off by 2^-17 at most;
+ *   all calls with max_T of 48 or more: for o to bfloat16 (2^-8), which o is itself, and what is added to
+ *   a state to two bfloat16 terms;
+ * so a row's o and a state may differ by such roundings from those of calls with other max_T.  Calls
+ * with max_T of 48 or more of that kind let a value, key or query that is not finite make outputs of its
+ * request and head not finite from the row's block of 128 rows on, the block's earlier rows among them;
+ * all others from its own row on.
+ *
+ * Over blocks of up to 128 rows, the decay from one row (or the state before) to a later one is a float32, the
+ * exponential of its logarithms' sum: where that leaves float32 it is 0 or infinite, even if what it
+ * multiplies would bring it back.  Positive logarithms are allowed.  Calls of the second kind may take five
+ * times as long where sums of theirs over up to 32 rows exceed 4 and leave -20 to 20. */
 typedef struct gdn_linear {
     int32_t batch;               /* B >= 0 requests (B = 0: calls return GDN_OK, no launch) */
     int32_t heads;               /* H >= 1: states, and heads of v and o */

@@ -38,7 +38,11 @@ cudaError_t launch_pages(const gdn_pages &g, cudaStream_t stream);
 // Linear attention (arguments already validated on the host); mode: kVerify, kCommit, or kFused
 // for a step.
 cudaError_t launch_linear(const LinearArgs &a, int mode, cudaStream_t stream);
-constexpr int kLinearTcRows = 48;  // rows a request from which the tensor-core kernel runs
+// Rows a request from which the prompts' kernel runs: one number, although the three calls cross at other
+// counts (left as it is).  64 requests of 32 heads of 128 x 128, all rows kept, us in the prompts' kernel / in the
+// other: verify 182 / 125 at 47 rows, 186 / 330 at 64; step 205 / 180 at 24, 203 / 217 at 32; commit 193 / 125 at
+// 47, 193 / 158 at 64.
+constexpr int kLinearTcRows = 48;
 bool linear_tc_runs(const gdn_linear &g);
 cudaError_t launch_linear_tc(const LinearArgs &a, int mode, cudaStream_t stream);
 bool linear_drafts_runs(const gdn_linear &g);  // a verify

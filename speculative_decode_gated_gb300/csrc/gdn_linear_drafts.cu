@@ -229,7 +229,8 @@ __device__ __forceinline__ void load_role(const Launch &L, Tiles<DK, NG> &s, int
         if (w.T < 0) break;
     }
     if (lane == 0)
-        wait_copies<Tiles<DK, NG>::BUFFERS>(issued, [&](uint32_t slot, uint32_t p) { wait_parity(bar(s.full[slot]), p); });
+        wait_copies<Tiles<DK, NG>::BUFFERS>(
+            issued, [&](uint32_t slot, uint32_t parity) { wait_parity(bar(s.full[slot]), parity); });
 }
 
 // The warp that works out their decays.
@@ -464,7 +465,8 @@ cudaError_t launch_one(const LinearArgs &a, cudaStream_t stream) {
 }  // namespace
 
 bool linear_drafts_runs(const gdn_linear &g) {
-    return g.dtype == GDN_BF16 && (g.dk == 64 || g.dk == 128) && g.dv % CV == 0 && g.max_T > 1 && g.max_T <= 48 &&
+    return g.dtype == GDN_BF16 && (g.dk == 64 || g.dk == 128) && g.dv % CV == 0 && g.max_T > 1 &&
+           g.max_T < kLinearTcRows &&
            g.pool_slots * g.heads * g.dk <= 0x7fffffffLL;  // the pool's rows are numbered in 32 bits
 }
 

@@ -12,7 +12,8 @@
 //   MMA warps    U; the other three products
 //   decays       (a warp, four rows a lane) see below
 //   weights      (warpgroup, a thread a row) W in two bf16 terms: each product v_j d enters its state
-//                to 2^-17 of itself
+//                to 2^-17 of itself (a state is off by 2.3e-6; a third term, for float32's 1.2e-7, took 180 us
+//                for the 133 below)
 //   mask         (a thread a row) scores times decays to P, in tensor memory over the scores
 //   state        (a thread a row of dk) S in registers, its bf16 copy in shared memory for O2
 //   output       (a thread a row) o, which leaves by TMA
@@ -30,9 +31,9 @@
 // decay as the exponential of its own sum, out of line (709 us where it is 132; with the exponentials
 // of the decays' warp alone taken so in every block it was 181).
 //
-// Bound by latencies from block to block, not by memory or products: 8001 rows of 32 heads take 132 us
+// Bound by latencies from block to block, not by memory or products: 8001 rows of 32 heads take 133 us
 // (64 blocks, an SM each; 39 us would be the bytes, and the tensor pipe is busy half the time there), six
-// prompts of up to 4000 rows 114 us (47% of the copy's rate).  What the load pipe carries matters most,
+// prompts of up to 4000 rows 115 us (46% of the copy's rate).  What the load pipe carries matters most,
 // since barriers, products' issue and tensor memory go through it too: rows come and go by TMA
 // only (queries loaded by the threads, 32 rows an instruction, 184 and 152 us against 146 and 130).  64 value
 // columns a block: with 128, 8001 rows would have 32 blocks.
@@ -685,7 +686,7 @@ __device__ __forceinline__ void state_role(const Launch &L, Shared &s, const Til
     }
 }
 
-// ---------------------------------------------------------------- the queries' and output's warpgroup
+// ---------------------------------------------------------------- the output's warpgroup
 
 __device__ __forceinline__ void output_role(const Launch &L, Shared &s, const Tiles &t, uint32_t tm, int i) {
     const gdn_linear &g = L.a.g;
@@ -816,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if ((tid & 31) == 0) {
             uint32_t issued = 0;
             load_role<OUT>(L, s, t, issued);
-            // Every copy has landed before the block ends (its roles waited for them unless one gave up; then those of
-            // a block of rows that was asked for in part may be on their way too, and its other waits run out).
+            // Every copy has landed before the block ends (its roles waited for them unless one gave up; then those
+            // of a block of rows that was asked for in part may be on their way too, and its other waits run out).
             for (uint32_t p = issued > 2 ? issued - 2 : 0; p < issued + (s.dead ? 1 : 0); ++p) {
                 wait_parity(bar(s.b.v_full[p & 1]), (p >> 1) & 1);
                 wait_parity(bar(s.b.k_full[p & 1]), (p >> 1) & 1);

@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kInline = 8192;   // rows of slots and positions that the planning launch writes itself
+// Rows of slots and positions that the planning launch writes itself.  8192 rows of 64 requests take 10 us so
+// and 16 in two launches; 16384 rows 12 and 14.
+constexpr int kInline = 8192;
 
 // What one request wants.
 struct Want {
@@ -271,7 +273,8 @@ cudaError_t launch_pages(const gdn_pages &g, cudaStream_t stream) {
     while (1 << shift < g.page_size) ++shift;
     const bool here = wanted && rows <= kInline && g.batch <= kThreads;
     cudaLaunchConfig_t cfg = {};
-    // One block suffices where a thread has a few numbers at most to move.
+    // One block suffices where a thread has a few numbers at most to move: up to 1024 rows it takes what
+    // eight take, 4096 rows of 64 requests 14 us for 10, 8192 rows 18 for 10.
     const int cs = rows <= 4096 && g.batch <= 512 ? 1 : kCluster;
     cfg.gridDim = dim3(cs);
     cfg.blockDim = dim3(kThreads);
