@@ -10,12 +10,13 @@ import pytest
 import torch
 
 from speculative_decode_gated_gb300 import binding
-from test_linear_gpu import TILES, Case
+from test_linear_drafts_gpu import Drafts
+from test_linear_gpu import TILES
 
 pytestmark = pytest.mark.gpu
 
 
-class Signs(Case):
+class Signs(Drafts):
     """Two requests and heads with the logarithms given, [rows].  only: rows whose values are not 0 (None:
     all)."""
 
@@ -64,6 +65,8 @@ PROFILES = {
     "long_with_values": np.concatenate([sums(-112, 24, 24, 24, -112, 40, 24, -40), sums(-24)[:17]]),
     # far below, with small rises
     "small_rises": np.tile([-2, -2, 0.25, -4, -2, -6, 0.25, -2], 25),
+    # a state that is forgotten in between
+    "forgets": np.where(np.arange(160) == 50, -np.inf, np.concatenate([sums(40, -8, 24, 24), sums(-16)])),
     # up and down within 32 rows, further than 60 from their start
     "steep_up_and_down": np.tile(np.concatenate([np.full(16, 4.5), np.full(16, -4.5)]), 4),
 }
@@ -105,5 +108,7 @@ def test_walks(T, dtype, seed, reach):
         at += step
     c = Signs(logs, seed=seed, dtype=dtype, dk=64, dv=64)
     o = c.output()
+    binding.gdn_linear_verify(c.lin, o)
+    c.check(o)
     binding.gdn_linear_step(c.lin, o)
     c.check(o, c.new)
